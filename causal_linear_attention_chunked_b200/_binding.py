@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_HERE, "liblt.so")
 
 LT_OK, LT_ERR_INVALID_ARG, LT_ERR_UNSUPPORTED, LT_ERR_CUDA = 0, 1, 2, 3
 LT_ERR_DEVICE_TIMEOUT, LT_ERR_DEVICE_BAD_SEQLENS, LT_ERR_SCRATCH_TOO_SMALL = 4, 5, 6
+LT_ERR_DEVICE_BAD_PAGE = 7
 LT_F32, LT_BF16, LT_F16 = 0, 1, 2
 FEATURE_MAPS = {"elu1": 0, "relu": 1, "exp": 2}
 LT_SCHED_AUTO, LT_SCHED_TWO_LAUNCH, LT_SCHED_GENERAL = 0, 1, 2
@@ -25,7 +26,10 @@ EXPORTED = ("lt_linear_attn_fwd", "lt_linear_attn_fwd_noalloc", "lt_linear_attn_
             "lt_linear_attn_fwd_state", "lt_linear_attn_decode_step", "lt_status_string",
             "lt_get_last_device_error", "lt_abi_version", "lt_selftest_wait_timeout",
             "lt_debug_set_schedule", "lt_linear_attn_state", "lt_linear_attn_state_carry",
-            "lt_linear_attn_bwd", "lt_linear_attn_fwd_ex", "lt_linear_attn_fwd_window")
+            "lt_linear_attn_bwd", "lt_linear_attn_fwd_ex", "lt_linear_attn_fwd_window",
+            "lt_qk_norm_rope", "lt_qk_norm_rope_bwd", "lt_qk_norm_rope_bwd_plan",
+            "lt_kv_cache_write", "lt_kv_cache_read", "lt_paged_attn_decode",
+            "lt_paged_attn_decode_plan")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError("liblt.so is not built (run `python -m "
@@ -71,6 +75,37 @@ lib.lt_linear_attn_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i
 lib.lt_linear_attn_bwd.restype = _i
 lib.lt_debug_set_schedule.argtypes = [_i, _i]
 lib.lt_debug_set_schedule.restype = _i
+_i64, _sz = ctypes.c_int64, ctypes.c_size_t
+lib.lt_qk_norm_rope.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _i, _i, _vp, _vp, _i64, _i,
+                                _i, _i, _i64, _i64, _f, _vp, _i, _i]
+lib.lt_qk_norm_rope.restype = _i
+lib.lt_qk_norm_rope_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i, _i, _vp,
+                                    _vp, _vp, _vp, _i64, _i, _i, _i, _i64, _i64, _i64, _i64, _f,
+                                    _vp, _sz, _vp, _i, _i]
+lib.lt_qk_norm_rope_bwd.restype = _i
+lib.lt_qk_norm_rope_bwd_plan.argtypes = [_i64, _i, _i, ctypes.POINTER(_sz)]
+lib.lt_qk_norm_rope_bwd_plan.restype = _i
+
+
+class KvCacheStruct(ctypes.Structure):
+    """lt_kv_cache_t."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp),
+                ("k_page_stride", _i64), ("k_slot_stride", _i64), ("k_head_stride", _i64),
+                ("v_page_stride", _i64), ("v_slot_stride", _i64), ("v_head_stride", _i64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("dtype", _i)]
+
+
+lib.lt_kv_cache_write.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i]
+lib.lt_kv_cache_write.restype = _i
+lib.lt_kv_cache_read.argtypes = [_vp, _vp, _i64, _i, _vp, _i, _i, _vp, _vp, _vp, _i]
+lib.lt_kv_cache_read.restype = _i
+lib.lt_paged_attn_decode.argtypes = [_vp, _vp, _vp, _i64, _i, _vp, _i, _i, _f, _i, _vp, _vp, _vp,
+                                     _sz, _vp, _i]
+lib.lt_paged_attn_decode.restype = _i
+lib.lt_paged_attn_decode_plan.argtypes = [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]
+lib.lt_paged_attn_decode_plan.restype = _i
 
 
 class LtError(RuntimeError):

@@ -151,6 +151,8 @@ const char* lt_status_string(lt_status_t s) {
     case LT_ERR_DEVICE_BAD_SEQLENS: return "LT_ERR_DEVICE_BAD_SEQLENS: inconsistent cu_seqlens";
     case LT_ERR_SCRATCH_TOO_SMALL:
       return "LT_ERR_SCRATCH_TOO_SMALL: the shape needs more than the fixed scratch array holds";
+    case LT_ERR_DEVICE_BAD_PAGE:
+      return "LT_ERR_DEVICE_BAD_PAGE: a page or slot index out of range";
   }
   return "unknown lt_status_t";
 }
@@ -335,6 +337,7 @@ lt_status_t lt_get_last_device_error(lt_stream_t stream) {
   }
   if (code == lt::kDevErrTimeout) return LT_ERR_DEVICE_TIMEOUT;
   if (code == lt::kDevErrBadSeqlens) return LT_ERR_DEVICE_BAD_SEQLENS;
+  if (code == lt::kDevErrBadPage) return LT_ERR_DEVICE_BAD_PAGE;
   return code == 0 ? LT_OK : LT_ERR_CUDA;
 }
 

@@ -28,6 +28,7 @@ enum : int {
   kDevErrNone = 0,
   kDevErrTimeout = 1,     // a bounded wait gave up (pipeline stalled)
   kDevErrBadSeqlens = 2,  // cu_seqlens not monotone / out of range
+  kDevErrBadPage = 3,     // a page or slot index outside the cache's pools
 };
 
 __device__ __forceinline__ void report_error(int* err, int code) {

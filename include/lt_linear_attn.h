@@ -27,7 +27,9 @@
  *     per-block partial states; lt_linear_attn_fwd_plan() gives its size.
  *     lt_linear_attn_fwd_state and lt_linear_attn_state with LT_BF16
  *     allocate the same way (always); lt_linear_attn_bwd allocates its
- *     workspace the same way.  No other entry point allocates.
+ *     workspace the same way.  lt_qk_norm_rope_bwd and lt_paged_attn_decode
+ *     allocate the same way unless the caller passes a workspace.  No other
+ *     entry point allocates.
  *   - Layouts are token-major and dense (row-major, no padding):
  *       dense:   q [B][N][H_q][d],  k [B][N][H_kv][d],  v [B][N][H_kv][dv],
  *                out [B][N][H_q][dv]
@@ -70,8 +72,9 @@ typedef enum {
   LT_ERR_CUDA = 3,            /* a CUDA runtime call or launch failed */
   LT_ERR_DEVICE_TIMEOUT = 4,  /* a kernel gave up on a stalled wait */
   LT_ERR_DEVICE_BAD_SEQLENS = 5, /* a kernel found cu_seqlens inconsistent */
-  LT_ERR_SCRATCH_TOO_SMALL = 6   /* lt_linear_attn_fwd_noalloc: the shape needs
+  LT_ERR_SCRATCH_TOO_SMALL = 6,  /* lt_linear_attn_fwd_noalloc: the shape needs
                                     more than LT_NOALLOC_SCRATCH_BYTES */
+  LT_ERR_DEVICE_BAD_PAGE = 7     /* a kernel found a page or slot index out of range */
 } lt_status_t;
 
 typedef enum {
@@ -375,6 +378,210 @@ LT_API lt_status_t lt_linear_attn_decode_step(const void *q, const void *k, cons
                                        int dv, float eps, lt_stream_t stream, lt_dtype_t dtype);
 
 /*
+ * lt_qk_norm_rope: what the query and key heads of an attention layer go
+ * through before any of the attention passes (linear or softmax): a
+ * root-mean-square norm of every head's d values, a gain, and the rotation by
+ * the token's position (the pages list a RoPE utility and its test,
+ * lineartile "Project Structure": utils/rope.py), in one pass.  For every
+ * token t and head h, with x the head's d values:
+ *     y = x * (mean(x^2) + eps)^(-1/2) * w
+ *     out = y, but for each pair (a, b) of the first `rot` values
+ *           (y_a cos A - y_b sin A,  y_b cos A + y_a sin A),
+ *           A = positions[t mod n_pos] * inv_freq[i],
+ * pair i being (i, i + rot/2) or, interleaved, (2i, 2i + 1).
+ *
+ * q, k       [tokens][H][d] of element type dtype, 16-byte aligned; the heads
+ *            of a token are contiguous, tokens are q_stride (k_stride)
+ *            elements apart (at least H*d; a multiple of 16 bytes), so a
+ *            slice of a fused projection's output can be passed as it is.
+ * q_weight, k_weight  [d] gains of element type w_dtype, or NULL (gain 1).
+ * positions  [n_pos] int32 device; tokens must be a multiple of n_pos (a
+ *            dense batch [B][N] shares one array of N, or passes B*N).
+ * inv_freq   [rot/2] fp32 device, angle per position.  Angles are formed and
+ *            reduced in 64 bits, so far positions lose nothing.
+ * rot        values rotated: a multiple of 8, 0 <= rot <= d.  0: the norm
+ *            alone (positions and inv_freq may be NULL).
+ * interleaved  0 or 1, the pairing.
+ * q_out, k_out  [tokens][H][d] dense, dtype, 16-byte aligned; written whole;
+ *            must not overlap any input or each other.
+ * tokens     >= 1, H_q, H_kv >= 1 (any two counts), d 64 or 128; a tensor's
+ *            extent below 2^62 bytes.
+ * eps        finite and > 0.
+ * dtype      LT_BF16, LT_F16 or LT_F32; arithmetic in fp32, one rounding at
+ *            the end.  The sum of squares is held in fp32: |x| above about
+ *            1e18 overflows it.
+ * w_dtype    LT_F32 or dtype.
+ * Returns LT_OK, LT_ERR_INVALID_ARG, LT_ERR_UNSUPPORTED or LT_ERR_CUDA.
+ */
+LT_API lt_status_t lt_qk_norm_rope(const void *q, const void *k, const void *q_weight,
+                                   const void *k_weight, const int32_t *positions, int64_t n_pos,
+                                   const float *inv_freq, int rot, int interleaved, void *q_out,
+                                   void *k_out, int64_t tokens, int H_q, int H_kv, int d,
+                                   int64_t q_stride, int64_t k_stride, float eps,
+                                   lt_stream_t stream, lt_dtype_t dtype, lt_dtype_t w_dtype);
+
+/*
+ * lt_qk_norm_rope_bwd: backward pass of lt_qk_norm_rope.  With g the upstream
+ * gradient turned back (the rotation by -A), r = (mean(x^2) + eps)^(-1/2) and
+ * u = g * w:
+ *     dx = r u - x r^3 mean(u x),     dw = sum over tokens and heads of g x r.
+ *
+ * dq_out, dk_out  [tokens][H][d] dense, dtype: the upstream gradients.
+ * q .. interleaved, tokens .. k_stride, eps, dtype, w_dtype   the forward's.
+ * dq, dk     the layouts of q and k with token strides dq_stride, dk_stride
+ *            (so that they can be slices of a fused gradient); nothing
+ *            between the heads of two tokens is written.
+ * dq_weight, dk_weight  [d] of w_dtype, each NULL (not wanted) or written
+ *            whole; a gain's gradient may be asked for with a NULL gain.
+ * Outputs must not overlap any input or each other (dq and dk may share one
+ * fused gradient tensor, in disjoint slices).
+ * workspace  NULL (the library allocates it stream-ordered and releases it
+ *            before returning), or 16-byte aligned device memory of at least
+ *            lt_qk_norm_rope_bwd_plan's bytes that no other call uses until
+ *            this one's work is done.
+ * Evaluation: the gains' gradients are summed in fp32 per thread, block and
+ * launch in a fixed order, so runs agree bit for bit.
+ * Returns as lt_qk_norm_rope.
+ */
+LT_API lt_status_t lt_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
+                                       const void *k, const void *q_weight, const void *k_weight,
+                                       const int32_t *positions, int64_t n_pos,
+                                       const float *inv_freq, int rot, int interleaved, void *dq,
+                                       void *dk, void *dq_weight, void *dk_weight, int64_t tokens,
+                                       int H_q, int H_kv, int d, int64_t q_stride,
+                                       int64_t k_stride, int64_t dq_stride, int64_t dk_stride,
+                                       float eps, void *workspace, size_t workspace_bytes,
+                                       lt_stream_t stream, lt_dtype_t dtype, lt_dtype_t w_dtype);
+
+/* Workspace bytes of lt_qk_norm_rope_bwd on a device with num_sms SMs (<= 0:
+ * the current device).  Host arithmetic only. */
+LT_API lt_status_t lt_qk_norm_rope_bwd_plan(int64_t tokens, int d, int num_sms,
+                                            size_t *workspace_bytes);
+
+/*
+ * A paged key-value cache for softmax layers: the cache of the pages'
+ * "KV-cache reuse" and "Flash Decoding" features where a layer keeps its keys
+ * instead of a linear-attention state.  The caller owns the two pools;
+ * a page holds page_size consecutive tokens of one sequence, and a block
+ * table lists each sequence's pages in order.  Slot s of a pool is row
+ * s % page_size of page s / page_size.
+ */
+typedef enum {
+  LT_KV_F32 = 0,
+  LT_KV_BF16 = 1,
+  LT_KV_F16 = 2,
+  LT_KV_E4M3 = 3, /* 8-bit floats (4 exponent bits, largest 448), one scale per row */
+  LT_KV_INT8 = 4  /* 8-bit integers (-127 .. 127), one scale per row */
+} lt_kv_dtype_t;
+
+typedef struct {
+  void *k, *v;              /* device pools, 16-byte aligned */
+  float *k_scale, *v_scale; /* [num_pages][H_kv][page_size] fp32, 8-bit caches only (else NULL) */
+  int64_t k_page_stride, k_slot_stride, k_head_stride; /* in elements; a row's values are */
+  int64_t v_page_stride, v_slot_stride, v_head_stride; /* contiguous; multiples of 16 bytes */
+  int32_t num_pages, page_size, H_kv, d, dv; /* page_size 1 .. 65536, d and dv 64 or 128 */
+  lt_kv_dtype_t dtype;
+} lt_kv_cache_t;
+
+/*
+ * lt_kv_cache_write: new keys and values into the cache, quantised as they
+ * are written where the cache holds 8 bits.  For token t, head g and its row
+ * x of d (keys) or dv (values) numbers:
+ *     scale = max(max_c |x_c| / qmax, 2^-126),  code_c = round(x_c / scale)
+ * (qmax 448 or 127; to nearest, ties to even, divisions correctly rounded),
+ * and the row stands for code * scale.  A row that holds an infinity or a NaN
+ * gets the scale NaN, and reads back as NaN.
+ *
+ * k, v       [tokens][H_kv][d], [tokens][H_kv][dv] of element type dtype,
+ *            16-byte aligned; token strides as for lt_qk_norm_rope.
+ * slots      [tokens] int32 device: each token's slot, or -1: skip the token.
+ *            Any other slot outside the pool is skipped and reported
+ *            (LT_ERR_DEVICE_BAD_PAGE).  The slots of one call must differ:
+ *            one given twice is left with unspecified content.
+ * cache      dtype LT_KV_E4M3, LT_KV_INT8, or the type that dtype names (an
+ *            exact copy).  The pools must not overlap k, v or slots.
+ * Returns LT_OK, LT_ERR_INVALID_ARG, LT_ERR_UNSUPPORTED or LT_ERR_CUDA.
+ */
+LT_API lt_status_t lt_kv_cache_write(const lt_kv_cache_t *cache, const void *k, const void *v,
+                                     const int32_t *slots, int64_t tokens, int64_t k_stride,
+                                     int64_t v_stride, lt_stream_t stream, lt_dtype_t dtype);
+
+/*
+ * lt_kv_cache_read: a batch of sequences read back from the cache, packed as
+ * lt_linear_attn_fwd and lt_linear_attn_state take packed inputs: token
+ * cu_seqlens[s] + i of the outputs is token i of sequence s, the fp32 product
+ * code * scale rounded to dtype.
+ *
+ * block_table [B][table_stride] int32 device, max_pages entries used per row;
+ *            entries past a sequence's last page are not read.
+ * cu_seqlens [B+1] int32 device, cu_seqlens[0] = 0, non-decreasing,
+ *            cu_seqlens[B] <= N; rows of the outputs from cu_seqlens[B] on
+ *            are left as they were.  Inconsistent offsets, or a sequence
+ *            longer than max_pages pages, are reported
+ *            (LT_ERR_DEVICE_BAD_SEQLENS) and leave the rows that they describe
+ *            unspecified; the rows of a page outside the pool are left as
+ *            they were and reported (LT_ERR_DEVICE_BAD_PAGE).
+ * k_out, v_out  [N][H_kv][d], [N][H_kv][dv] dense, 16-byte aligned, 1 <= N <
+ *            2^31; they must not overlap the pools, the other inputs or each
+ *            other.
+ * dtype      LT_BF16, LT_F16 or LT_F32; for a cache that does not hold 8
+ *            bits, the cache's own type.
+ * Returns as lt_kv_cache_write.
+ */
+LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *block_table,
+                                    int64_t table_stride, int max_pages,
+                                    const int32_t *cu_seqlens, int B, int N, void *k_out,
+                                    void *v_out, lt_stream_t stream, lt_dtype_t dtype);
+
+/*
+ * lt_paged_attn_decode: softmax attention of one new token per sequence over
+ * the paged cache (the new token's own key and value written first, with
+ * lt_kv_cache_write).  For sequence b of n = seq_lens[b] tokens and query
+ * head h, with g = floor(h * H_kv / H_q) and j over the last min(n, window)
+ * tokens (window 0: all):
+ *     out_bh = sum_j p_j V_jg / sum_j p_j,   p_j = exp(scale * q_bh . K_jg)
+ *     lse_bh = log sum_j p_j
+ * A sequence of no tokens gives out = 0 and lse = -infinity.  The 8-bit
+ * caches are read as 8 bits; nothing is written back.
+ *
+ * q          [B][H_q][d] of element type dtype, dense, 16-byte aligned.
+ * cache, block_table, table_stride, max_pages   as for lt_kv_cache_read; the
+ *            cache's type is dtype's own or 8 bits.
+ * seq_lens   [B] int32 device.  A negative length, or one over max_pages
+ *            pages, is reported (LT_ERR_DEVICE_BAD_SEQLENS) and its rows of
+ *            out and lse are left as they were.  A page outside the pool is
+ *            reported (LT_ERR_DEVICE_BAD_PAGE) and its tokens take no part.
+ * scale      finite (1/sqrt(d) is usual).
+ * window     >= 0.
+ * out        [B][H_q][dv] of dtype, 16-byte aligned; lse [B][H_q] fp32 or
+ *            NULL; no overlaps with inputs or each other.
+ * B, H_q     1 <= B <= 65535, H_q a multiple of the cache's H_kv, at most
+ *            65535.
+ * workspace  as for lt_qk_norm_rope_bwd, with lt_paged_attn_decode_plan's bytes.
+ * Evaluation: the tiles of all (sequence, KV head) pairs are dealt out evenly
+ * to the warps of one persistent launch, whatever the lengths; each warp
+ * keeps a running maximum and sum in fp32, and a second launch joins the
+ * pieces of a pair that several warps share, in their order.  Scores, sums
+ * and accumulators are fp32; the weights are rounded to the cache's 16-bit
+ * type (fp16 for 8-bit caches) for the tensor cores, and not at all for
+ * LT_F32.
+ * Returns as lt_kv_cache_write.
+ */
+LT_API lt_status_t lt_paged_attn_decode(const void *q, const lt_kv_cache_t *cache,
+                                        const int32_t *block_table, int64_t table_stride,
+                                        int max_pages, const int32_t *seq_lens, int B, int H_q,
+                                        float scale, int window, void *out, float *lse,
+                                        void *workspace, size_t workspace_bytes,
+                                        lt_stream_t stream, lt_dtype_t dtype);
+
+/* Workspace bytes of lt_paged_attn_decode on a device with num_sms SMs (<= 0:
+ * the current device); they do not depend on the sequences.  Host arithmetic
+ * only. */
+LT_API lt_status_t lt_paged_attn_decode_plan(int H_q, int H_kv, int d, int dv, lt_dtype_t dtype,
+                                             lt_kv_dtype_t kv_dtype, int num_sms,
+                                             size_t *workspace_bytes);
+
+/*
  * Diagnostic schedule override, for tests and ablations only: makes every
  * later forward call of this process (every device, every thread) use a
  * given kernel path and/or block count instead of the one the library picks.
@@ -414,7 +621,7 @@ LT_API const char *lt_status_string(lt_status_t status);
 /*
  * Synchronise `stream`, then read and clear the current device's error
  * word.  Returns LT_OK, LT_ERR_DEVICE_TIMEOUT, LT_ERR_DEVICE_BAD_SEQLENS,
- * or LT_ERR_CUDA if the synchronisation itself failed.
+ * LT_ERR_DEVICE_BAD_PAGE, or LT_ERR_CUDA if the synchronisation itself failed.
  */
 LT_API lt_status_t lt_get_last_device_error(lt_stream_t stream);
 
