@@ -83,7 +83,7 @@ lib.lt_qk_norm_rope_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp
                                     _vp, _vp, _vp, _i64, _i, _i, _i, _i64, _i64, _i64, _i64, _f,
                                     _vp, _sz, _vp, _i, _i]
 lib.lt_qk_norm_rope_bwd.restype = _i
-lib.lt_qk_norm_rope_bwd_plan.argtypes = [_i64, _i, _i, ctypes.POINTER(_sz)]
+lib.lt_qk_norm_rope_bwd_plan.argtypes = [_i, _i, ctypes.POINTER(_sz)]
 lib.lt_qk_norm_rope_bwd_plan.restype = _i
 
 

@@ -7,10 +7,14 @@
 // do not depend on how a row is spread over lanes.  The floor on the scale
 // makes a row of zeros read back as zeros without a case of its own.
 //
-// Bound by memory.  A row is spread over w/8 lanes (the maximum is a 3- or
-// 4-step shuffle); each lane moves 8 elements, and holds kU rows in flight.
-// A block takes kTok tokens: their slots (or the sequences they belong to)
-// are looked up once, in shared memory, and used by all heads.
+// Bound by memory, quantising also close to instruction issue: the maximum of
+// a 16-bit row is taken two values at a time, and the quotients by a
+// multiplication and two corrections that round them exactly (see quotients).
+// A row is spread over w/16 lanes (the maximum is a 2- or 3-step shuffle);
+// each lane moves two chunks of 8 elements, w/2 apart, so that both the 16-bit
+// and the 8-bit side are accessed in whole runs.  A block looks up its tokens'
+// slots (or the sequences they belong to) once, in shared memory, for all
+// heads.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -24,9 +28,8 @@
 namespace lt {
 namespace {
 
-constexpr int kT = 256;   // threads
-constexpr int kTok = 32;  // tokens per block
-constexpr int kU = 4;     // rows in flight per thread
+constexpr int kT = 256;      // threads
+constexpr int kMaxTok = 64;  // tokens per block, at most
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 struct Pool {
@@ -39,6 +42,7 @@ struct Pool {
 struct CacheArgs {
   Pool pool[2];  // keys, values
   int num_pages, page_size, H;
+  int tok;  // tokens per block
   // write
   const void* in[2];
   int64_t stride[2];
@@ -59,259 +63,425 @@ struct Place {
   int page, slot;
 };
 
-// ------------------------------------------------ eight elements <-> codes
-// the cache's element types; Code<KV>::Raw is a lane's eight elements
+// A block's (token, head) rows in order, advanced by a fixed step.
+struct RowAt {
+  int tt, h, dt, dh, H;
+  __device__ __forceinline__ RowAt(int first, int step, int heads) : H(heads) {
+    tt = first / heads;
+    h = first - tt * heads;
+    dt = step / heads;
+    dh = step - dt * heads;
+  }
+  __device__ __forceinline__ void next() {
+    tt += dt;
+    h += dh;
+    if (h >= H) {
+      h -= H;
+      ++tt;
+    }
+  }
+};
+
+// ------------------------------------------------- chunks of eight elements
 struct E4M3 {};
 struct Int8 {};
+template <typename KV>
+struct KvMax;
+template <>
+struct KvMax<E4M3> {
+  static constexpr float value = 448.0f;
+};
+template <>
+struct KvMax<Int8> {
+  static constexpr float value = 127.0f;
+};
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* f) {
-  widen(load_quad(p), f);
-  widen(load_quad(p + 4), f + 4);
+struct Chunk {  // 16-bit elements
+  uint4 r;
+};
+template <>
+struct Chunk<float> {
+  float4 r[2];
+};
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_chunk(const T* p) {
+  Chunk<T> c;
+  if constexpr (sizeof(T) == 2) {
+    c.r = __ldg(reinterpret_cast<const uint4*>(p));
+  } else {
+    c.r[0] = __ldg(reinterpret_cast<const float4*>(p));
+    c.r[1] = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  return c;
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float* f) {
-  store_quad(p, f);
-  store_quad(p + 4, f + 4);
+__device__ __forceinline__ void widen8(const Chunk<T>& c, F2* f) {
+  if constexpr (sizeof(T) == 2) {
+    widen2x2(Quad<T>{make_uint2(c.r.x, c.r.y)}, f);
+    widen2x2(Quad<T>{make_uint2(c.r.z, c.r.w)}, f + 2);
+  } else {
+    widen2x2(Quad<float>{c.r[0]}, f);
+    widen2x2(Quad<float>{c.r[1]}, f + 2);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const F2* f) {
+  if constexpr (sizeof(T) == 2) {
+    uint4 r;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = unpack_f2(f[e]);
+      T two[2];
+      from_float(&two[0], x.x);
+      from_float(&two[1], x.y);
+      w[e] = *reinterpret_cast<const uint32_t*>(two);
+    }
+    *reinterpret_cast<uint4*>(p) = r;
+  } else {
+    store_quad(p, f[0], f[1]);
+    store_quad(p + 4, f[2], f[3]);
+  }
 }
 
-__device__ __forceinline__ uint2 encode(const float* y, E4M3) {
-  uint2 r;
-  const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(y[4], y[5]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t d = __nv_cvt_float2_to_fp8x2(make_float2(y[6], y[7]), __NV_SATFINITE, __NV_E4M3);
-  r.x = a | (b << 16);
-  r.y = c | (d << 16);
-  return r;
+// Bits of the largest magnitude of a chunk, as fp32.  Those of an infinity and
+// of a NaN lie above every finite value's, so a row that holds one is seen.
+__device__ __forceinline__ uint32_t top_bits(const Chunk<float>& c) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float f[4] = {c.r[q].x, c.r[q].y, c.r[q].z, c.r[q].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+  }
+  return m;
 }
-__device__ __forceinline__ uint2 encode(const float* y, Int8) {
+template <typename T>
+__device__ __forceinline__ uint32_t top_bits(const Chunk<T>& c) {
+  // 16-bit magnitudes order as integers, NaN last, like fp32's; two at a time
+  const uint32_t k = 0x7fff7fffu;
+  const uint32_t m = __vmaxu2(__vmaxu2(c.r.x & k, c.r.y & k), __vmaxu2(c.r.z & k, c.r.w & k));
+  const uint16_t top = (uint16_t)max(m & 0xffffu, m >> 16);
+  if constexpr (sizeof(T) == 2) {
+    T x;
+    *reinterpret_cast<uint16_t*>(&x) = top;
+    return __float_as_uint(to_float(x)) & 0x7fffffffu;
+  }
+}
+
+// y[0..3] / scale, each quotient correctly rounded.  With v the correctly
+// rounded reciprocal, q = x v is within two steps of x / scale; one correction
+// q + (x - q scale) v brings it within one, and Markstein's theorem (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990) makes the second, whose remainder is exact, the rounded quotient.  The
+// remainder is exact while it stays above fp32's smallest numbers: for scales
+// within 2^-80 .. 2^80 and quotients that do not round to code 0 anyway.
+// Rows outside divide.
+__device__ __forceinline__ void quotients(F2* y, float scale) {
+  if (scale >= 8.2718061e-25f && scale <= 1.2089258e+24f) {
+    const float v = __frcp_rn(scale);
+    const F2 v2 = pack_f2(v, v), n2 = pack_f2(-scale, -scale);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      F2 q = mul2(y[e], v2);
+      q = fma2(fma2(q, n2, y[e]), v2, q);
+      y[e] = fma2(fma2(q, n2, y[e]), v2, q);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = unpack_f2(y[e]);
+      y[e] = pack_f2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale));
+    }
+  }
+}
+
+__device__ __forceinline__ uint2 encode(const F2* y, E4M3) {
+  uint32_t h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    h[e] = __nv_cvt_float2_to_fp8x2(unpack_f2(y[e]), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+__device__ __forceinline__ uint2 encode(const F2* y, Int8) {
+  // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the
+  // low bits as a two's complement number
+  const F2 magic = pack_f2(12582912.0f, 12582912.0f);
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    w[h] = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[h] |= ((uint32_t)__float2int_rn(y[4 * h + e]) & 0xffu) << (8 * e);
+    const float2 a = unpack_f2(add2(y[2 * h], magic)), b = unpack_f2(add2(y[2 * h + 1], magic));
+    const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+    w[h] = __byte_perm(lo, hi, 0x5410);
   }
   return make_uint2(w[0], w[1]);
 }
-__device__ __forceinline__ void decode(uint2 r, float* y, E4M3) {
+__device__ __forceinline__ void decode(uint2 r, F2* y, E4M3) {
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     const uint32_t word = h < 2 ? r.x : r.y;
     const __half2_raw t =
         __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word >> (16 * (h & 1))), __NV_E4M3);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&t));
-    y[2 * h] = f.x;
-    y[2 * h + 1] = f.y;
+    y[h] = pack_f2(f.x, f.y);
   }
 }
-__device__ __forceinline__ void decode(uint2 r, float* y, Int8) {
+__device__ __forceinline__ void decode(uint2 r, F2* y, Int8) {
+  // the byte, offset by 128, as the low bits of 2^23, less 2^23 + 128: exact
+  const F2 bias = pack_f2(-8388736.0f, -8388736.0f);
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    y[e] = (float)(int8_t)((e < 4 ? r.x : r.y) >> (8 * (e & 3)));
+  for (int h = 0; h < 4; ++h) {
+    const uint32_t word = (h < 2 ? r.x : r.y) ^ 0x80808080u;
+    const uint32_t a = __byte_perm(word, 0x4b000000u, h & 1 ? 0x7442 : 0x7440);
+    const uint32_t b = __byte_perm(word, 0x4b000000u, h & 1 ? 0x7443 : 0x7441);
+    y[h] = add2(pack_f2(__uint_as_float(a), __uint_as_float(b)), bias);
+  }
 }
 
-template <typename KV>
-struct IsQuant {
-  static constexpr bool value = false;
-};
-template <>
-struct IsQuant<E4M3> {
-  static constexpr bool value = true;
-};
-template <>
-struct IsQuant<Int8> {
-  static constexpr bool value = true;
-};
-template <typename KV>
-__device__ __forceinline__ float qmax() {
-  return 448.0f;
-}
-template <>
-__device__ __forceinline__ float qmax<Int8>() {
-  return 127.0f;
+// ---------------------------------------------------------- tokens' places
+__device__ __forceinline__ Place place_of_slot(const CacheArgs& a, int64_t t) {
+  const int s = a.slots[t];
+  if (s >= 0 && s / a.page_size < a.num_pages) return Place{s / a.page_size, s % a.page_size};
+  if (s != -1) report_error(a.err, kDevErrBadPage);
+  return Place{-1, 0};
 }
 
-// ------------------------------------------------------------------- write
+__device__ __forceinline__ Place place_of_row(const CacheArgs& a, int t) {
+  // the sequence that holds row t: the last s with cu[s] <= t; a row that no
+  // sequence holds is left alone
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.cu + mid) <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int begin = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1);
+  if (begin >= 0 && t >= begin && t < end &&
+      (int64_t)end - begin <= (int64_t)a.max_pages * a.page_size) {
+    const int i = t - begin, n = i / a.page_size;
+    const int page = __ldg(a.table + (int64_t)lo * a.table_stride + n);
+    if (page >= 0 && page < a.num_pages) return Place{page, i - n * a.page_size};
+    report_error(a.err, kDevErrBadPage);
+  }
+  return Place{-1, 0};
+}
+
+// every offset of a batch, whichever rows it describes
+__device__ __forceinline__ void check_offsets(const CacheArgs& a) {
+  for (int s = threadIdx.x; s < a.B; s += kT) {
+    const int begin = a.cu[s], end = a.cu[s + 1];
+    if ((s == 0 && begin != 0) || begin < 0 || end < begin || end > a.N ||
+        (int64_t)end - begin > (int64_t)a.max_pages * a.page_size)
+      report_error(a.err, kDevErrBadSeqlens);
+  }
+}
+
+// ----------------------------------------------------------------- kernels
 // blockIdx.y: 0 keys, 1 values
 template <typename T, typename KV>
-__global__ void __launch_bounds__(kT) lt_kv_write_kernel(const CacheArgs a) {
-  __shared__ Place place[kTok];
+__global__ void __launch_bounds__(kT) lt_kv_quant_kernel(const CacheArgs a) {
+  constexpr int kU = 2;  // rows in flight per thread
+  __shared__ Place place[kMaxTok];
   const int which = blockIdx.y;
   const Pool pool = a.pool[which];
-  const int64_t t0 = (int64_t)blockIdx.x * kTok;
-  const int nt = (int)min((int64_t)kTok, a.tokens - t0);
-  if (threadIdx.x < nt) {
-    const int s = a.slots[t0 + threadIdx.x];
-    Place pl{-1, 0};
-    if (s >= 0 && s / a.page_size < a.num_pages)
-      pl = Place{s / a.page_size, s % a.page_size};
-    else if (s != -1)
-      report_error(a.err, kDevErrBadPage);
-    place[threadIdx.x] = pl;
-  }
+  const int64_t t0 = (int64_t)blockIdx.x * a.tok;
+  const int nt = (int)min((int64_t)a.tok, a.tokens - t0);
+  if (threadIdx.x < nt) place[threadIdx.x] = place_of_slot(a, t0 + threadIdx.x);
   __syncthreads();
-  const int L = pool.w >> 3, RG = kT / L;  // lanes per row, rows at a time
+  const int half = pool.w >> 1, L = pool.w >> 4, RG = kT / L;  // lanes per row, rows at a time
   const int grp = threadIdx.x / L, j = threadIdx.x % L;
   const int rows = nt * a.H;
   const T* in = static_cast<const T*>(a.in[which]) + t0 * a.stride[which] + j * 8;
   const int first = (threadIdx.x & ~31) / L;  // warps stay converged for the shuffles
+  RowAt at(grp, RG, a.H);
 #pragma unroll 1
   for (int r = grp, rw = first; rw < rows; r += RG * kU, rw += RG * kU) {
-    float y[kU][8];
+    Chunk<T> x[kU][2];
     Place pl[kU];
     int hd[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int row = r + u * RG;
       pl[u].page = -1;
-      hd[u] = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[u][e] = 0.0f;
-      if (row < rows) {
-        const int tt = row / a.H;
-        hd[u] = row - tt * a.H;
-        pl[u] = place[tt];
-        if (pl[u].page >= 0) load8(in + (int64_t)tt * a.stride[which] + hd[u] * pool.w, y[u]);
+      hd[u] = at.h;
+      x[u][0] = x[u][1] = Chunk<T>{};
+      if (r + u * RG < rows) {
+        pl[u] = place[at.tt];
+        const T* p = in + at.tt * a.stride[which] + at.h * pool.w;
+        x[u][0] = load_chunk(p);
+        x[u][1] = load_chunk(p + half);
       }
+      at.next();
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int64_t off = (int64_t)pl[u].page * pool.page + (int64_t)pl[u].slot * pool.slot +
-                          (int64_t)hd[u] * pool.head + j * 8;
-      if constexpr (!IsQuant<KV>::value) {
-        if (pl[u].page >= 0) store8(static_cast<T*>(pool.p) + off, y[u]);
-      } else {
-        // the largest magnitude as bits: those of a NaN and of an infinity lie
-        // above every finite one, so a row that holds any is seen
-        uint32_t top = 0;
+      uint32_t top = max(top_bits(x[u][0]), top_bits(x[u][1]));
+      for (int o = L >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool finite = top < 0x7f800000u;
+      const float scale = fmaxf(__fdiv_rn(__uint_as_float(top), KvMax<KV>::value), kTiny);
+      if (pl[u].page < 0) continue;
+      uint8_t* out = static_cast<uint8_t*>(pool.p) + (int64_t)pl[u].page * pool.page +
+                     (int64_t)pl[u].slot * pool.slot + (int64_t)hd[u] * pool.head + j * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[u][e]) & 0x7fffffffu);
-        for (int o = L >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const bool finite = top < 0x7f800000u;
-        const float scale = finite ? fmaxf(__fdiv_rn(__uint_as_float(top), qmax<KV>()), kTiny)
-                                   : __uint_as_float(0x7fc00000u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[u][e] = finite ? __fdiv_rn(y[u][e], scale) : 0.0f;
-        const uint2 c = encode(y[u], KV());
-        if (pl[u].page >= 0) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool.p) + off) = c;
-          if (j == 0)
-            pool.scale[((int64_t)pl[u].page * a.H + hd[u]) * a.page_size + pl[u].slot] = scale;
-        }
+      for (int c = 0; c < 2; ++c) {
+        F2 y[4];
+        widen8(x[u][c], y);
+        quotients(y, scale);
+        const uint2 code = encode(y, KV());
+        *reinterpret_cast<uint2*>(out + c * half) = finite ? code : make_uint2(0, 0);
       }
+      if (j == 0)
+        pool.scale[((int64_t)pl[u].page * a.H + hd[u]) * a.page_size + pl[u].slot] =
+            finite ? scale : __uint_as_float(0x7fc00000u);
     }
   }
 }
 
-// -------------------------------------------------------------------- read
 template <typename T, typename KV>
-__global__ void __launch_bounds__(kT) lt_kv_read_kernel(const CacheArgs a) {
-  __shared__ Place place[kTok];
+__global__ void __launch_bounds__(kT) lt_kv_dequant_kernel(const CacheArgs a) {
+  constexpr int kU = 4;
+  __shared__ Place place[kMaxTok];
   const int which = blockIdx.y;
   const Pool pool = a.pool[which];
-  const int t0 = blockIdx.x * kTok;
-  const int nt = min(kTok, a.N - t0);
-  if (blockIdx.x == 0 && which == 0) {  // every offset, whichever rows it describes
-    for (int s = threadIdx.x; s < a.B; s += kT) {
-      const int begin = a.cu[s], end = a.cu[s + 1];
-      if ((s == 0 && begin != 0) || begin < 0 || end < begin || end > a.N ||
-          (int64_t)end - begin > (int64_t)a.max_pages * a.page_size)
-        report_error(a.err, kDevErrBadSeqlens);
-    }
-  }
-  if (threadIdx.x < nt) {
-    // the sequence that holds row t: the last s with cu[s] <= t; a row that
-    // no sequence holds is left alone
-    const int t = t0 + threadIdx.x;
-    int lo = 0, hi = a.B;  // cu[lo] <= t < cu[hi], for consistent offsets
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu[mid] <= t)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int begin = a.cu[lo], end = a.cu[lo + 1];
-    Place pl{-1, 0};
-    if (begin >= 0 && t >= begin && t < end &&
-        (int64_t)end - begin <= (int64_t)a.max_pages * a.page_size) {
-      const int i = t - begin, page = a.table[(int64_t)lo * a.table_stride + i / a.page_size];
-      if (page >= 0 && page < a.num_pages)
-        pl = Place{page, i % a.page_size};
-      else
-        report_error(a.err, kDevErrBadPage);
-    }
-    place[threadIdx.x] = pl;
-  }
+  const int t0 = blockIdx.x * a.tok;
+  const int nt = min(a.tok, a.N - t0);
+  if (blockIdx.x == 0 && which == 0) check_offsets(a);
+  if (threadIdx.x < nt) place[threadIdx.x] = place_of_row(a, t0 + threadIdx.x);
   __syncthreads();
-  const int L = pool.w >> 3, RG = kT / L;
+  const int half = pool.w >> 1, L = pool.w >> 4, RG = kT / L;
   const int grp = threadIdx.x / L, j = threadIdx.x % L;
   const int rows = nt * a.H;
   T* out = static_cast<T*>(a.out[which]) + (int64_t)t0 * a.H * pool.w + j * 8;
+  RowAt at(grp, RG, a.H);
 #pragma unroll 1
   for (int r = grp; r < rows; r += RG * kU) {
-    float y[kU][8], scale[kU];
-    uint2 c[kU];
+    uint2 code[kU][2];
+    float scale[kU];
     bool live[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int row = r + u * RG;
       live[u] = false;
-      if (row < rows) {
-        const int tt = row / a.H, h = row - tt * a.H;
-        const Place pl = place[tt];
+      if (r + u * RG < rows) {
+        const Place pl = place[at.tt];
         live[u] = pl.page >= 0;
         if (live[u]) {
-          const int64_t off = (int64_t)pl.page * pool.page + (int64_t)pl.slot * pool.slot +
-                              (int64_t)h * pool.head + j * 8;
-          if constexpr (IsQuant<KV>::value) {
-            c[u] = __ldg(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(pool.p) + off));
-            scale[u] = __ldg(&pool.scale[((int64_t)pl.page * a.H + h) * a.page_size + pl.slot]);
-          } else {
-            load8(static_cast<const T*>(pool.p) + off, y[u]);
-          }
+          const uint8_t* p = static_cast<const uint8_t*>(pool.p) + (int64_t)pl.page * pool.page +
+                             (int64_t)pl.slot * pool.slot + (int64_t)at.h * pool.head + j * 8;
+          code[u][0] = __ldg(reinterpret_cast<const uint2*>(p));
+          code[u][1] = __ldg(reinterpret_cast<const uint2*>(p + half));
+          scale[u] = __ldg(&pool.scale[((int64_t)pl.page * a.H + at.h) * a.page_size + pl.slot]);
         }
       }
+      at.next();
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (!live[u]) continue;
-      if constexpr (IsQuant<KV>::value) {
-        decode(c[u], y[u], KV());
+      const F2 s2 = pack_f2(scale[u], scale[u]);
+      T* o = out + (int64_t)(r + u * RG) * pool.w;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[u][e] *= scale[u];
+      for (int c = 0; c < 2; ++c) {
+        F2 y[4];
+        decode(code[u][c], y, KV());
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], s2);
+        store8(o + c * half, y);
       }
-      store8(out + (int64_t)(r + u * RG) * pool.w, y[u]);
     }
   }
 }
 
-template <typename T, typename KV>
-cudaError_t launch_t(const CacheArgs& a, bool write, cudaStream_t s) {
-  const int64_t n = write ? a.tokens : a.N;
-  const dim3 grid((unsigned)((n + kTok - 1) / kTok), 2);
-  if (write)
-    lt_kv_write_kernel<T, KV><<<grid, kT, 0, s>>>(a);
-  else
-    lt_kv_read_kernel<T, KV><<<grid, kT, 0, s>>>(a);
-  return cudaGetLastError();
+// Rows as they are, in 16-byte pieces: into the cache, or out of it.  Strides
+// and widths are in bytes here, whatever the type.
+template <bool kWrite>
+__global__ void __launch_bounds__(kT) lt_kv_copy_kernel(const CacheArgs a) {
+  constexpr int kU = 4;
+  __shared__ Place place[kMaxTok];
+  const int which = blockIdx.y;
+  const Pool pool = a.pool[which];
+  const int64_t t0 = (int64_t)blockIdx.x * a.tok;
+  const int nt = (int)min((int64_t)a.tok, (kWrite ? a.tokens : (int64_t)a.N) - t0);
+  if (!kWrite && blockIdx.x == 0 && which == 0) check_offsets(a);
+  if (threadIdx.x < nt)
+    place[threadIdx.x] =
+        kWrite ? place_of_slot(a, t0 + threadIdx.x) : place_of_row(a, (int)t0 + threadIdx.x);
+  __syncthreads();
+  const int L = pool.w >> 4, RG = kT / L;
+  const int grp = threadIdx.x / L, j = threadIdx.x % L;
+  const int rows = nt * a.H;
+  const uint8_t* in = static_cast<const uint8_t*>(a.in[which]) + t0 * a.stride[which] + j * 16;
+  uint8_t* out = static_cast<uint8_t*>(a.out[which]) + t0 * a.H * pool.w + j * 16;
+  RowAt at(grp, RG, a.H);
+#pragma unroll 1
+  for (int r = grp; r < rows; r += RG * kU) {
+    uint4 x[kU];
+    uint8_t* dst[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      dst[u] = nullptr;
+      if (r + u * RG < rows) {
+        const Place pl = place[at.tt];
+        if (pl.page >= 0) {
+          uint8_t* row = static_cast<uint8_t*>(pool.p) + (int64_t)pl.page * pool.page +
+                         (int64_t)pl.slot * pool.slot + (int64_t)at.h * pool.head + j * 16;
+          const uint8_t* src = kWrite ? in + at.tt * a.stride[which] + at.h * pool.w : row;
+          dst[u] = kWrite ? row : out + (int64_t)(r + u * RG) * pool.w;
+          x[u] = __ldg(reinterpret_cast<const uint4*>(src));
+        }
+      }
+      at.next();
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = x[u];
+  }
 }
 
 template <typename T>
-cudaError_t launch_kv(const CacheArgs& a, lt_kv_dtype_t kv, bool write, cudaStream_t s) {
-  if (kv == LT_KV_E4M3) return launch_t<T, E4M3>(a, write, s);
-  if (kv == LT_KV_INT8) return launch_t<T, Int8>(a, write, s);
-  return launch_t<T, T>(a, write, s);
+cudaError_t launch_quant(const CacheArgs& a, bool e4m3, bool write, dim3 grid, cudaStream_t s) {
+  if (write)
+    e4m3 ? lt_kv_quant_kernel<T, E4M3><<<grid, kT, 0, s>>>(a)
+         : lt_kv_quant_kernel<T, Int8><<<grid, kT, 0, s>>>(a);
+  else
+    e4m3 ? lt_kv_dequant_kernel<T, E4M3><<<grid, kT, 0, s>>>(a)
+         : lt_kv_dequant_kernel<T, Int8><<<grid, kT, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
-cudaError_t launch(const CacheArgs& a, lt_dtype_t t, lt_kv_dtype_t kv, bool write,
+// Tokens per block: enough to share the lookup of their places, few enough
+// that a decode step's tokens spread over the device.
+int token_block(int64_t tokens, int sms) {
+  const int64_t n = tokens / (4 * sms);
+  return n < 1 ? 1 : n > kMaxTok ? kMaxTok : (int)n;
+}
+
+cudaError_t launch(CacheArgs a, lt_dtype_t t, lt_kv_dtype_t kv, bool write, int sms,
                    cudaStream_t s) {
-  return t == LT_BF16  ? launch_kv<__nv_bfloat16>(a, kv, write, s)
-         : t == LT_F16 ? launch_kv<__half>(a, kv, write, s)
-                       : launch_kv<float>(a, kv, write, s);
+  const int64_t n = write ? a.tokens : a.N;
+  a.tok = token_block(n, sms);
+  const dim3 grid((unsigned)((n + a.tok - 1) / a.tok), 2);
+  if (eight_bit(kv)) {
+    const bool e4m3 = kv == LT_KV_E4M3;
+    return t == LT_BF16  ? launch_quant<__nv_bfloat16>(a, e4m3, write, grid, s)
+           : t == LT_F16 ? launch_quant<__half>(a, e4m3, write, grid, s)
+                         : launch_quant<float>(a, e4m3, write, grid, s);
+  }
+  const int es = (int)kv_size(kv);
+  for (int i = 0; i < 2; ++i) {
+    a.pool[i].page *= es;
+    a.pool[i].slot *= es;
+    a.pool[i].head *= es;
+    a.pool[i].w *= es;
+    a.stride[i] *= es;
+  }
+  if (write)
+    lt_kv_copy_kernel<true><<<grid, kT, 0, s>>>(a);
+  else
+    lt_kv_copy_kernel<false><<<grid, kT, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 CacheArgs args_of(const lt_kv_cache_t* c) {
@@ -390,7 +560,7 @@ extern "C" lt_status_t lt_kv_cache_write(const lt_kv_cache_t* cache, const void*
   if (!dtype_ok(dtype) || (!eight_bit(cache->dtype) && cache->dtype != kv_of(dtype)))
     return LT_ERR_UNSUPPORTED;
   const size_t es = dtype_size(dtype);
-  if (!k || !v || !slots || tokens < 1 || tokens > (int64_t)kTok * 0x7fffffff ||
+  if (!k || !v || !slots || tokens < 1 || tokens > 0x7fffffff ||
       !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(slots, 4) ||
       !stride_ok(tokens, k_stride, cache->H_kv, cache->d, es) ||
       !stride_ok(tokens, v_stride, cache->H_kv, cache->dv, es))
@@ -414,9 +584,11 @@ extern "C" lt_status_t lt_kv_cache_write(const lt_kv_cache_t* cache, const void*
   a.slots = slots;
   a.tokens = tokens;
   a.err = device_error_word_current();
-  if (!a.err) return LT_ERR_CUDA;
-  return launch(a, dtype, cache->dtype, true, (cudaStream_t)stream) == cudaSuccess ? LT_OK
-                                                                                    : LT_ERR_CUDA;
+  const int sms = device_sm_count();
+  if (!a.err || sms <= 0) return LT_ERR_CUDA;
+  return launch(a, dtype, cache->dtype, true, sms, (cudaStream_t)stream) == cudaSuccess
+             ? LT_OK
+             : LT_ERR_CUDA;
 }
 
 extern "C" lt_status_t lt_kv_cache_read(const lt_kv_cache_t* cache, const int32_t* block_table,
@@ -456,7 +628,9 @@ extern "C" lt_status_t lt_kv_cache_read(const lt_kv_cache_t* cache, const int32_
   a.out[0] = k_out;
   a.out[1] = v_out;
   a.err = device_error_word_current();
-  if (!a.err) return LT_ERR_CUDA;
-  return launch(a, dtype, cache->dtype, false, (cudaStream_t)stream) == cudaSuccess ? LT_OK
-                                                                                     : LT_ERR_CUDA;
+  const int sms = device_sm_count();
+  if (!a.err || sms <= 0) return LT_ERR_CUDA;
+  return launch(a, dtype, cache->dtype, false, sms, (cudaStream_t)stream) == cudaSuccess
+             ? LT_OK
+             : LT_ERR_CUDA;
 }

@@ -69,6 +69,56 @@ __device__ __forceinline__ void store_quad(__half* p, const float* f) {
                                             *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// ------------------------------------------------------- two fp32 at a time
+// sm_100 multiplies and adds register pairs of fp32 in one instruction, each
+// half rounded as by the scalar one.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 pack_f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f2(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 swap2(F2 a) {
+  const float2 t = unpack_f2(a);
+  return pack_f2(t.y, t.x);
+}
+
+template <typename T>
+__device__ __forceinline__ void widen2x2(const Quad<T>& q, F2* f) {
+  float x[4];
+  widen(q, x);
+  f[0] = pack_f2(x[0], x[1]);
+  f[1] = pack_f2(x[2], x[3]);
+}
+template <typename T>
+__device__ __forceinline__ void store_quad(T* p, F2 a, F2 b) {
+  const float2 x = unpack_f2(a), y = unpack_f2(b);
+  const float f[4] = {x.x, x.y, y.x, y.y};
+  store_quad(p, f);
+}
+
 // The results of the launch before this one on the stream are complete and
 // visible after dependency_wait(); dependency_release() lets the launch after
 // this one start early (its own wait still covers this whole launch).

@@ -1,0 +1,958 @@
+// paged_attn.cuh -- softmax attention of one new token per sequence over a
+// paged key-value cache: the first launch, and the schedule that both share.
+//
+// For sequence b, KV head g and its query heads h (G per KV head), over the
+// keys j that the window keeps:
+//     out_h = sum_j p_j V_j / sum_j p_j,   p_j = exp(scale q_h . K_j).
+// One pass over the cache: with m the largest score so far, each tile adds
+// exp2(s_j - m) and exp2(s_j - m) V_j to a running sum and accumulator, which
+// are rescaled when m grows.  Pieces of a sequence join by the same rule.
+//
+// Bound by memory: every key and value is read once, for G <= 16 query heads,
+// 2G flops per byte of a 16-bit cache.
+//
+// Split: the cache of all (sequence, KV head) pairs, cut into tiles of kTile
+// tokens and laid end to end, is dealt out in equal runs to the warps of one
+// launch with a fixed number of blocks, whatever the lengths: a batch of very
+// different sequences and one long sequence load the SMs alike, and the
+// workspace does not grow with either.  A warp owns its run: its own ring of
+// tiles in shared memory, filled with 16-byte asynchronous copies, its own
+// running maximum and sum; no barrier between warps.  A pair that lies inside
+// one run is finished by its warp.  A pair that several runs share leaves one
+// partial result per run, and a second launch, which starts early and waits
+// for the first, joins them in run order, so results do not depend on timing.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/lt_linear_attn.h"
+#include "lt_check.h"
+#include "lt_internal.h"
+#include "lt_ptx.cuh"
+#include "lt_vec.cuh"
+
+namespace lt {
+namespace paged {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTokens = 16;  // tokens per tile, in every engine
+
+struct E4M3 {
+  uint8_t b;
+};
+struct Int8 {
+  int8_t b;
+};
+
+struct DecodeArgs {
+  const void* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* ks;
+  const float* vs;
+  int64_t kpg, ksl, khd, vpg, vsl, vhd;  // pool strides, bytes
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  int B, Hq, Hkv, G, nhb;  // nhb: blocks of query heads per KV head
+  int hb;                  // query heads per block (the engine's kHeads)
+  int num_pages, page_size, max_pages, window;
+  int warps;      // runs the tiles are dealt to
+  int min_tiles;  // shortest run
+  float scale;
+  void* out;
+  float* lse;
+  float* part;  // [warps][2][hb][dv] partial accumulators
+  float* ml;    // [warps][2][hb][2] their maximum and sum
+  int dv, dtype;
+  int* err;
+};
+
+// ------------------------------------------------------------ the schedule
+struct Seq {
+  int first, len;  // keys [first, len) take part
+  int tiles;
+  bool bad;
+};
+__device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b) {
+  Seq s;
+  s.len = a.lens[b];
+  // (positions up to a tile past the end stay inside 32 bits)
+  s.bad = s.len < 0 || (int64_t)s.len > min((int64_t)a.max_pages * a.page_size, (int64_t)0x7fffff00);
+  if (s.bad) s.len = 0;
+  s.first = a.window ? max(0, s.len - a.window) : 0;
+  s.tiles = (s.len - s.first + kTokens - 1) / kTokens;
+  return s;
+}
+
+// tiles per run, from the tiles of all pairs
+__device__ __forceinline__ int64_t run_length(const DecodeArgs& a, int64_t total) {
+  return max((total + a.warps - 1) / a.warps, (int64_t)a.min_tiles);
+}
+
+// --------------------------------------------------------------- copies
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;  // the rest of the 16 bytes is zero-filled
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Position of 16-byte chunk c of row r in a tile whose rows are RB bytes:
+// chunks are permuted within 128 bytes so that eight consecutive rows' chunk c
+// lie in eight different bank groups.
+template <int RB>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  constexpr int kPer = RB >= 128 ? 1 : 128 / RB;        // rows per 128 bytes
+  constexpr int kMask = (RB >= 128 ? 8 : RB / 16) - 1;  // chunks permuted among
+  return (uint32_t)(r * RB + ((c ^ ((r / kPer) & kMask)) << 4));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return ex2_approx(x); }
+
+// What an engine is told of a tile in shared memory.
+struct TileAt {
+  uint32_t k, v;     // shared addresses of the two tiles
+  const float* ks;   // scales of the tile's tokens (8-bit caches)
+  const float* vs;
+  uint32_t mask;     // tokens that take part
+};
+
+// ------------------------------------------------- tensor-core instructions
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0,
+                                                   uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the transpose of an 8 x 8 tile of 16-bit values held one word per lane
+__device__ __forceinline__ uint32_t transpose8(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 t = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// two values of a word
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (__is_same(T, __nv_bfloat16))
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+__device__ __forceinline__ void store_pair(float* p, float a, float b) {
+  *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
+template <typename T>
+__device__ __forceinline__ void store_pair(T* p, float a, float b) {
+  *reinterpret_cast<uint32_t*>(p) = pack2<T>(a, b);
+}
+
+// Where an engine leaves a pair's result: rows of out and lse, or of the
+// partial accumulators with their maximum and sum.
+template <typename T>
+struct Sink {
+  bool partial;
+  T* out;       // [heads][dv]
+  float* lse;   // [heads] or nullptr
+  float* part;  // [heads][dv]
+  float* ml;    // [heads][2]
+};
+
+// the sum's reciprocal; no key with a weight above zero gives zeros
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+// log of the sum, of weights relative to 2^m
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// --------------------------------------------------- engine: tensor cores
+template <typename KT>
+struct KvTraits {  // 16-bit caches: the cache's own type
+  using Math = KT;
+  static constexpr int kBytes = 2;
+  static constexpr bool kQuant = false;
+};
+template <>
+struct KvTraits<E4M3> {
+  using Math = __half;  // every e4m3 value is an fp16 value
+  static constexpr int kBytes = 1;
+  static constexpr bool kQuant = true;
+};
+template <>
+struct KvTraits<Int8> {
+  using Math = __half;
+  static constexpr int kBytes = 1;
+  static constexpr bool kQuant = true;
+};
+
+// two bytes (the low half of w) -> two fp16 values, exactly
+__device__ __forceinline__ uint32_t widen2(uint32_t w, E4M3) {
+  const __half2_raw t = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+// four bytes -> (bytes 0, 1) and (bytes 2, 3), or with kSplit (0, 2) and (1, 3)
+template <bool kSplit>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi, E4M3 t) {
+  if (kSplit) w = __byte_perm(w, 0, 0x3120);
+  lo = widen2(w, t);
+  hi = widen2(w >> 16, t);
+}
+// an integer byte x as the fp16 value 1024 + (x + 128) (its bits are 0x6400 plus
+// the offset byte), less 1152: exact
+template <bool kSplit>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi, Int8) {
+  w ^= 0x80808080u;
+  uint32_t a = __byte_perm(w, 0x64646464u, kSplit ? 0x4240 : 0x4140);
+  uint32_t b = __byte_perm(w, 0x64646464u, kSplit ? 0x4341 : 0x4342);
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+  const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias);
+  const __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// Legacy mma on purpose: a KV head has G query heads, so a tcgen05 tile of 128
+// rows would be nearly empty, and the work is bound by memory.  The tokens are
+// the 16 rows of the instruction and the query heads its 8 columns, so that
+// few of its lanes idle: per 16 tokens of a 16-bit cache of width 128 a warp
+// issues 24 mma and 16 ldmatrix for 8 KB read.  kNB blocks of 8 heads share a
+// tile's registers.
+//
+// Scores S^T = K Q^T: A = K (ldmatrix of the token rows), B = Q (in registers).
+// Values O^T = V^T P^T: A = V by transposing ldmatrix, B = the weights, whose
+// 8 x 8 tiles are turned from S^T's layout by movmatrix.
+//
+// The weights of 16-bit caches are split into two terms of the cache's type,
+// high and rest (two products), so that their rounding, which would be as
+// large as the output's own, drops out; those of 8-bit caches are fp16, whose
+// 2^-11 is far below a bf16 output's 2^-8, and split for fp16 outputs only.
+//
+// 8-bit caches are widened to fp16 in registers.  A lane's four bytes of a key
+// row are four neighbouring d, where the instruction's A layout has two pairs
+// eight apart: Q's registers are filled in the same order instead.  A lane's
+// transposed word of V holds two columns of two tokens: the even columns are
+// rows 0 .. 7 of the product, the odd ones rows 8 .. 15.  Key scales multiply
+// the scores; value scales go into the weights, relative to a power of two A
+// >= every scale seen, so that the fp16 weights stay at most 2^kShift.  Q is
+// scaled by a power of two per head into [1, 2), so that no bf16 query leaves
+// fp16's range.
+//
+// kShift: fp16 weights are held times 2^12 (it cancels in the division), so
+// that weights down to 2^-26 of the largest keep fp16's full precision; 2^12 *
+// 65504 * 2^31 keys stay inside fp32.  bf16 has fp32's range and needs none.
+//
+// The maximum moves only when some score passes it: one vote per tile instead
+// of a reduction.
+template <typename QT_, typename KT, int D, int DV, int kNB>
+struct MmaEngine {
+  using QT = QT_;
+  using Kv = KvTraits<KT>;
+  using MT = typename Kv::Math;
+  static constexpr bool kQuant = Kv::kQuant;
+  static constexpr bool kHalf = !__is_same(MT, __nv_bfloat16);
+  static constexpr bool kSplit = !kQuant || __is_same(QT, __half);
+  // 8-bit tiles are half the bytes and as many instructions: twice the warps
+  // (which the registers of one block of heads allow) hide their latency
+  static constexpr int kD = D, kHeads = 8 * kNB, kTile = kTokens, kWarps = kQuant && kNB == 1 ? 16 : 8;
+  static constexpr int kKRow = D * Kv::kBytes, kVRow = DV * Kv::kBytes;  // bytes
+  static constexpr int kExtra = 0;  // shared bytes per warp beside the ring
+  static constexpr float kShift = kHalf ? 12.0f : 0.0f;
+  uint32_t qf[kNB][D / 16][2];
+  float o[kNB][DV / 16][4];
+  // per head 2c, 2c + 1 of each block (c the lane's index among four)
+  float m[kNB][2], l[kNB][2], sl2[kNB][2];
+  uint32_t vtop;  // A's bits
+  int heads;
+
+  __device__ __forceinline__ void init(uint8_t*) {}
+
+  __device__ __forceinline__ void begin(const QT* q, int nheads, float scale) {
+    const int lane = threadIdx.x & 31, c = lane & 3;
+    heads = nheads;
+    vtop = 0x00800000u;
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[b][e] = -INFINITY;
+        l[b][e] = 0.0f;
+        sl2[b][e] = scale * kLog2e;
+      }
+#pragma unroll
+      for (int j = 0; j < DV / 16; ++j) o[b][j][0] = o[b][j][1] = o[b][j][2] = o[b][j][3] = 0.0f;
+      const int h = 8 * b + (lane >> 2);
+      const bool live = h < nheads;
+      const uint32_t* row = reinterpret_cast<const uint32_t*>(q + (size_t)h * D);
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) {
+        // pairs of elements, in words of two
+        const int w0 = kQuant ? 8 * s + 2 * c : 8 * s + c;
+        qf[b][s][0] = live ? __ldg(row + w0) : 0u;
+        qf[b][s][1] = live ? __ldg(row + w0 + (kQuant ? 1 : 4)) : 0u;
+      }
+      if constexpr (kQuant) {
+        float top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 x = unpack2<QT>(qf[b][s][e]);
+            top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t ex = min(max(__float_as_uint(top) >> 23, 7u), 247u);
+        const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sl2[b][e] *= __shfl_sync(0xffffffffu, up, 8 * c + 4 * e);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 x = unpack2<QT>(qf[b][s][e]);
+            qf[b][s][e] = pack2<__half>(x.x * down, x.y * down);
+          }
+      }
+    }
+  }
+
+  // the maximum (and A) moved: what is summed so far goes by the new ones
+  __device__ __forceinline__ void rescale(const float (*s)[4], uint32_t top) {
+    top = __reduce_max_sync(0xffffffffu, top);
+    const float fa = kQuant ? __uint_as_float(vtop) * __uint_as_float(0x7f000000u - top) : 1.0f;
+    vtop = top;
+#pragma unroll
+    for (int b = 0; b < kNB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(m[b][e], fmaxf(s[b][e], s[b][2 + e]));
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        float f = mx == m[b][e] ? 1.0f : exp2_fast(m[b][e] - mx);
+        m[b][e] = mx;
+        l[b][e] *= f;
+        f *= fa;
+#pragma unroll
+        for (int j = 0; j < DV / 16; ++j) {
+          o[b][j][e] *= f;
+          o[b][j][2 + e] *= f;
+        }
+      }
+  }
+
+  __device__ __forceinline__ void tile(const TileAt& t) {
+    const int lane = threadIdx.x & 31, r = lane >> 2;
+    float s[kNB][4], s2[kNB][4];  // even and odd steps: two chains of products
+#pragma unroll
+    for (int b = 0; b < kNB; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[b][e] = s2[b][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 16; i += 2) {
+      uint32_t a0[4], a1[4];
+      if constexpr (!kQuant) {
+        ldsm4(a0, t.k + chunk_at<kKRow>(lane & 15, 2 * i + (lane >> 4)));
+        ldsm4(a1, t.k + chunk_at<kKRow>(lane & 15, 2 * i + 2 + (lane >> 4)));
+      } else {
+        uint32_t w[4];
+        ldsm4(w, t.k + chunk_at<kKRow>(lane & 15, i + (lane >> 4)));
+        widen4<false>(w[0], a0[0], a0[2], KT());
+        widen4<false>(w[1], a0[1], a0[3], KT());
+        widen4<false>(w[2], a1[0], a1[2], KT());
+        widen4<false>(w[3], a1[1], a1[3], KT());
+      }
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) {
+        mma<MT>(s[b], a0, qf[b][i][0], qf[b][i][1]);
+        mma<MT>(s2[b], a1, qf[b][i + 1][0], qf[b][i + 1][1]);
+      }
+    }
+    // scores in units of log 2; tokens that take no part get -infinity
+    const bool live0 = (t.mask >> r) & 1u, live1 = (t.mask >> (r + 8)) & 1u;
+    float k0 = 1.0f, k1 = 1.0f, v0 = 1.0f, v1 = 1.0f;
+    uint32_t top = vtop;
+    if constexpr (kQuant) {
+      k0 = t.ks[r];
+      k1 = t.ks[r + 8];
+      v0 = t.vs[r];
+      v1 = t.vs[r + 8];
+      // A: the next power of two of the largest scale, within 2^-126 .. 2^126
+      // (the scales of tokens that take no part are zeros)
+      uint32_t v = max(__float_as_uint(v0) & 0x7fffffffu, __float_as_uint(v1) & 0x7fffffffu);
+      v = v >= 0x7e800000u ? 0x7e800000u : (v + 0x7fffffu) & 0x7f800000u;
+      top = max(top, v);
+    }
+    bool moved = top != vtop;
+#pragma unroll
+    for (int b = 0; b < kNB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        s[b][e] = live0 ? (s[b][e] + s2[b][e]) * (sl2[b][e] * k0) : -INFINITY;
+        s[b][2 + e] = live1 ? (s[b][2 + e] + s2[b][2 + e]) * (sl2[b][e] * k1) : -INFINITY;
+        moved |= fmaxf(s[b][e], s[b][2 + e]) > m[b][e];
+      }
+    if (__any_sync(0xffffffffu, moved)) rescale(s, top);
+    if constexpr (kQuant) {
+      const float inv_a = __uint_as_float(0x7f000000u - vtop);
+      v0 *= inv_a;
+      v1 *= inv_a;
+    }
+    uint32_t hi[kNB][2], lo[kNB][2];
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float base = (m[b][e] == -INFINITY ? 0.0f : m[b][e]) - kShift;
+        p[e] = exp2_fast(s[b][e] - base);
+        p[2 + e] = exp2_fast(s[b][2 + e] - base);
+        l[b][e] += p[e] + p[2 + e];
+        if constexpr (kQuant) {
+          p[e] *= v0;
+          p[2 + e] *= v1;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t w = pack2<MT>(p[2 * u], p[2 * u + 1]);
+        hi[b][u] = transpose8(w);
+        if constexpr (kSplit) {
+          const float2 x = unpack2<MT>(w);
+          lo[b][u] = transpose8(pack2<MT>(p[2 * u] - x.x, p[2 * u + 1] - x.y));
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < DV / 16; j += 2) {
+      uint32_t a0[4], a1[4];
+      if constexpr (!kQuant) {
+        const int row = (lane & 7) + ((lane >> 4) << 3), ch = 2 * j + ((lane >> 3) & 1);
+        ldsm4t(a0, t.v + chunk_at<kVRow>(row, ch));
+        ldsm4t(a1, t.v + chunk_at<kVRow>(row, ch + 2));
+      } else {
+        uint32_t w[4];
+        ldsm4t(w, t.v + chunk_at<kVRow>(lane & 15, j + (lane >> 4)));
+        widen4<true>(w[0], a0[0], a0[1], KT());
+        widen4<true>(w[1], a0[2], a0[3], KT());
+        widen4<true>(w[2], a1[0], a1[1], KT());
+        widen4<true>(w[3], a1[2], a1[3], KT());
+      }
+#pragma unroll
+      for (int b = 0; b < kNB; ++b) {
+        mma<MT>(o[b][j], a0, hi[b][0], hi[b][1]);
+        mma<MT>(o[b][j + 1], a1, hi[b][0], hi[b][1]);
+        if constexpr (kSplit) {
+          mma<MT>(o[b][j], a0, lo[b][0], lo[b][1]);
+          mma<MT>(o[b][j + 1], a1, lo[b][0], lo[b][1]);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void finish(const Sink<QT>& out) {
+    const int lane = threadIdx.x & 31, c = lane & 3;
+#pragma unroll
+    for (int b = 0; b < kNB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[b][e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const int h = 8 * b + 2 * c + e;
+        if (h >= heads) continue;
+        const float mm = m[b][e] - kShift;
+        const float f = kQuant ? __uint_as_float(vtop) : 1.0f;
+        if (out.partial) {
+          if (lane < 4) *reinterpret_cast<float2*>(out.ml + 2 * h) = make_float2(mm, sum);
+          put(out.part + (size_t)h * DV, b, e, f);
+        } else {
+          if (lane < 4 && out.lse) out.lse[h] = log_sum(mm, sum);
+          put(out.out + (size_t)h * DV, b, e, f * inverse_sum(sum));
+        }
+      }
+  }
+
+  template <typename P>
+  __device__ __forceinline__ void put(P* row, int b, int e, float f) {
+    const int r = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int j = 0; j < DV / 16; ++j) {
+      const float x = o[b][j][e] * f, y = o[b][j][2 + e] * f;
+      if constexpr (kQuant) {
+        store_pair(row + 16 * j + 2 * r, x, y);
+      } else {
+        from_float(row + 16 * j + r, x);
+        from_float(row + 16 * j + r + 8, y);
+      }
+    }
+  }
+};
+
+// ----------------------------------------------------- engine: fp32 FMA
+__device__ __forceinline__ void shared4(uint32_t addr, float* f, float) {
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+               : "r"(addr)
+               : "memory");
+}
+template <typename KT>
+__device__ __forceinline__ void shared4(uint32_t addr, float* f, KT) {
+  uint32_t w, a, b;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
+  widen4<false>(w, a, b, KT());
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  f[0] = x.x;
+  f[1] = x.y;
+  f[2] = y.x;
+  f[3] = y.y;
+}
+
+// fp32 queries: scores with two lanes per token (each half of the row's
+// quads), then the weights through shared memory, each lane owning DV/32
+// columns of the accumulator.  Up to eight query heads share a tile.
+template <typename KT, int D, int DV>
+struct FmaEngine {
+  using QT = float;
+  static constexpr int kBytes = sizeof(KT);
+  static constexpr int kD = D, kHeads = 8, kTile = kTokens, kWarps = 4;
+  static constexpr int kKRow = D * kBytes, kVRow = DV * kBytes;
+  static constexpr bool kQuant = kBytes == 1;
+  static constexpr int kExtra = kHeads * (D + kTile) * 4;  // queries, weights
+  static constexpr int NC = DV / 32;                       // columns per lane
+  float* qs;  // [kHeads][D]
+  float* ps;  // [kHeads][kTile]
+  float acc[kHeads][NC];
+  float m[kHeads], l[kHeads];
+  float sl2;
+  int heads;
+
+  __device__ __forceinline__ void init(uint8_t* extra) {
+    qs = reinterpret_cast<float*>(extra);
+    ps = qs + kHeads * D;
+  }
+
+  __device__ __forceinline__ void begin(const float* q, int nheads, float scale) {
+    const int lane = threadIdx.x & 31;
+    heads = nheads;
+    sl2 = scale * kLog2e;
+    __syncwarp();
+    for (int i = lane; i < nheads * D; i += 32) qs[i] = __ldg(q + i);
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      m[h] = -INFINITY;
+      l[h] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) acc[h][i] = 0.0f;
+    }
+  }
+
+  // four values at element e of row r
+  template <int RB>
+  __device__ __forceinline__ static void load4(uint32_t base, int r, int e, float* f) {
+    const int byte = e * kBytes;
+    shared4(base + chunk_at<RB>(r, byte >> 4) + (byte & 15), f, KT());
+  }
+
+  __device__ __forceinline__ void tile(const TileAt& t) {
+    const int lane = threadIdx.x & 31, tok = lane >> 1, half = lane & 1;
+    float s[kHeads];
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) s[h] = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      const int e = 4 * (2 * i + half);
+      float k[4];
+      load4<kKRow>(t.k, tok, e, k);
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h)
+        if (h < heads) {
+          const float4 q = *reinterpret_cast<const float4*>(qs + h * D + e);
+          s[h] = fmaf(q.x, k[0], fmaf(q.y, k[1], fmaf(q.z, k[2], fmaf(q.w, k[3], s[h]))));
+        }
+    }
+    const bool live = (t.mask >> tok) & 1u;
+    const float kf = sl2 * (kQuant ? t.ks[tok] : 1.0f), vf = kQuant ? t.vs[tok] : 1.0f;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+      if (h < heads) {
+        float x = s[h] + __shfl_xor_sync(0xffffffffu, s[h], 1);
+        x = live ? x * kf : -INFINITY;
+        float mx = fmaxf(m[h], x);
+#pragma unroll
+        for (int off = 2; off < 32; off <<= 1)
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        if (mx > m[h]) {
+          const float f = exp2f(m[h] - mx);
+          l[h] *= f;
+#pragma unroll
+          for (int i = 0; i < NC; ++i) acc[h][i] *= f;
+          m[h] = mx;
+        }
+        const float p = exp2f(x - (mx == -INFINITY ? 0.0f : mx));
+        l[h] += p;
+        // a token that takes no part has zero-filled values, whatever its scale
+        if (half == 0) ps[h * kTile + tok] = live ? p * vf : 0.0f;
+      }
+    __syncwarp();
+#pragma unroll 2
+    for (int j = 0; j < kTile; j += 4) {
+      float v[4][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if constexpr (NC == 4) {
+          load4<kVRow>(t.v, j + u, 4 * lane, v[u]);
+        } else {  // two columns: this lane's half of a quad
+          float x[4];
+          load4<kVRow>(t.v, j + u, 4 * (lane >> 1), x);
+          v[u][0] = half ? x[2] : x[0];
+          v[u][1] = half ? x[3] : x[1];
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h)
+        if (h < heads) {
+          const float4 p = *reinterpret_cast<const float4*>(ps + h * kTile + j);
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+            acc[h][i] = fmaf(p.x, v[0][i],
+                             fmaf(p.y, v[1][i], fmaf(p.z, v[2][i], fmaf(p.w, v[3][i], acc[h][i]))));
+        }
+    }
+  }
+
+  __device__ __forceinline__ void finish(const Sink<float>& out) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+      if (h < heads) {
+        float sum = l[h];
+#pragma unroll
+        for (int off = 2; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const float f = out.partial ? 1.0f : inverse_sum(sum);
+        float* row = (out.partial ? out.part : out.out) + (size_t)h * DV + NC * lane;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) row[i] = acc[h][i] * f;
+        if (lane == 0) {
+          if (out.partial)
+            *reinterpret_cast<float2*>(out.ml + 2 * h) = make_float2(m[h], sum);
+          else if (out.lse)
+            out.lse[h] = log_sum(m[h], sum);
+        }
+      }
+  }
+};
+
+// ------------------------------------------------------------ first launch
+template <typename E>
+struct Ring {
+  static constexpr int kK = E::kTile * E::kKRow, kV = E::kTile * E::kVRow;
+  static constexpr int kScale = E::kQuant ? E::kTile * 4 : 0;
+  static constexpr int kStage = (kK + kV + 2 * kScale + 16 + 127) / 128 * 128;
+  // about 24 KB per warp (48 KB for the fp32 engine's four warps): with eight
+  // warps, the bytes in flight that cover the memory latency of an SM's share
+  static constexpr int kWant = 8 * 24576 / E::kWarps / kStage;
+  static constexpr int kStages = kWant < 3 ? 3 : kWant > 8 ? 8 : kWant;
+  static constexpr int kWarpBytes = kStage * kStages + (E::kExtra + 127) / 128 * 128;
+  static constexpr int kBytes = kWarpBytes * E::kWarps;
+  static_assert(kBytes <= 220 * 1024, "shared memory");
+};
+
+// a tile of a run: sequence b, unit u of it (KV head and block of query
+// heads), tile t of the unit
+struct Cursor {
+  int b, u, t;
+  Seq s;
+  __device__ __forceinline__ void next(const DecodeArgs& a, int units) {
+    if (++t < s.tiles) return;
+    t = 0;
+    if (++u < units) return;
+    u = 0;
+    while (b + 1 < a.B) {
+      s = seq_of(a, ++b);
+      if (s.tiles) return;
+    }
+  }
+};
+
+// a tile whose table entries have been asked for: lane i holds row i % kTile's
+struct Lookup {
+  int page, slot, g;
+  bool in;
+};
+
+template <typename E>
+__global__ void __launch_bounds__(E::kWarps * 32, 1)
+    lt_paged_decode_kernel(const DecodeArgs a) {
+  using R = Ring<E>;
+  using QT = typename E::QT;
+  constexpr int kThreads = E::kWarps * 32, TILE = E::kTile, S = R::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t before[kThreads];     // tiles of the sequences before this thread's
+  __shared__ int64_t warp_sum[E::kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  dependency_release();
+
+  // each thread adds a run of sequences' tiles; a scan gives the runs' starts
+  const int per = (a.B + kThreads - 1) / kThreads;
+  int64_t sum = 0;
+  for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+    const Seq s = seq_of(a, b);
+    if (s.bad && blockIdx.x == 0) report_error(a.err, kDevErrBadSeqlens);
+    sum += s.tiles;
+  }
+  int64_t scan = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, scan, off);
+    if (lane >= off) scan += x;
+  }
+  if (lane == 31) warp_sum[warp] = scan;
+  __syncthreads();
+  int64_t total = 0, mine = 0;
+#pragma unroll
+  for (int w = 0; w < E::kWarps; ++w) {
+    if (w < warp) mine += warp_sum[w];
+    total += warp_sum[w];
+  }
+  before[tid] = mine + scan - sum;
+  __syncthreads();
+
+  const int units = a.Hkv * a.nhb;
+  total *= units;
+  const int64_t run = run_length(a, total);
+  const int gw = warp * gridDim.x + blockIdx.x;  // runs spread over the SMs first
+  const int64_t start = gw * run, end = min(start + run, total);
+  if (start >= end) return;
+
+  Cursor cc;
+  {
+    int lo = 0, hi = kThreads;  // the last thread whose sequences begin at or before start
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] * units <= start)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    int64_t rem = start - before[lo] * units;
+    cc.b = lo * per;
+    cc.s = seq_of(a, cc.b);
+    while (cc.b + 1 < a.B && rem >= (int64_t)cc.s.tiles * units) {
+      rem -= (int64_t)cc.s.tiles * units;
+      cc.s = seq_of(a, ++cc.b);
+    }
+    cc.u = (int)(rem / cc.s.tiles);
+    cc.t = (int)(rem - (int64_t)cc.u * cc.s.tiles);
+  }
+  Cursor pc = cc;
+
+  uint8_t* ring = smem + warp * R::kWarpBytes;
+  const uint32_t ring_u = smem_u32(ring);
+  E eng;
+  eng.init(ring + R::kStage * S);
+
+  const int row = lane & (TILE - 1);
+  auto look = [&](const Cursor& c) {
+    Lookup p;
+    const int pos = c.s.first + c.t * TILE + row;
+    p.in = pos < c.s.len;
+    const int idx = pos / a.page_size;
+    p.slot = pos - idx * a.page_size;
+    p.page = p.in ? __ldg(a.table + (int64_t)c.b * a.table_stride + idx) : 0;
+    p.g = c.u / a.nhb;
+    return p;
+  };
+  auto issue = [&](int stage, const Lookup& p) {
+    bool live = p.in;
+    if (live && (p.page < 0 || p.page >= a.num_pages)) {
+      report_error(a.err, kDevErrBadPage);
+      live = false;
+    }
+    uint32_t mask = __ballot_sync(0xffffffffu, live);
+    if (TILE < 32) mask &= (1u << (TILE & 31)) - 1u;
+    const int64_t page = live ? p.page : 0, slot = live ? p.slot : 0;
+    const int64_t ko = page * a.kpg + slot * a.ksl + p.g * a.khd;
+    const int64_t vo = page * a.vpg + slot * a.vsl + p.g * a.vhd;
+    const uint32_t dst = ring_u + stage * R::kStage;
+    constexpr int kc = E::kKRow / 16, vc = E::kVRow / 16;  // chunks per row
+#pragma unroll
+    for (int i = 0; i < TILE * kc / 32; ++i) {
+      const int r = i * (32 / kc) + lane / kc, c = lane % kc;
+      const int64_t off = __shfl_sync(0xffffffffu, ko, r);
+      copy16(dst + chunk_at<E::kKRow>(r, c), a.k + off + c * 16, (mask >> r) & 1u);
+    }
+#pragma unroll
+    for (int i = 0; i < TILE * vc / 32; ++i) {
+      const int r = i * (32 / vc) + lane / vc, c = lane % vc;
+      const int64_t off = __shfl_sync(0xffffffffu, vo, r);
+      copy16(dst + R::kK + chunk_at<E::kVRow>(r, c), a.v + off + c * 16, (mask >> r) & 1u);
+    }
+    if constexpr (E::kQuant) {
+      const int64_t at = (page * a.Hkv + p.g) * a.page_size + slot;
+      if (lane < TILE) {
+        copy4(dst + R::kK + R::kV + lane * 4, a.ks + at, live);
+        copy4(dst + R::kK + R::kV + R::kScale + lane * 4, a.vs + at, live);
+      }
+    }
+    if (lane == 0)
+      *reinterpret_cast<uint32_t*>(ring + stage * R::kStage + R::kK + R::kV + 2 * R::kScale) = mask;
+  };
+
+  const int64_t count = end - start;
+  int64_t issued = 0;
+  Lookup pend = look(pc);
+  auto feed = [&](int stage) {
+    if (issued < count) {
+      issue(stage, pend);
+      if (++issued < count) {
+        pc.next(a, units);
+        pend = look(pc);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int s = 0; s < S - 1; ++s) feed(s);
+
+  int stage = 0, seg_t = cc.t;
+  bool first_seg = true;
+#pragma unroll 1
+  for (int64_t i = 0; i < count; ++i) {
+    if (i == 0 || cc.t == 0) {  // a new unit
+      const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
+      const int h0 = g * a.G + blk * E::kHeads;
+      eng.begin(static_cast<const QT*>(a.q) + ((size_t)cc.b * a.Hq + h0) * E::kD,
+                min(E::kHeads, a.G - blk * E::kHeads), a.scale);
+      seg_t = cc.t;
+    }
+    copy_wait<S - 2>();
+    __syncwarp();  // every lane's copies of this tile have landed, and the last tile is read
+    feed(stage == 0 ? S - 1 : stage - 1);
+    const uint8_t* st = ring + stage * R::kStage;
+    TileAt t;
+    t.k = ring_u + stage * R::kStage;
+    t.v = t.k + R::kK;
+    t.ks = reinterpret_cast<const float*>(st + R::kK + R::kV);
+    t.vs = reinterpret_cast<const float*>(st + R::kK + R::kV + R::kScale);
+    t.mask = *reinterpret_cast<const uint32_t*>(st + R::kK + R::kV + 2 * R::kScale);
+    eng.tile(t);
+    if (++stage == S) stage = 0;
+    const bool unit_done = cc.t + 1 == cc.s.tiles;
+    if (unit_done || i + 1 == count) {
+      const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
+      const int h0 = g * a.G + blk * E::kHeads;
+      Sink<QT> out;
+      out.partial = !(unit_done && seg_t == 0);
+      const size_t orow = (size_t)cc.b * a.Hq + h0;
+      out.out = static_cast<QT*>(a.out) + orow * a.dv;
+      out.lse = a.lse ? a.lse + orow : nullptr;
+      const size_t piece = (size_t)gw * 2 + (first_seg ? 0 : 1);
+      out.part = a.part + piece * a.hb * a.dv;
+      out.ml = a.ml + piece * a.hb * 2;
+      eng.finish(out);
+      first_seg = false;
+    }
+    if (i + 1 < count) cc.next(a, units);
+  }
+  copy_wait<0>();
+}
+
+template <typename E>
+cudaError_t launch_engine(const DecodeArgs& a, int sms, cudaStream_t stream) {
+  auto kern = lt_paged_decode_kernel<E>;
+  constexpr int smem = Ring<E>::kBytes;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<sms, E::kWarps * 32, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// 16-bit queries: one engine for up to 8 query heads per KV head, one for more
+template <typename QT, typename KT>
+cudaError_t launch_mma(const DecodeArgs& a, int d, int sms, cudaStream_t s) {
+  auto go = [&](auto nb) {
+    constexpr int NB = decltype(nb)::value;
+    if (d == 64)
+      return a.dv == 64 ? launch_engine<MmaEngine<QT, KT, 64, 64, NB>>(a, sms, s)
+                        : launch_engine<MmaEngine<QT, KT, 64, 128, NB>>(a, sms, s);
+    return a.dv == 64 ? launch_engine<MmaEngine<QT, KT, 128, 64, NB>>(a, sms, s)
+                      : launch_engine<MmaEngine<QT, KT, 128, 128, NB>>(a, sms, s);
+  };
+  return a.G <= 8 ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 2>());
+}
+
+template <typename KT>
+cudaError_t launch_fma(const DecodeArgs& a, int d, int sms, cudaStream_t s) {
+  if (d == 64)
+    return a.dv == 64 ? launch_engine<FmaEngine<KT, 64, 64>>(a, sms, s)
+                      : launch_engine<FmaEngine<KT, 64, 128>>(a, sms, s);
+  return a.dv == 64 ? launch_engine<FmaEngine<KT, 128, 64>>(a, sms, s)
+                    : launch_engine<FmaEngine<KT, 128, 128>>(a, sms, s);
+}
+
+// the first launch, one translation unit per query type
+cudaError_t launch_bf16(const DecodeArgs& a, lt_kv_dtype_t kv, int d, int sms, cudaStream_t s);
+cudaError_t launch_f16(const DecodeArgs& a, lt_kv_dtype_t kv, int d, int sms, cudaStream_t s);
+cudaError_t launch_f32(const DecodeArgs& a, lt_kv_dtype_t kv, int d, int sms, cudaStream_t s);
+
+}  // namespace paged
+}  // namespace lt

@@ -1,0 +1,14 @@
+// paged_attn_f32.cu -- the first decode launch for fp32 queries.
+#include "paged_attn.cuh"
+
+namespace lt {
+namespace paged {
+
+cudaError_t launch_f32(const DecodeArgs& a, lt_kv_dtype_t kv, int d, int sms, cudaStream_t s) {
+  if (kv == LT_KV_E4M3) return launch_fma<E4M3>(a, d, sms, s);
+  if (kv == LT_KV_INT8) return launch_fma<Int8>(a, d, sms, s);
+  return launch_fma<float>(a, d, sms, s);
+}
+
+}  // namespace paged
+}  // namespace lt

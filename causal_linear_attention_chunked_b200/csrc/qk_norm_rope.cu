@@ -7,15 +7,15 @@
 //               dw = sum over rows of g x r
 // R turns each pair (a, b) by A = position * inv_freq.  A reaches millions of
 // turns, so it is formed in turns and reduced in fp64; only the fraction of a
-// turn, at most 1/2, goes to fp32 sine and cosine.  They depend on the token
-// and the pair alone: a block computes them once for its tokens, in shared
-// memory, and all heads of those tokens use them.
+// turn, at most 1/2, goes to fp32 sine and cosine.
 //
-// Bound by memory (about 8 flops per 2-byte element).  A row is spread over
-// d/8 lanes so that the norm is a 3- or 4-step shuffle, and each lane holds
-// two quads of elements, 4j.. and rot/2 + 4j..: whichever way the pairs are
-// laid out, both halves of a pair are in one lane, and no value crosses lanes
-// for the rotation.  Every thread has kU rows in flight.
+// Bound by memory and, close behind, by instruction issue, so the layout is
+// chosen to need few of them: a warp takes whole tokens, and its angles stay
+// in registers for all heads.  A row is spread over d/8 lanes (the norm is a
+// 3- or 4-step shuffle); each lane holds two quads of elements, 4j.. and
+// rot/2 + 4j..: whichever way the pairs are laid out, both halves of a pair
+// are in one lane, and no value crosses lanes for the rotation.  Products run
+// two at a time (f32x2).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -28,8 +28,7 @@
 namespace lt {
 namespace {
 
-constexpr int kT = 256;   // threads
-constexpr int kMaxTB = 8; // tokens per block (sets the table of angles)
+constexpr int kT = 256, kW = kT / 32;  // threads, warps
 
 struct NormArgs {
   const void* x[2];    // q, k
@@ -42,10 +41,12 @@ struct NormArgs {
   const int32_t* positions;
   int64_t n_pos;
   const float* inv_freq;
-  int rot, tb;
+  int rot;
+  int parts;       // warps that share a token's heads
+  int per;         // forward: tokens per warp
   int64_t tokens;
   float eps;
-  int w_f32;      // gains are fp32
+  int w_f32;       // gains are fp32
   float* partial;  // backward: [block][2][d] sums of the gains' gradients
 };
 
@@ -55,254 +56,274 @@ struct GainArgs {
   int blocks, d, dtype;  // dtype of out (lt_dtype_t)
 };
 
-// positions of the block's tokens x frequencies -> cosines and sines
-// [tokens][rot/2]
-__device__ __forceinline__ void fill_angles(const NormArgs& a, int64_t t0, int nt, float* cosv,
-                                            float* sinv) {
-  const int half = a.rot >> 1;
+// A lane's place: index j in its row, row `grp` of the warp's step, and the
+// offsets of its two quads.
+template <int D>
+struct Lane {
+  static constexpr int L = D / 8, RW = 32 / L;  // lanes per row, rows per warp
+  int j, grp, qa, qb;
+  bool rotated;
+  __device__ __forceinline__ explicit Lane(int rot) {
+    const int lane = threadIdx.x & 31;
+    j = lane % L;
+    grp = lane / L;
+    rotated = j < (rot >> 3);
+    qa = rotated ? 4 * j : 8 * j;
+    qb = rotated ? (rot >> 1) + 4 * j : 8 * j + 4;
+  }
+  __device__ __forceinline__ static float row_sum(float x) {
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+  }
+};
+
+// Cosines and sines of a lane's four pairs, as the rotation's products take
+// them: halves (i, i + rot/2): c[0..1] and s[0..1] over pairs (0,1), (2,3);
+// neighbours: c[p] = (cos, cos), s[p] = (-sin, sin) of pair p.
+template <bool IL>
+struct Angles {
+  F2 c[IL ? 4 : 2], s[IL ? 4 : 2];
+};
+
+// sine and cosine of a fraction of a turn, |t| <= 1/2.  16-bit outputs: the
+// hardware functions, within 2^-21 on [-pi, pi], far below half a step of the
+// type (2^-11 at least); fp32: the accurate ones.
+template <typename T>
+__device__ __forceinline__ void sincos_turn(float t, float* s, float* c) {
+  if constexpr (sizeof(T) == 2)
+    __sincosf(6.2831853071795865f * t, s, c);
+  else
+    sincospif(2.0f * t, s, c);
+}
+
+// the token's angles: the rows of a warp's step compute a share each and
+// exchange them
+template <typename T, int D, bool IL>
+__device__ __forceinline__ void angles_of(const NormArgs& a, const Lane<D>& ln, int64_t t,
+                                          Angles<IL>& out) {
+  constexpr int L = Lane<D>::L, RW = Lane<D>::RW, SH = 4 / RW;  // a lane's share
   constexpr double kInvTwoPi = 0.15915494309189533577;
-  for (int i = threadIdx.x; i < nt * half; i += kT) {
-    const int tt = i / half, p = i - tt * half;
-    const int64_t t = t0 + tt;
-    const int pos = a.positions[a.n_pos == a.tokens ? t : t % a.n_pos];
-    double turns = (double)pos * (double)a.inv_freq[p] * kInvTwoPi;
-    turns -= rint(turns);
-    float s, c;
-    sincospif(2.0f * (float)turns, &s, &c);
-    cosv[i] = c;
-    sinv[i] = s;
+  float c[4], s[4];
+  float mc[SH], ms[SH];
+  if (ln.rotated) {
+    const int pos = __ldg(a.positions + (a.n_pos == a.tokens ? t : t % a.n_pos));
+#pragma unroll
+    for (int e = 0; e < SH; ++e) {
+      const int i = ln.grp * SH + e;  // which of the lane's four
+      const int pair = IL ? (i < 2 ? 2 * ln.j + i : (a.rot >> 2) + 2 * ln.j + i - 2)
+                          : 4 * ln.j + i;
+      double turns = (double)pos * (double)__ldg(a.inv_freq + pair) * kInvTwoPi;
+      turns -= rint(turns);
+      sincos_turn<T>((float)turns, &ms[e], &mc[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < SH; ++e) mc[e] = 1.0f, ms[e] = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = __shfl_sync(0xffffffffu, mc[i % SH], (i / SH) * L + ln.j);
+    s[i] = __shfl_sync(0xffffffffu, ms[i % SH], (i / SH) * L + ln.j);
+  }
+  if constexpr (IL) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      out.c[p] = pack_f2(c[p], c[p]);
+      out.s[p] = pack_f2(-s[p], s[p]);
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      out.c[p] = pack_f2(c[2 * p], c[2 * p + 1]);
+      out.s[p] = pack_f2(s[2 * p], s[2 * p + 1]);
+    }
   }
 }
 
-// the lane's two quads: the rotated lanes hold both halves of their pairs
-struct Lane {
-  int qa, qb;  // element offsets of the quads
-  bool rotated;
-};
-__device__ __forceinline__ Lane lane_of(int j, int rot) {
-  Lane l;
-  l.rotated = j < (rot >> 3);
-  l.qa = l.rotated ? 4 * j : 8 * j;
-  l.qb = l.rotated ? (rot >> 1) + 4 * j : 8 * j + 4;
-  return l;
-}
+__device__ __forceinline__ F2 negate2(F2 a) { return F2{a.v ^ 0x8000000080000000ull}; }
 
-// turn the lane's pairs in y[0..7] by the token's angles (sign -1: back);
-// j is the lane's index in its row
-template <bool IL>
-__device__ __forceinline__ void turn(float* y, const float* c, const float* s, int j, int rot,
-                                     float sign) {
-  if (IL) {
-    const float2 c0 = *reinterpret_cast<const float2*>(c + 2 * j);
-    const float2 s0 = *reinterpret_cast<const float2*>(s + 2 * j);
-    const float2 c1 = *reinterpret_cast<const float2*>(c + (rot >> 2) + 2 * j);
-    const float2 s1 = *reinterpret_cast<const float2*>(s + (rot >> 2) + 2 * j);
-    const float cc[4] = {c0.x, c0.y, c1.x, c1.y}, ss[4] = {s0.x, s0.y, s1.x, s1.y};
+// turn the lane's eight values y[0..3] (pairs of neighbours in registers);
+// kBack: by the negative angle
+template <bool IL, bool kBack>
+__device__ __forceinline__ void turn(F2* y, const Angles<IL>& g) {
+  if constexpr (IL) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const float A = y[2 * p], B = y[2 * p + 1], sn = sign * ss[p];
-      y[2 * p] = A * cc[p] - B * sn;
-      y[2 * p + 1] = B * cc[p] + A * sn;
-    }
+    for (int p = 0; p < 4; ++p)
+      y[p] = fma2(swap2(y[p]), kBack ? negate2(g.s[p]) : g.s[p], mul2(y[p], g.c[p]));
   } else {
-    const float4 c4 = *reinterpret_cast<const float4*>(c + 4 * j);
-    const float4 s4 = *reinterpret_cast<const float4*>(s + 4 * j);
-    const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const float A = y[p], B = y[p + 4], sn = sign * ss[p];
-      y[p] = A * cc[p] - B * sn;
-      y[p + 4] = B * cc[p] + A * sn;
+    for (int p = 0; p < 2; ++p) {
+      const F2 A = y[p], B = y[2 + p], n = negate2(g.s[p]);
+      y[p] = fma2(B, kBack ? g.s[p] : n, mul2(A, g.c[p]));
+      y[2 + p] = fma2(A, kBack ? n : g.s[p], mul2(B, g.c[p]));
     }
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void load_gain(const void* w, int w_f32, const Lane& l, float* f) {
+__device__ __forceinline__ void load_gain(const void* w, int w_f32, int qa, int qb, F2* f) {
   if (!w) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = 1.0f;
+    for (int e = 0; e < 4; ++e) f[e] = pack_f2(1.0f, 1.0f);
   } else if (w_f32) {
-    widen(load_quad(static_cast<const float*>(w) + l.qa), f);
-    widen(load_quad(static_cast<const float*>(w) + l.qb), f + 4);
+    widen2x2(load_quad(static_cast<const float*>(w) + qa), f);
+    widen2x2(load_quad(static_cast<const float*>(w) + qb), f + 2);
   } else {
-    widen(load_quad(static_cast<const T*>(w) + l.qa), f);
-    widen(load_quad(static_cast<const T*>(w) + l.qb), f + 4);
+    widen2x2(load_quad(static_cast<const T*>(w) + qa), f);
+    widen2x2(load_quad(static_cast<const T*>(w) + qb), f + 2);
   }
 }
 
-template <int L>
-__device__ __forceinline__ float row_sum(float x) {
+// sum over the lane's eight products of x and y
+__device__ __forceinline__ float dot8(const F2* x, const F2* y) {
+  F2 s = mul2(x[0], y[0]);
 #pragma unroll
-  for (int off = L / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-  return x;
+  for (int e = 1; e < 4; ++e) s = fma2(x[e], y[e], s);
+  const float2 t = unpack_f2(s);
+  return t.x + t.y;
 }
 
-// row index of a block's (token, head) list, advanced by a fixed step
-struct RowAt {
-  int tt, h, dt, dh, H;
-  __device__ __forceinline__ RowAt(int first, int step, int heads) : H(heads) {
-    tt = first / heads;
-    h = first - tt * heads;
-    dt = step / heads;
-    dh = step - dt * heads;
-  }
-  __device__ __forceinline__ void next() {
-    tt += dt;
-    h += dh;
-    if (h >= H) {
-      h -= H;
-      ++tt;
-    }
-  }
-};
+// Rows in flight per lane: with two or three blocks per SM these cover the
+// memory latency of an SM's share of the bandwidth.
+template <typename T>
+constexpr int rows_in_flight() {
+  return sizeof(T) == 2 ? 4 : 2;
+}
 
+// A token's heads are walked in batches of RW * kU, queries' then keys'; the
+// parts of a token take every parts-th batch.
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(kT) lt_norm_rope_kernel(const NormArgs a) {
-  constexpr int L = D / 8, RG = kT / L, kU = 4;
-  extern __shared__ float4 smem4[];
-  float* cosv = reinterpret_cast<float*>(smem4);
-  const int half = a.rot >> 1;
-  float* sinv = cosv + a.tb * half;
-  const int64_t t0 = (int64_t)blockIdx.x * a.tb;
-  const int nt = (int)min((int64_t)a.tb, a.tokens - t0);
-  const int grp = threadIdx.x / L, j = threadIdx.x % L;
-  const Lane ln = lane_of(j, a.rot);
-  if (half) {
-    fill_angles(a, t0, nt, cosv, sinv);
-    __syncthreads();
-  }
+__global__ void __launch_bounds__(kT, 3) lt_norm_rope_kernel(const NormArgs a) {
+  using LN = Lane<D>;
+  constexpr int kU = rows_in_flight<T>(), STEP = LN::RW * kU;
+  const LN ln(a.rot);
+  const int64_t unit = (int64_t)blockIdx.x * kW + (threadIdx.x >> 5);
+  const int64_t first = unit / a.parts * a.per;
+  const int part = (int)(unit % a.parts);
+  const int nbq = (a.H[0] + STEP - 1) / STEP, nb = nbq + (a.H[1] + STEP - 1) / STEP;
+  F2 w[2][4];
+  load_gain<T>(a.w[0], a.w_f32, ln.qa, ln.qb, w[0]);
+  load_gain<T>(a.w[1], a.w_f32, ln.qa, ln.qb, w[1]);
 #pragma unroll 1
-  for (int ph = 0; ph < 2; ++ph) {
-    const int H = a.H[ph], rows = nt * H;
-    const T* x = static_cast<const T*>(a.x[ph]) + t0 * a.stride[ph];
-    T* out = static_cast<T*>(a.out[ph]) + t0 * (int64_t)(H * D);
-    float w[8];
-    load_gain<T>(a.w[ph], a.w_f32, ln, w);
-    RowAt at(grp, RG, H);
-    // a warp's groups take as many turns as its first one, so that its
-    // shuffles stay converged; a group past the last row works on zeros
-    const int first = (threadIdx.x & ~31) / L;
+  for (int64_t t = first; t < min(first + a.per, a.tokens); ++t) {
+    Angles<IL> ang;
+    bool have = false;
 #pragma unroll 1
-    for (int r = grp, rw = first; rw < rows; r += RG * kU, rw += RG * kU) {
+    for (int b = part; b < nb; b += a.parts) {
+      const int ph = b >= nbq, H = ph ? a.H[1] : a.H[0];
+      const int h0 = (ph ? b - nbq : b) * STEP + ln.grp;
+      const T* x = static_cast<const T*>(ph ? a.x[1] : a.x[0]) +
+                   t * (ph ? a.stride[1] : a.stride[0]) + h0 * D;
+      T* out = static_cast<T*>(ph ? a.out[1] : a.out[0]) + (t * H + h0) * D;
       Quad<T> qa[kU], qb[kU];
-      int tt[kU], hh[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        tt[u] = at.tt;
-        hh[u] = at.h;
-        qa[u] = Quad<T>{};
-        qb[u] = Quad<T>{};
-        if (r + u * RG < rows) {
-          const T* p = x + (int64_t)at.tt * a.stride[ph] + at.h * D;
-          qa[u] = load_quad(p + ln.qa);
-          qb[u] = load_quad(p + ln.qb);
+        qa[u] = qb[u] = Quad<T>{};
+        if (h0 + u * LN::RW < H) {
+          qa[u] = load_quad(x + u * (LN::RW * D) + ln.qa);
+          qb[u] = load_quad(x + u * (LN::RW * D) + ln.qb);
         }
-        at.next();
+      }
+      if (!have) {  // the first rows' loads are under way
+        if (a.rot) angles_of<T, D, IL>(a, ln, t, ang);
+        have = true;
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        float y[8];
-        widen(qa[u], y);
-        widen(qb[u], y + 4);
-        float ss = 0.0f;
+        F2 y[4];
+        widen2x2(qa[u], y);
+        widen2x2(qb[u], y + 2);
+        const float rr = rsqrtf(LN::row_sum(dot8(y, y)) * (1.0f / D) + a.eps);
+        const F2 r2 = pack_f2(rr, rr);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-        const float rr = 1.0f / sqrtf(row_sum<L>(ss) * (1.0f / D) + a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = y[e] * rr * w[e];
-        if (r + u * RG < rows) {
-          if (ln.rotated) turn<IL>(y, cosv + tt[u] * half, sinv + tt[u] * half, j, a.rot, 1.0f);
-          T* p = out + (int64_t)tt[u] * (H * D) + hh[u] * D;
-          store_quad(p + ln.qa, y);
-          store_quad(p + ln.qb, y + 4);
+        for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], r2), ph ? w[1][e] : w[0][e]);
+        if (ln.rotated) turn<IL, false>(y, ang);
+        if (h0 + u * LN::RW < H) {
+          store_quad(out + u * (LN::RW * D) + ln.qa, y[0], y[1]);
+          store_quad(out + u * (LN::RW * D) + ln.qb, y[2], y[3]);
         }
       }
     }
   }
 }
 
-// One block walks token blocks blockIdx.x, + gridDim.x, ...; each thread sums
-// its eight columns' gain gradients over its rows, the block's row groups are
-// added in order at the end, and the launch below adds the blocks in order.
+// A warp walks units (token, part) in steps of the launch's warps; each lane
+// sums its eight columns' gain gradients over its rows, the block's rows of
+// lanes are added in order at the end, and the launch below adds the blocks
+// in order.
 template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(kT) lt_norm_rope_bwd_kernel(const NormArgs a) {
-  constexpr int L = D / 8, RG = kT / L, kU = 2;
-  extern __shared__ float4 smem4[];
+__global__ void __launch_bounds__(kT, 2) lt_norm_rope_bwd_kernel(const NormArgs a) {
+  using LN = Lane<D>;
+  constexpr int kU = rows_in_flight<T>(), STEP = LN::RW * kU, RG = kW * LN::RW;
   __shared__ float red[RG][D];
-  float* cosv = reinterpret_cast<float*>(smem4);
-  const int half = a.rot >> 1;
-  float* sinv = cosv + a.tb * half;
-  const int grp = threadIdx.x / L, j = threadIdx.x % L;
-  const Lane ln = lane_of(j, a.rot);
-  const int first = (threadIdx.x & ~31) / L;
-  float dw[2][8] = {};
-  for (int64_t t0 = (int64_t)blockIdx.x * a.tb; t0 < a.tokens;
-       t0 += (int64_t)gridDim.x * a.tb) {
-    const int nt = (int)min((int64_t)a.tb, a.tokens - t0);
-    if (half) {
-      __syncthreads();  // the last token block's angles are no longer read
-      fill_angles(a, t0, nt, cosv, sinv);
-      __syncthreads();
-    }
+  const LN ln(a.rot);
+  F2 w[2][4], dw[2][4];
+  load_gain<T>(a.w[0], a.w_f32, ln.qa, ln.qb, w[0]);
+  load_gain<T>(a.w[1], a.w_f32, ln.qa, ln.qb, w[1]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dw[0][e] = dw[1][e] = F2{0};
+  const int64_t units = a.tokens * a.parts;
+#pragma unroll 1
+  for (int64_t unit = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x; unit < units;
+       unit += (int64_t)gridDim.x * kW) {
+    const int64_t t = unit / a.parts;
+    const int part = (int)(unit - t * a.parts);
+    Angles<IL> ang;
+    bool have = false;
 #pragma unroll
     for (int ph = 0; ph < 2; ++ph) {
-      const int H = a.H[ph], rows = nt * H;
-      const T* x = static_cast<const T*>(a.x[ph]) + t0 * a.stride[ph];
-      const T* g = static_cast<const T*>(a.g[ph]) + t0 * (int64_t)(H * D);
-      T* out = static_cast<T*>(a.out[ph]) + t0 * a.ostride[ph];
-      float w[8];
-      load_gain<T>(a.w[ph], a.w_f32, ln, w);
-      RowAt at(grp, RG, H);
+      const int H = a.H[ph];
+      // the parts share out the batches of both phases in one count
+      const int skip = ph ? (a.H[0] + STEP - 1) / STEP % a.parts : 0;
+      const int b0 = part >= skip ? part - skip : part - skip + a.parts;
+      const T* x = static_cast<const T*>(a.x[ph]) + t * a.stride[ph];
+      const T* g = static_cast<const T*>(a.g[ph]) + t * H * D;
+      T* out = static_cast<T*>(a.out[ph]) + t * a.ostride[ph];
 #pragma unroll 1
-      for (int r = grp, rw = first; rw < rows; r += RG * kU, rw += RG * kU) {
+      for (int h0 = b0 * STEP + ln.grp, hw = b0 * STEP; hw < H;
+           h0 += a.parts * STEP, hw += a.parts * STEP) {
         Quad<T> xa[kU], xb[kU], ga[kU], gb[kU];
-        int tt[kU], hh[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          tt[u] = at.tt;
-          hh[u] = at.h;
           xa[u] = xb[u] = ga[u] = gb[u] = Quad<T>{};
-          if (r + u * RG < rows) {
-            const T* p = x + (int64_t)at.tt * a.stride[ph] + at.h * D;
-            const T* q = g + (int64_t)at.tt * (H * D) + at.h * D;
-            xa[u] = load_quad(p + ln.qa);
-            xb[u] = load_quad(p + ln.qb);
-            ga[u] = load_quad(q + ln.qa);
-            gb[u] = load_quad(q + ln.qb);
+          const int h = h0 + u * LN::RW;
+          if (h < H) {
+            xa[u] = load_quad(x + h * D + ln.qa);
+            xb[u] = load_quad(x + h * D + ln.qb);
+            ga[u] = load_quad(g + h * D + ln.qa);
+            gb[u] = load_quad(g + h * D + ln.qb);
           }
-          at.next();
+        }
+        if (!have) {
+          if (a.rot) angles_of<T, D, IL>(a, ln, t, ang);
+          have = true;
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const bool live = r + u * RG < rows;
-          float xv[8], gv[8];
-          widen(xa[u], xv);
-          widen(xb[u], xv + 4);
-          widen(ga[u], gv);
-          widen(gb[u], gv + 4);
-          if (live && ln.rotated)
-            turn<IL>(gv, cosv + tt[u] * half, sinv + tt[u] * half, j, a.rot, -1.0f);
-          float ss = 0.0f, ux = 0.0f;
+          F2 xv[4], gv[4], uv[4];
+          widen2x2(xa[u], xv);
+          widen2x2(xb[u], xv + 2);
+          widen2x2(ga[u], gv);
+          widen2x2(gb[u], gv + 2);
+          if (ln.rotated) turn<IL, true>(gv, ang);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss = fmaf(xv[e], xv[e], ss);
-            ux = fmaf(gv[e] * w[e], xv[e], ux);
-          }
-          const float rr = 1.0f / sqrtf(row_sum<L>(ss) * (1.0f / D) + a.eps);
+          for (int e = 0; e < 4; ++e) uv[e] = mul2(gv[e], w[ph][e]);
+          const float ss = LN::row_sum(dot8(xv, xv)), ux = LN::row_sum(dot8(uv, xv));
+          const float rr = rsqrtf(ss * (1.0f / D) + a.eps);
           // n = x r: dx = r (u - n mean(u n)), dw += g n
-          const float m = row_sum<L>(ux) * rr * (1.0f / D);
-          float dx[8];
+          const float m = -(ux * rr * (1.0f / D));
+          const F2 r2 = pack_f2(rr, rr), m2 = pack_f2(m, m);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float n = xv[e] * rr;
-            dx[e] = rr * (gv[e] * w[e] - n * m);
-            dw[ph][e] = fmaf(gv[e], n, dw[ph][e]);  // zeros past the last row
+          for (int e = 0; e < 4; ++e) {
+            const F2 n = mul2(xv[e], r2);
+            dw[ph][e] = fma2(gv[e], n, dw[ph][e]);  // adds zeros past the last head
+            uv[e] = mul2(r2, fma2(n, m2, uv[e]));
           }
-          if (live) {
-            T* p = out + (int64_t)tt[u] * a.ostride[ph] + hh[u] * D;
-            store_quad(p + ln.qa, dx);
-            store_quad(p + ln.qb, dx + 4);
+          const int h = h0 + u * LN::RW;
+          if (h < H) {
+            store_quad(out + h * D + ln.qa, uv[0], uv[1]);
+            store_quad(out + h * D + ln.qb, uv[2], uv[3]);
           }
         }
       }
@@ -310,13 +331,14 @@ __global__ void __launch_bounds__(kT) lt_norm_rope_bwd_kernel(const NormArgs a) 
   }
   dependency_release();
   if (!a.partial) return;
+  const int grp = (threadIdx.x >> 5) * LN::RW + ln.grp;
 #pragma unroll
   for (int ph = 0; ph < 2; ++ph) {
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      red[grp][ln.qa + e] = dw[ph][e];
-      red[grp][ln.qb + e] = dw[ph][4 + e];
+      const float2 s = unpack_f2(dw[ph][e]);
+      *reinterpret_cast<float2*>(&red[grp][(e < 2 ? ln.qa : ln.qb) + 2 * (e & 1)]) = s;
     }
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += kT) {
@@ -356,11 +378,10 @@ __global__ void __launch_bounds__(1024) lt_norm_rope_gain_kernel(const GainArgs 
 
 template <typename T, int D, bool IL>
 cudaError_t launch_t(const NormArgs& a, int blocks, bool bwd, cudaStream_t stream) {
-  const size_t smem = (size_t)a.tb * a.rot * sizeof(float);
   if (bwd)
-    lt_norm_rope_bwd_kernel<T, D, IL><<<blocks, kT, smem, stream>>>(a);
+    lt_norm_rope_bwd_kernel<T, D, IL><<<blocks, kT, 0, stream>>>(a);
   else
-    lt_norm_rope_kernel<T, D, IL><<<blocks, kT, smem, stream>>>(a);
+    lt_norm_rope_kernel<T, D, IL><<<blocks, kT, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -378,17 +399,19 @@ cudaError_t launch(const NormArgs& a, int blocks, int d, int il, bool bwd, lt_dt
                            : launch_d<float>(a, blocks, d, il, bwd, s);
 }
 
-// tokens per block
-int token_block(int64_t tokens, int sms) {
-  int tb = kMaxTB;
-  while (tb > 1 && (tokens + tb - 1) / tb < sms) tb >>= 1;
-  return tb;
+// Warps that share a token's heads: one where the tokens alone fill the
+// device's warps, more where they are few (a decode step), up to a batch of
+// rows each.
+int token_parts(int64_t tokens, int H_q, int H_kv, int d, lt_dtype_t dtype, int sms) {
+  const int step = 32 / (d / 8) * (dtype == LT_F32 ? 2 : 4);  // RW * kU
+  const int batches = (H_q + step - 1) / step + (H_kv + step - 1) / step;
+  const int64_t want = (int64_t)sms * kW / tokens;
+  return want < 1 ? 1 : want > batches ? batches : (int)want;
 }
 
-// blocks of the backward launch: two per SM, at most one per token block
-int64_t bwd_blocks(int64_t tokens, int sms) {
-  const int tb = token_block(tokens, sms);
-  const int64_t n = (tokens + tb - 1) / tb;
+// blocks of the backward launch: two per SM, at most one per eight units
+int64_t bwd_blocks(int64_t units, int sms) {
+  const int64_t n = (units + kW - 1) / kW;
   return n < 2 * sms ? n : 2 * sms;
 }
 
@@ -407,8 +430,8 @@ lt_status_t check(const void* q, const void* k, const void* qw, const void* kw,
   if (rot > 0 && (!positions || !inv_freq || n_pos < 1 || tokens % n_pos != 0))
     return LT_ERR_INVALID_ARG;
   const size_t es = dtype_size(dtype);
-  // a block index is 32 bits
-  if (tokens > (int64_t)kMaxTB * 0x7fffffff || !stride_ok(tokens, q_stride, H_q, d, es) ||
+  // (a block index is 32 bits)
+  if (tokens > (int64_t)kW * 0x7fffffff || !stride_ok(tokens, q_stride, H_q, d, es) ||
       !stride_ok(tokens, k_stride, H_kv, d, es))
     return LT_ERR_INVALID_ARG;
   if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(qw, 16) || !aligned_to(kw, 16) ||
@@ -489,20 +512,23 @@ extern "C" lt_status_t lt_qk_norm_rope(const void* q, const void* k, const void*
   a.tokens = tokens;
   a.eps = eps;
   a.w_f32 = w_dtype == LT_F32;
-  a.tb = token_block(tokens, sms);
-  const int64_t blocks = (tokens + a.tb - 1) / a.tb;
+  a.parts = token_parts(tokens, H_q, H_kv, d, dtype, sms);
+  // four tokens per warp share the loaded gains where that leaves a few waves
+  // of blocks to even out the load
+  a.per = tokens >= (int64_t)16 * sms * kW ? 4 : 1;
+  const int64_t blocks = ((tokens + a.per - 1) / a.per * a.parts + kW - 1) / kW;
   return launch(a, (int)blocks, d, interleaved, false, dtype, (cudaStream_t)stream) == cudaSuccess
              ? LT_OK
              : LT_ERR_CUDA;
 }
 
-extern "C" lt_status_t lt_qk_norm_rope_bwd_plan(int64_t tokens, int d, int num_sms,
-                                                size_t* workspace_bytes) {
-  if (!workspace_bytes || tokens < 1) return LT_ERR_INVALID_ARG;
+extern "C" lt_status_t lt_qk_norm_rope_bwd_plan(int d, int num_sms, size_t* workspace_bytes) {
+  if (!workspace_bytes) return LT_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return LT_ERR_UNSUPPORTED;
   if (num_sms <= 0) num_sms = lt::device_sm_count();
   if (num_sms <= 0) return LT_ERR_CUDA;
-  *workspace_bytes = (size_t)lt::bwd_blocks(tokens, num_sms) * 2 * d * sizeof(float);
+  // (a launch has at most two blocks per SM, however a token's heads are shared)
+  *workspace_bytes = (size_t)2 * num_sms * 2 * d * sizeof(float);
   return LT_OK;
 }
 
@@ -550,11 +576,12 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
     return LT_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return LT_ERR_CUDA;
-  const int64_t blocks = bwd_blocks(tokens, sms);
+  const int parts = token_parts(tokens, H_q, H_kv, d, dtype, sms);
+  const int64_t blocks = bwd_blocks(tokens * parts, sms);
   Workspace w;
   if (gains) {
     const lt_status_t sw = w.take(workspace, workspace_bytes,
-                                  (size_t)blocks * 2 * d * sizeof(float), (cudaStream_t)stream);
+                                  (size_t)2 * sms * 2 * d * sizeof(float), (cudaStream_t)stream);
     if (sw != LT_OK) return sw;
   }
   NormArgs a = {};
@@ -579,7 +606,7 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
   a.tokens = tokens;
   a.eps = eps;
   a.w_f32 = w_dtype == LT_F32;
-  a.tb = token_block(tokens, sms);
+  a.parts = parts;
   a.partial = static_cast<float*>(w.p);
   cudaError_t e = launch(a, (int)blocks, d, interleaved, true, dtype, (cudaStream_t)stream);
   if (e == cudaSuccess && gains) {

@@ -14,39 +14,45 @@ Calls run on the tensors' device and, unless ``stream`` is given, on its
 current stream.  Tensors that a call allocates (outputs, workspace) belong to
 the stream that it runs on.
 """
-import contextlib
 import ctypes
 import math
 
 import torch
 
-from ._binding import KvCacheStruct, _check, _dtype_code, _ptr, lib
+from ._binding import KvCacheStruct, _check, lib
 
+_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # lt_dtype_t
 _KV_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.float8_e4m3fn: 3,
              torch.int8: 4}
-_NO_CTX = contextlib.nullcontext()
-_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+_raw_stream = torch._C._cuda_getCurrentRawStream   # a device's current stream, as a handle
+_current_device = torch._C._cuda_getDevice
 
 
-class _On:
-    """The device and stream of a call: entered around its allocations and
-    launch where they are not the current ones already."""
+def _elsewhere(dev, stream, tensors):
+    """None where the call can be made as it stands: every tensor on CUDA device
+    `dev`, the current one, and no stream named.  Else the context to make it
+    in, so that its allocations belong to the stream that it runs on."""
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    if stream is not None:
+        if stream.device_index != dev:
+            raise ValueError("stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    return None if _current_device() == dev else torch.cuda.device(dev)
 
-    def __init__(self, device, stream, *tensors):
-        if device.type != "cuda":
-            raise ValueError("the tensors must be CUDA tensors")
-        for t in tensors:
-            if t is not None and t.device != device:
-                raise ValueError("all tensors must be on one device")
-        if stream is None:
-            self.handle = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-            self.ctx = _NO_CTX if torch.cuda.current_device() == device.index \
-                else torch.cuda.device(device)
-        else:
-            if stream.device != device:
-                raise ValueError("stream belongs to another device than the tensors")
-            self.handle = ctypes.c_void_p(stream.cuda_stream)
-            self.ctx = torch.cuda.stream(stream)
+
+def _dtype_code(t):
+    code = _CODES.get(t)
+    if code is None:
+        raise TypeError("unsupported dtype %s (bfloat16, float16 or float32)" % t)
+    return code
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _int32(t, name, dim):
@@ -58,26 +64,25 @@ def _int32(t, name, dim):
 def _tokens(t, name):
     """(tokens, heads, width, token stride) of [.., heads, width]: heads and
     width contiguous, tokens evenly spaced."""
-    if t.dim() not in (3, 4):
-        raise ValueError("%s must be [tokens, heads, width] or [B, N, heads, width]" % name)
-    H, w = t.shape[-2:]
-    if (w > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != w):
-        raise ValueError("%s must be contiguous in its heads and width" % name)
-    if t.dim() == 3:
-        n, step = t.shape[0], t.stride(0)
-    else:
-        B, N = t.shape[:2]
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        n, H, w = shape
+        step = stride[0]
+    elif len(shape) == 4:
+        B, N, H, w = shape
         n = B * N
-        step = t.stride(1) if N > 1 else t.stride(0)
-        if B > 1 and N > 1 and t.stride(0) != N * step:
+        step = stride[1] if N > 1 else stride[0]
+        if B > 1 and N > 1 and stride[0] != N * step:
             raise ValueError("%s must have evenly spaced tokens" % name)
+    else:
+        raise ValueError("%s must be [tokens, heads, width] or [B, N, heads, width]" % name)
+    if (w > 1 and stride[-1] != 1) or (H > 1 and stride[-2] != w):
+        raise ValueError("%s must be contiguous in its heads and width" % name)
     return n, H, w, step if n > 1 else H * w
 
 
-def _out(t, shape, dtype, device, name):
-    """A given output, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _given(t, shape, dtype, name):
+    """Checks an output that the caller passed."""
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s"
                          % (name, dtype, tuple(shape)))
@@ -89,16 +94,20 @@ def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
     nk, Hkv, dk, k_step = _tokens(k, "k")
     if nk != n or dk != d or q.shape[:-2] != k.shape[:-2]:
         raise ValueError("q and k must have the same tokens and width")
-    if k.dtype != q.dtype or q.dtype not in _FLOATS:
-        raise TypeError("q and k must have one dtype (bfloat16, float16 or float32)")
-    w_dtype = q.dtype
-    given = [w for w in (q_weight, k_weight) if w is not None]
-    for w in given:
-        w_dtype = given[0].dtype
-        if w.shape != (d,) or not w.is_contiguous() or w.dtype != w_dtype or \
-                w_dtype not in (torch.float32, q.dtype):
-            raise ValueError("weights must be contiguous [d] tensors, both float32 or both of "
-                             "q's dtype")
+    dtype = q.dtype
+    if k.dtype != dtype:
+        raise TypeError("q and k must have one dtype")
+    code = w_code = _dtype_code(dtype)
+    w_dtype = None
+    for w in (q_weight, k_weight):
+        if w is not None:
+            if w_dtype is None:
+                w_dtype = w.dtype
+            if w.shape != (d,) or not w.is_contiguous() or w.dtype != w_dtype or \
+                    w_dtype not in (dtype, torch.float32):
+                raise ValueError("weights must be contiguous [d] tensors, both float32 or both "
+                                 "of q's dtype")
+            w_code = _CODES[w_dtype]
     n_pos = rot = 0
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq are given together")
@@ -108,11 +117,9 @@ def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise TypeError("inv_freq must be a contiguous float32 vector")
         n_pos, rot = positions.numel(), 2 * inv_freq.numel()
-        if rot and (n_pos == 0 or n % n_pos):
-            raise ValueError("the number of tokens must be a multiple of the positions'")
-        if rot and q.dim() == 4 and n_pos not in (q.shape[1], n):
-            raise ValueError("positions must be [N] or [B, N]")
-    return n, Hq, Hkv, d, q_step, k_step, w_dtype, n_pos, rot
+        if rot and n_pos != n and (q.dim() != 4 or n_pos != q.shape[1]):
+            raise ValueError("positions must be one per token, or [N] for a [B, N] batch")
+    return n, Hq, Hkv, d, q_step, k_step, code, w_code, n_pos, rot
 
 
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, eps=1e-6,
@@ -123,21 +130,24 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
     q [.., H_q, d], k [.., H_kv, d] with leading [B, N] or [tokens]; slices of
     a fused projection are taken as they are (evenly spaced tokens).
     q_weight, k_weight: [d] gains (float32 or q's dtype) or None.  positions:
-    int32, one per token, or [N] shared by a dense batch; inv_freq: float32
+    int32, one per token, or [N] shared by a [B, N] batch; inv_freq: float32
     [rot / 2] angles per position (rot values of each head are rotated, a
     multiple of 8); both None: the norm alone.  interleaved: pairs (2i, 2i + 1)
     instead of (i, i + rot / 2).  See lt_qk_norm_rope."""
-    n, Hq, Hkv, d, q_step, k_step, w_dtype, n_pos, rot = _norm_args(q, k, q_weight, k_weight,
-                                                                    positions, inv_freq)
-    on = _On(q.device, stream, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
-    with on.ctx:
-        q_out = _out(q_out, q.shape, q.dtype, q.device, "q_out")
-        k_out = _out(k_out, k.shape, q.dtype, q.device, "k_out")
-        _check(lib.lt_qk_norm_rope(
-            q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions), n_pos,
-            _ptr(inv_freq), rot, int(bool(interleaved)), q_out.data_ptr(), k_out.data_ptr(), n, Hq,
-            Hkv, d, q_step, k_step, float(eps), on.handle, _dtype_code(q.dtype),
-            _dtype_code(w_dtype)))
+    n, Hq, Hkv, d, q_step, k_step, code, w_code, n_pos, rot = _norm_args(q, k, q_weight, k_weight,
+                                                                         positions, inv_freq)
+    dev = q.get_device()
+    ctx = _elsewhere(dev, stream, (k, q_weight, k_weight, positions, inv_freq, q_out, k_out))
+    if ctx is not None:
+        with ctx:
+            return qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved,
+                                q_out, k_out)
+    q_out = q.new_empty(q.shape) if q_out is None else _given(q_out, q.shape, q.dtype, "q_out")
+    k_out = k.new_empty(k.shape) if k_out is None else _given(k_out, k.shape, q.dtype, "k_out")
+    _check(lib.lt_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions), n_pos,
+        _ptr(inv_freq), rot, 1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), n, Hq,
+        Hkv, d, q_step, k_step, eps, _raw_stream(dev), code, w_code))
     return q_out, k_out
 
 
@@ -147,39 +157,45 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positio
     gradients dq_out, dk_out; the weights' are None where a weight is None.
     dq and dk may be given as slices of a fused gradient.  See
     lt_qk_norm_rope_bwd."""
-    n, Hq, Hkv, d, q_step, k_step, w_dtype, n_pos, rot = _norm_args(q, k, q_weight, k_weight,
-                                                                    positions, inv_freq)
+    n, Hq, Hkv, d, q_step, k_step, code, w_code, n_pos, rot = _norm_args(q, k, q_weight, k_weight,
+                                                                         positions, inv_freq)
     for g, x, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
-        if g.shape != x.shape or g.dtype != q.dtype or not g.is_contiguous():
+        if g.shape != x.shape or g.dtype != x.dtype or not g.is_contiguous():
             raise ValueError("%s must be contiguous, of its input's shape and dtype" % name)
-    on = _On(q.device, stream, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, dq, dk)
-    with on.ctx:
-        steps = []
-        grads = []
-        for t, x, H, name in ((dq, q, Hq, "dq"), (dk, k, Hkv, "dk")):
-            if t is None:
-                t = torch.empty(x.shape, dtype=q.dtype, device=q.device)
-                steps.append(H * d)
-            else:
-                if t.shape != x.shape or t.dtype != q.dtype:
-                    raise ValueError("%s must have its input's shape and dtype" % name)
-                steps.append(_tokens(t, name)[3])
-            grads.append(t)
-        dqw = torch.empty_like(q_weight) if q_weight is not None else None
-        dkw = torch.empty_like(k_weight) if k_weight is not None else None
-        ws, ws_bytes = None, 0
-        if dqw is not None or dkw is not None:
-            need = ctypes.c_size_t()
-            _check(lib.lt_qk_norm_rope_bwd_plan(n, d, 0, ctypes.byref(need)))
-            ws_bytes = need.value
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        _check(lib.lt_qk_norm_rope_bwd(
-            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _ptr(q_weight),
-            _ptr(k_weight), _ptr(positions), n_pos, _ptr(inv_freq), rot, int(bool(interleaved)),
-            grads[0].data_ptr(), grads[1].data_ptr(), _ptr(dqw), _ptr(dkw), n, Hq, Hkv, d, q_step,
-            k_step, steps[0], steps[1], float(eps), _ptr(ws), ws_bytes, on.handle,
-            _dtype_code(q.dtype), _dtype_code(w_dtype)))
-    return grads[0], grads[1], dqw, dkw
+    dev = q.get_device()
+    ctx = _elsewhere(dev, stream, (k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, dq,
+                                   dk))
+    if ctx is not None:
+        with ctx:
+            return qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq,
+                                    eps, interleaved, dq, dk)
+    dq_step, dk_step = Hq * d, Hkv * d
+    if dq is None:
+        dq = q.new_empty(q.shape)
+    elif dq.shape != q.shape or dq.dtype != q.dtype:
+        raise ValueError("dq must have q's shape and dtype")
+    else:
+        dq_step = _tokens(dq, "dq")[3]
+    if dk is None:
+        dk = k.new_empty(k.shape)
+    elif dk.shape != k.shape or dk.dtype != q.dtype:
+        raise ValueError("dk must have k's shape and dtype")
+    else:
+        dk_step = _tokens(dk, "dk")[3]
+    dqw = torch.empty_like(q_weight) if q_weight is not None else None
+    dkw = torch.empty_like(k_weight) if k_weight is not None else None
+    ws, ws_bytes = None, 0
+    if dqw is not None or dkw is not None:
+        need = ctypes.c_size_t()
+        _check(lib.lt_qk_norm_rope_bwd_plan(d, 0, need))
+        ws_bytes = need.value
+        ws = q.new_empty(ws_bytes, dtype=torch.uint8)
+    _check(lib.lt_qk_norm_rope_bwd(
+        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _ptr(q_weight),
+        _ptr(k_weight), _ptr(positions), n_pos, _ptr(inv_freq), rot, 1 if interleaved else 0,
+        dq.data_ptr(), dk.data_ptr(), _ptr(dqw), _ptr(dkw), n, Hq, Hkv, d, q_step, k_step, dq_step,
+        dk_step, eps, _ptr(ws), ws_bytes, _raw_stream(dev), code, w_code))
+    return dq, dk, dqw, dkw
 
 
 class PagedKVCache:
@@ -215,7 +231,7 @@ class PagedKVCache:
             if t is not None and t.device != k.device:
                 raise ValueError("all tensors must be on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self._dev = k.dtype, k.device, k.get_device()
         self.num_pages, self.page_size, self.H_kv, self.d, self.dv = pages, page_size, H, d, \
             v.shape[3]
         self._c = KvCacheStruct(
@@ -225,6 +241,16 @@ class PagedKVCache:
             _KV_CODES[k.dtype])
         self._ref = ctypes.byref(self._c)
         self._workspace_bytes = {}
+
+    def _workspace(self, Hq, code):
+        """Workspace bytes of paged_attn_decode for Hq query heads of dtype `code`."""
+        n = self._workspace_bytes.get((Hq, code))
+        if n is None:
+            need = ctypes.c_size_t()
+            _check(lib.lt_paged_attn_decode_plan(Hq, self.H_kv, self.d, self.dv, code,
+                                                 _KV_CODES[self.dtype], 0, need))
+            n = self._workspace_bytes[(Hq, code)] = need.value
+        return n
 
     @classmethod
     def empty(cls, num_pages, page_size, H_kv, d, dv=None, dtype=torch.bfloat16, device="cuda"):
@@ -252,10 +278,12 @@ def kv_cache_write(cache, k, v, slots, stream=None):
         raise TypeError("k and v must have one dtype")
     if slots.dtype != torch.int32 or not slots.is_contiguous() or slots.numel() != n:
         raise TypeError("slots must be a contiguous int32 tensor, one per token")
-    on = _On(cache.device, stream, k, v, slots)
-    with on.ctx:
-        _check(lib.lt_kv_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), slots.data_ptr(), n,
-                                     k_step, v_step, on.handle, _dtype_code(k.dtype)))
+    ctx = _elsewhere(cache._dev, stream, (k, v, slots))
+    if ctx is not None:
+        with ctx:
+            return kv_cache_write(cache, k, v, slots)
+    _check(lib.lt_kv_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), slots.data_ptr(), n,
+                                 k_step, v_step, _raw_stream(cache._dev), _dtype_code(k.dtype)))
 
 
 def kv_cache_read(cache, block_table, cu_seqlens, N, dtype=None, k_out=None, v_out=None,
@@ -272,16 +300,21 @@ def kv_cache_read(cache, block_table, cu_seqlens, N, dtype=None, k_out=None, v_o
     if block_table.shape[0] != B:
         raise ValueError("block_table must have a row per sequence")
     if dtype is None:
-        dtype = cache.dtype if cache.dtype in _FLOATS else torch.bfloat16
-    on = _On(cache.device, stream, block_table, cu_seqlens, k_out, v_out)
-    with on.ctx:
-        k_out = _out(k_out, (N, cache.H_kv, cache.d), dtype, cache.device, "k_out")
-        v_out = _out(v_out, (N, cache.H_kv, cache.dv), dtype, cache.device, "v_out")
-        pages = block_table.shape[1]
-        _check(lib.lt_kv_cache_read(cache._ref, block_table.data_ptr(),
-                                    block_table.stride(0) if B > 1 else pages, pages,
-                                    cu_seqlens.data_ptr(), B, N, k_out.data_ptr(),
-                                    v_out.data_ptr(), on.handle, _dtype_code(dtype)))
+        dtype = cache.dtype if cache.dtype in _CODES else torch.bfloat16
+    ctx = _elsewhere(cache._dev, stream, (block_table, cu_seqlens, k_out, v_out))
+    if ctx is not None:
+        with ctx:
+            return kv_cache_read(cache, block_table, cu_seqlens, N, dtype, k_out, v_out)
+    k_shape, v_shape = (N, cache.H_kv, cache.d), (N, cache.H_kv, cache.dv)
+    k_out = cache.k.new_empty(k_shape, dtype=dtype) if k_out is None \
+        else _given(k_out, k_shape, dtype, "k_out")
+    v_out = cache.k.new_empty(v_shape, dtype=dtype) if v_out is None \
+        else _given(v_out, v_shape, dtype, "v_out")
+    pages = block_table.shape[1]
+    _check(lib.lt_kv_cache_read(cache._ref, block_table.data_ptr(),
+                                block_table.stride(0) if B > 1 else pages, pages,
+                                cu_seqlens.data_ptr(), B, N, k_out.data_ptr(), v_out.data_ptr(),
+                                _raw_stream(cache._dev), _dtype_code(dtype)))
     return k_out, v_out
 
 
@@ -304,21 +337,21 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
     if block_table.shape[0] != B or seq_lens.numel() != B:
         raise ValueError("block_table and seq_lens must have a row per sequence")
     code = _dtype_code(q.dtype)
-    on = _On(cache.device, stream, q, block_table, seq_lens, out)
-    with on.ctx:
-        out = _out(out, (B, Hq, cache.dv), q.dtype, q.device, "out")
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-        ws_bytes = cache._workspace_bytes.get((Hq, code))
-        if ws_bytes is None:
-            need = ctypes.c_size_t()
-            _check(lib.lt_paged_attn_decode_plan(Hq, cache.H_kv, d, cache.dv, code,
-                                                 _KV_CODES[cache.dtype], 0, ctypes.byref(need)))
-            ws_bytes = cache._workspace_bytes[(Hq, code)] = need.value
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        pages = block_table.shape[1]
-        _check(lib.lt_paged_attn_decode(
-            q.data_ptr(), cache._ref, block_table.data_ptr(),
-            block_table.stride(0) if B > 1 else pages, pages, seq_lens.data_ptr(), B, Hq,
-            1.0 / math.sqrt(d) if scale is None else float(scale), int(window), out.data_ptr(),
-            _ptr(lse), ws.data_ptr(), ws_bytes, on.handle, code))
+    dev = cache._dev
+    ctx = _elsewhere(dev, stream, (q, block_table, seq_lens, out))
+    if ctx is not None:
+        with ctx:
+            return paged_attn_decode(q, cache, block_table, seq_lens, scale, window, out,
+                                     return_lse)
+    out = q.new_empty((B, Hq, cache.dv)) if out is None \
+        else _given(out, (B, Hq, cache.dv), q.dtype, "out")
+    lse = q.new_empty((B, Hq), dtype=torch.float32) if return_lse else None
+    ws_bytes = cache._workspace(Hq, code)
+    ws = q.new_empty(ws_bytes, dtype=torch.uint8)
+    pages = block_table.shape[1]
+    _check(lib.lt_paged_attn_decode(
+        q.data_ptr(), cache._ref, block_table.data_ptr(),
+        block_table.stride(0) if B > 1 else pages, pages, seq_lens.data_ptr(), B, Hq,
+        1.0 / math.sqrt(d) if scale is None else scale, window, out.data_ptr(), _ptr(lse),
+        ws.data_ptr(), ws_bytes, _raw_stream(dev), code))
     return (out, lse) if return_lse else out

@@ -455,8 +455,7 @@ LT_API lt_status_t lt_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, c
 
 /* Workspace bytes of lt_qk_norm_rope_bwd on a device with num_sms SMs (<= 0:
  * the current device).  Host arithmetic only. */
-LT_API lt_status_t lt_qk_norm_rope_bwd_plan(int64_t tokens, int d, int num_sms,
-                                            size_t *workspace_bytes);
+LT_API lt_status_t lt_qk_norm_rope_bwd_plan(int d, int num_sms, size_t *workspace_bytes);
 
 /*
  * A paged key-value cache for softmax layers: the cache of the pages'

@@ -54,28 +54,30 @@ def pair_size(y, rot, interleaved):
 def norm_rope(x, w, positions, inv_freq, eps, interleaved):
     """(value, bound without the last rounding) of x [T, H, d].
 
-    fp32 errors, relative to the pair's size: the sum of squares is at most 7
-    fused steps and 4 shuffles (11 U32, halved by the root), the root, the
-    division, two products (4), cosine and sine (the reduced angle in fp32, 2
-    pi 2^-25 < 4 U32, and 2 steps of the functions, 4), two more products and a
-    sum (3): under 24 U32."""
+    fp32 errors, in U32 of the pair's size: the sum of squares is at most 5
+    fused steps and 5 sums (10, halved by the root), the root's reciprocal 2
+    steps (4), mean and eps (1), two products (2); the reduced angle in fp32, 2
+    pi 2^-26 and its product by 2 pi (3 + 4); sine and cosine 2 steps for fp32
+    (4), 2^-21.2 absolute for the 16-bit types (7); two products and a sum (3).
+    In all under 30."""
     x = x.double()
     d = x.shape[-1]
     w = torch.ones(d, dtype=torch.float64) if w is None else w.double()
     y = x / torch.sqrt(x.square().mean(-1, keepdim=True) + eps) * w
     y = rotate(y, positions, inv_freq, interleaved)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    return y, 24 * U32 * pair_size(y, rot, interleaved)
+    return y, 30 * U32 * pair_size(y, rot, interleaved)
 
 
 def norm_rope_bwd(g, x, w, positions, inv_freq, eps, interleaved, adds=256):
     """((dx, bound), (dw, bound)).
 
-    dx = r (u - n m): u carries the rotation's and the gain's errors (16 U32 of
-    the pair's size), n those of the norm (12), m a sum of d products (11 adds
-    and what its terms carry: 40 U32 of mean|u n|); r again 12.  dw: each term
-    carries 30 U32 of its size, and a sum with at most `adds` roundings in a
-    row."""
+    dx = r (u - n m): u carries the rotation's and the gain's errors (19 U32 of
+    the pair's size), n and r those of the norm (12), m a sum of d products (10
+    and what its terms carry: 45 U32 of mean|u n|); so the first term 19 + 12 +
+    1, the second 12 + 45 + 12 + 3.  dw: each term carries 19 + 12 + 1 U32 of its
+    size, and a sum with at most `adds` roundings in a row (a lane's rows, the
+    block's 32 rows of lanes, the blocks)."""
     g, x = g.double(), x.double()
     d = x.shape[-1]
     w1 = torch.ones(d, dtype=torch.float64) if w is None else w.double()
@@ -89,7 +91,7 @@ def norm_rope_bwd(g, x, w, positions, inv_freq, eps, interleaved, adds=256):
     dx = r * (u - n * m)
     dx_bound = r * U32 * (32 * size * w1.abs() + 80 * n.abs() * m_size)
     dw = (g * n).sum((0, 1))
-    dw_bound = (30 + adds) * U32 * (size * n.abs()).sum((0, 1))
+    dw_bound = (32 + adds) * U32 * (size * n.abs()).sum((0, 1))
     return (dx, dx_bound), (dw, dw_bound)
 
 
@@ -130,9 +132,11 @@ def decode(q, k_pool, v_pool, k_scale, v_scale, table, lens, page_size, scale, w
     exponential 2^-22; 8-bit caches take q in fp16 relative to the head's
     largest entry, 2^-25 of it.  That moves every weight by a factor within
     e^delta, the quotient by 2 delta W.  The weights for the tensor cores are
-    rounded by half a step of their type (none for fp32 queries), sums over n
-    keys by n U32 of W, and weights under 2^-26 of the largest lose at most
-    2^-37 each against the largest value row."""
+    two terms of the cache's 16-bit type, so half a step of it squared (2^-16,
+    2^-22); for 8-bit caches fp16, one term for bf16 queries (2^-11), two for
+    fp16; fp32 queries keep fp32.  Sums over n keys round by n U32 of W, and
+    weights under 2^-26 of the largest lose at most 2^-37 each against the
+    largest value row."""
     B, Hq, d = q.shape
     Hkv, dv = k_pool.shape[2], v_pool.shape[3]
     out = torch.zeros(B, Hq, dv, dtype=torch.float64)
@@ -141,7 +145,7 @@ def decode(q, k_pool, v_pool, k_scale, v_scale, table, lens, page_size, scale, w
     lse_bound = torch.zeros(B, Hq, dtype=torch.float64)
     quant = k_scale is not None
     weight = 0.0 if q.dtype == torch.float32 else \
-        2.0 ** -11 if quant else half_step(q.dtype)
+        2.0 ** -11 if quant and q.dtype == torch.bfloat16 else half_step(q.dtype) ** 2
     for b in range(B):
         n = int(lens[b])
         K = rows_of(k_pool, k_scale, table[b], n, page_size)

@@ -158,13 +158,11 @@ def test_plans():
                      ((0, 8, 128, 128, 1, 1, 148), 1)):
         assert lib.lt_paged_attn_decode_plan(*args, ctypes.byref(n)) == st
     assert lib.lt_paged_attn_decode_plan(32, 8, 128, 128, 1, 1, 148, None) == 1
-    assert lib.lt_qk_norm_rope_bwd_plan(100000, 128, 148, ctypes.byref(n)) == 0
-    most = n.value
-    assert most % (2 * 128 * 4) == 0
-    assert lib.lt_qk_norm_rope_bwd_plan(1, 128, 148, ctypes.byref(n)) == 0
-    assert n.value == 2 * 128 * 4  # one block
-    assert lib.lt_qk_norm_rope_bwd_plan(0, 128, 148, ctypes.byref(n)) == 1
-    assert lib.lt_qk_norm_rope_bwd_plan(8, 80, 148, ctypes.byref(n)) == 2
+    # one row of sums per block, at most two blocks per SM; tokens do not count
+    assert lib.lt_qk_norm_rope_bwd_plan(128, 148, ctypes.byref(n)) == 0
+    assert n.value == 2 * 148 * 2 * 128 * 4
+    assert lib.lt_qk_norm_rope_bwd_plan(80, 148, ctypes.byref(n)) == 2
+    assert lib.lt_qk_norm_rope_bwd_plan(64, 148, None) == 1
 
 
 def test_token_layouts():
