@@ -31,5 +31,6 @@ def __getattr__(name):
         return getattr(_binding, name)
     if name in _CACHE_API:
         from . import kv_cache
-        return getattr(kv_cache, name)
+        globals()[name] = getattr(kv_cache, name)  # found at once from now on
+        return globals()[name]
     raise AttributeError(name)

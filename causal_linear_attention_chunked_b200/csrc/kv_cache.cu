@@ -260,7 +260,7 @@ __device__ __forceinline__ Place place_of_row(const CacheArgs& a, int t) {
       hi = mid;
   }
   const int begin = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1);
-  if (begin >= 0 && t >= begin && t < end &&
+  if (begin >= 0 && t >= begin && t < end && end <= a.N &&
       (int64_t)end - begin <= (int64_t)a.max_pages * a.page_size) {
     const int i = t - begin, n = i / a.page_size;
     const int page = __ldg(a.table + (int64_t)lo * a.table_stride + n);

@@ -7,23 +7,11 @@ namespace lt {
 namespace paged {
 namespace {
 
-// One block per (query head, sequence): nothing to do where one warp had the
-// whole pair; else its pieces, weighted by exp2(their maximum - the largest)
-// and added in run order.  A piece is read four columns per lane, and the
-// block's groups of lanes take the pieces in turn.
+// Block (x, h): head h of the unit that begins in block x of the first launch
+// and goes on in others, if there is one.  Its pieces are weighted by
+// exp2(their maximum - the largest) and added in the order of the blocks:
+// four columns per lane, groups of lanes taking the pieces in turn.
 constexpr int kJoin = 256;
-
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* red) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  int64_t s = 0;
-#pragma unroll
-  for (int w = 0; w < kJoin / 32; ++w) s += red[w];
-  return s;
-}
 
 template <typename T>
 __device__ __forceinline__ void store4(void* out, size_t at, const float* f) {
@@ -31,37 +19,20 @@ __device__ __forceinline__ void store4(void* out, size_t at, const float* f) {
 }
 
 __global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const DecodeArgs a) {
-  __shared__ int64_t red[kJoin / 32];
   __shared__ float fred[kJoin / 32];
   __shared__ float4 acc_s[kJoin];
   __shared__ float l_s[kJoin];
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  int64_t all = 0, pre = 0;
-  for (int i = tid; i < a.B; i += kJoin) {
-    const int n = seq_of(a, i).tiles;
-    all += n;
-    if (i < b) pre += n;
-  }
-  all = block_sum(all, red);
-  pre = block_sum(pre, red);
-  const Seq s = seq_of(a, b);
-  const int units = a.Hkv * a.nhb;
-  const int g = h / a.G, hh = h - g * a.G, blk = hh / a.hb, r = hh - blk * a.hb;
-  const int64_t run = run_length(a, all * units);
-  const int64_t from = pre * units + (int64_t)(g * a.nhb + blk) * s.tiles;
-  const int64_t w0 = from / run, w1 = s.tiles ? (from + s.tiles - 1) / run : w0;
+  const int x = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   // every block waits, so that this launch ends after the first one has
   dependency_wait();
-  if (s.bad || (s.tiles && w0 == w1)) return;
-  const size_t orow = (size_t)b * a.Hq + h;
+  const Shared s = a.shared[x];
+  const int n = s.blocks, g = s.u / a.nhb, blk = s.u - g * a.nhb;
+  if (n == 0 || h >= a.G - blk * a.hb) return;
   const int lanes = a.dv >> 2, groups = kJoin / lanes, c4 = tid % lanes, grp = tid / lanes;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float l = 0.0f, mx = -INFINITY;
-  const int n = s.tiles ? (int)(w1 - w0 + 1) : 0;
-  // piece i of the pair: slot 1 only of a warp that began with another pair
-  const size_t row0 = (size_t)(w0 * 2 + (from > w0 * run ? 1 : 0)) * a.hb + r;
-  auto row = [&](int i) { return i == 0 ? row0 : (size_t)(w0 + i) * 2 * a.hb + r; };
-  for (int i = tid; i < n; i += kJoin) mx = fmaxf(mx, a.ml[row(i) * 2]);
+  // the first piece is the second of its block, the others the first of theirs
+  auto row = [&](int i) { return ((size_t)(x + i) * 2 + (i == 0 ? 1 : 0)) * a.hb + h; };
+  float mx = -INFINITY;
+  for (int i = tid; i < n; i += kJoin) mx = fmaxf(mx, a.block.ml[row(i) * 2]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
   if ((tid & 31) == 0) fred[tid >> 5] = mx;
@@ -69,32 +40,29 @@ __global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const DecodeArgs a
 #pragma unroll
   for (int w = 0; w < kJoin / 32; ++w) mx = fmaxf(mx, fred[w]);
   const float base = mx == -INFINITY ? 0.0f : mx;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float l = 0.0f;
 #pragma unroll 4
   for (int i = grp; i < n; i += groups) {
     const size_t p = row(i);
-    const float2 ml = *reinterpret_cast<const float2*>(a.ml + p * 2);
-    const float4 x = *reinterpret_cast<const float4*>(a.part + p * a.dv + c4 * 4);
-    const float f = exp2f(ml.x - base);
-    l = fmaf(f, ml.y, l);
-    o.x = fmaf(f, x.x, o.x);
-    o.y = fmaf(f, x.y, o.y);
-    o.z = fmaf(f, x.z, o.z);
-    o.w = fmaf(f, x.w, o.w);
+    add_piece(o, l, *reinterpret_cast<const float2*>(a.block.ml + p * 2),
+              *reinterpret_cast<const float4*>(a.block.part + p * a.dv + c4 * 4), base);
   }
   acc_s[tid] = o;
   l_s[tid] = l;
   __syncthreads();
   if (grp != 0) return;
   for (int q = 1; q < groups; ++q) {
-    const float4 x = acc_s[q * lanes + c4];
-    o.x += x.x;
-    o.y += x.y;
-    o.z += x.z;
-    o.w += x.w;
+    const float4 y = acc_s[q * lanes + c4];
+    o.x += y.x;
+    o.y += y.y;
+    o.z += y.z;
+    o.w += y.w;
     l += l_s[q * lanes + c4];
   }
   const float f = inverse_sum(l);
   const float y[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
+  const size_t orow = (size_t)s.b * a.Hq + g * a.G + blk * a.hb + h;
   const size_t at = orow * a.dv + c4 * 4;
   if (a.dtype == LT_F32)
     store4<float>(a.out, at, y);
@@ -103,6 +71,12 @@ __global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const DecodeArgs a
   else
     store4<__half>(a.out, at, y);
   if (a.lse && c4 == 0) a.lse[orow] = log_sum(mx, l);
+}
+
+bool pools_within(const lt_kv_cache_t* c, size_t bytes) {
+  Span s[4];
+  cache_spans(c, s);
+  return s[0].n <= bytes && s[1].n <= bytes;
 }
 
 // query heads per unit, and warps (runs) on a device: the engines' kHeads and
@@ -115,8 +89,12 @@ int run_count(lt_dtype_t t, lt_kv_dtype_t kv, int G, int sms) {
   return sms * (t == LT_F32 ? 4 : eight_bit(kv) && G <= 8 ? 16 : 8);
 }
 
-size_t workspace_floats(lt_dtype_t t, lt_kv_dtype_t kv, int G, int dv, int sms) {
-  return (size_t)run_count(t, kv, G, sms) * 2 * heads_per_unit(t, G) * (dv + 2);
+// bytes of the pieces of n owners (two each), and the whole workspace
+size_t piece_bytes(int n, int hb, int dv) { return (size_t)n * 2 * hb * (dv + 2) * sizeof(float); }
+size_t workspace_of(lt_dtype_t t, lt_kv_dtype_t kv, int G, int dv, int sms) {
+  const int hb = heads_per_unit(t, G);
+  return piece_bytes(run_count(t, kv, G, sms), hb, dv) + piece_bytes(sms, hb, dv) +
+         (size_t)sms * sizeof(Shared);
 }
 
 }  // namespace
@@ -136,7 +114,7 @@ extern "C" lt_status_t lt_paged_attn_decode_plan(int H_q, int H_kv, int d, int d
     return LT_ERR_INVALID_ARG;
   if (num_sms <= 0) num_sms = device_sm_count();
   if (num_sms <= 0) return LT_ERR_CUDA;
-  *workspace_bytes = workspace_floats(dtype, kv_dtype, H_q / H_kv, dv, num_sms) * sizeof(float);
+  *workspace_bytes = workspace_of(dtype, kv_dtype, H_q / H_kv, dv, num_sms);
   return LT_OK;
 }
 
@@ -158,6 +136,11 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
     return LT_ERR_INVALID_ARG;
   if (!aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(block_table, 4) ||
       !aligned_to(seq_lens, 4) || !aligned_to(lse, 4))
+    return LT_ERR_INVALID_ARG;
+  // pools are addressed in 32 bits of 16 bytes, and a warp's tiles counted in 31
+  const int64_t most = (int64_t)max_pages * cache->page_size;
+  const int64_t tiles = ((most < 0x7fffffff ? most : 0x7fffffff) / kTokens + 1) * H_q;
+  if (!pools_within(cache, (size_t)64 << 30) || tiles > ((int64_t)1 << 40) / B)
     return LT_ERR_INVALID_ARG;
   const size_t es = dtype_size(dtype);
   Span ins[8];
@@ -187,20 +170,20 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   Workspace w;
   const lt_status_t sw =
       w.take(workspace, workspace_bytes,
-             workspace_floats(dtype, cache->dtype, a.G, cache->dv, sms) * sizeof(float), (cudaStream_t)stream);
+             workspace_of(dtype, cache->dtype, a.G, cache->dv, sms), (cudaStream_t)stream);
   if (sw != LT_OK) return sw;
-  const int64_t ks = (int64_t)kv_size(cache->dtype);
   a.q = q;
   a.k = static_cast<const uint8_t*>(cache->k);
   a.v = static_cast<const uint8_t*>(cache->v);
   a.ks = cache->k_scale;
   a.vs = cache->v_scale;
-  a.kpg = cache->k_page_stride * ks;
-  a.ksl = cache->k_slot_stride * ks;
-  a.khd = cache->k_head_stride * ks;
-  a.vpg = cache->v_page_stride * ks;
-  a.vsl = cache->v_slot_stride * ks;
-  a.vhd = cache->v_head_stride * ks;
+  const int64_t ks = (int64_t)kv_size(cache->dtype);
+  a.kpg = (uint32_t)(cache->k_page_stride * ks / 16);
+  a.ksl = (uint32_t)(cache->k_slot_stride * ks / 16);
+  a.khd = (uint32_t)(cache->k_head_stride * ks / 16);
+  a.vpg = (uint32_t)(cache->v_page_stride * ks / 16);
+  a.vsl = (uint32_t)(cache->v_slot_stride * ks / 16);
+  a.vhd = (uint32_t)(cache->v_head_stride * ks / 16);
   a.table = block_table;
   a.table_stride = table_stride;
   a.lens = seq_lens;
@@ -210,22 +193,28 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.num_pages = cache->num_pages;
   a.page_size = cache->page_size;
   a.max_pages = max_pages;
+  while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
+  a.page_magic = (uint32_t)(((uint64_t)1 << (31 + a.page_shift)) / a.page_size + 1);
   a.window = window;
-  a.min_tiles = 2;
   a.scale = scale;
   a.out = out;
   a.lse = lse;
   a.dv = cache->dv;
   a.dtype = (int)dtype;
-  a.part = static_cast<float*>(w.p);
-  a.ml = a.part + (size_t)a.warps * 2 * a.hb * a.dv;
+  float* p = static_cast<float*>(w.p);
+  a.warp.part = p;
+  a.warp.ml = p + (size_t)a.warps * 2 * a.hb * a.dv;
+  p += piece_bytes(a.warps, a.hb, a.dv) / sizeof(float);
+  a.block.part = p;
+  a.block.ml = p + (size_t)sms * 2 * a.hb * a.dv;
+  a.shared = reinterpret_cast<Shared*>(p + piece_bytes(sms, a.hb, a.dv) / sizeof(float));
   a.err = err;
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = dtype == LT_BF16  ? launch_bf16(a, cache->dtype, cache->d, sms, s)
                   : dtype == LT_F16 ? launch_f16(a, cache->dtype, cache->d, sms, s)
                                     : launch_f32(a, cache->dtype, cache->d, sms, s);
   if (e == cudaSuccess)
-    e = launch_dependent(lt_paged_join_kernel, dim3(a.Hq, a.B), kJoin, 0, s, a);
+    e = launch_dependent(lt_paged_join_kernel, dim3(sms, a.hb), kJoin, 0, s, a);
   const cudaError_t f = w.release();
   if (e == cudaSuccess) e = f;
   return e == cudaSuccess ? LT_OK : LT_ERR_CUDA;

@@ -11,16 +11,18 @@
 // Bound by memory: every key and value is read once, for G <= 16 query heads,
 // 2G flops per byte of a 16-bit cache.
 //
-// Split: the cache of all (sequence, KV head) pairs, cut into tiles of kTile
+// Split: the cache of all (sequence, KV head) pairs, cut into tiles of kTokens
 // tokens and laid end to end, is dealt out in equal runs to the warps of one
-// launch with a fixed number of blocks, whatever the lengths: a batch of very
+// launch with one block per SM, whatever the lengths: a batch of very
 // different sequences and one long sequence load the SMs alike, and the
 // workspace does not grow with either.  A warp owns its run: its own ring of
 // tiles in shared memory, filled with 16-byte asynchronous copies, its own
 // running maximum and sum; no barrier between warps.  A pair that lies inside
-// one run is finished by its warp.  A pair that several runs share leaves one
-// partial result per run, and a second launch, which starts early and waits
-// for the first, joins them in run order, so results do not depend on timing.
+// one run is finished by its warp.  Where several warps of a block share a
+// pair, each leaves a piece, and the block joins them at its end; where
+// several blocks share it, each leaves one, and a second launch (which starts
+// early and waits for the first) joins those.  Pieces are always added in the
+// order of the tiles, so results do not depend on timing.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,26 +53,41 @@ struct Int8 {
   int8_t b;
 };
 
+// A piece of a pair: unnormalised sums of values [heads][dv], and the maximum
+// and sum of weights [heads][2].
+struct Pieces {
+  float* part;
+  float* ml;
+};
+// what a block leaves for the second launch: the unit that begins in it and
+// goes on in the blocks after it
+struct Shared {
+  int b, u;    // sequence and unit
+  int blocks;  // blocks that share it, this one first (0: none)
+  int pad;
+};
+
 struct DecodeArgs {
   const void* q;
   const uint8_t* k;
   const uint8_t* v;
   const float* ks;
   const float* vs;
-  int64_t kpg, ksl, khd, vpg, vsl, vhd;  // pool strides, bytes
+  uint32_t kpg, ksl, khd, vpg, vsl, vhd;  // pool strides, in 16 bytes
   const int32_t* table;
   int64_t table_stride;
   const int32_t* lens;
   int B, Hq, Hkv, G, nhb;  // nhb: blocks of query heads per KV head
-  int hb;                  // query heads per block (the engine's kHeads)
+  int hb;                  // query heads per block of them
   int num_pages, page_size, max_pages, window;
-  int warps;      // runs the tiles are dealt to
-  int min_tiles;  // shortest run
+  uint32_t page_magic;  // floor(2^(31 + page_shift) / page_size) + 1
+  int page_shift;       // ceil(log2(page_size))
+  int warps;            // runs that the tiles are dealt to
   float scale;
   void* out;
   float* lse;
-  float* part;  // [warps][2][hb][dv] partial accumulators
-  float* ml;    // [warps][2][hb][2] their maximum and sum
+  Pieces warp, block;  // [warps][2] and [blocks][2] pieces of hb heads
+  Shared* shared;      // [blocks]
   int dv, dtype;
   int* err;
 };
@@ -92,9 +109,11 @@ __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b) {
   return s;
 }
 
-// tiles per run, from the tiles of all pairs
-__device__ __forceinline__ int64_t run_length(const DecodeArgs& a, int64_t total) {
-  return max((total + a.warps - 1) / a.warps, (int64_t)a.min_tiles);
+// pos / page_size for 0 <= pos < 2^31: with m = page_magic, m page_size exceeds
+// 2^(31 + s) by at most page_size <= 2^s, so pos m / 2^(31 + s) exceeds the
+// quotient by less than 1 / page_size
+__device__ __forceinline__ int page_of(const DecodeArgs& a, int pos) {
+  return (int)(((uint64_t)(uint32_t)pos * a.page_magic) >> (31 + a.page_shift));
 }
 
 // --------------------------------------------------------------- copies
@@ -218,6 +237,16 @@ __device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f 
 // log of the sum, of weights relative to 2^m
 __device__ __forceinline__ float log_sum(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// one more piece (maximum and sum ml, values x) relative to 2^base
+__device__ __forceinline__ void add_piece(float4& o, float& l, float2 ml, float4 x, float base) {
+  const float f = exp2f(ml.x - base);
+  l = fmaf(f, ml.y, l);
+  o.x = fmaf(f, x.x, o.x);
+  o.y = fmaf(f, x.y, o.y);
+  o.z = fmaf(f, x.z, o.z);
+  o.w = fmaf(f, x.w, o.w);
 }
 
 // --------------------------------------------------- engine: tensor cores
@@ -738,15 +767,26 @@ struct Lookup {
   bool in;
 };
 
+// a warp's pieces of pairs that it shares: [0] the segment that its run began
+// in the middle of, or that fills the run; [1] the one that its run ends in
+struct Left {
+  int64_t from;  // the unit's first tile, end to end
+  int b, u, tiles;
+  bool any;
+};
+
 template <typename E>
 __global__ void __launch_bounds__(E::kWarps * 32, 1)
     lt_paged_decode_kernel(const DecodeArgs a) {
   using R = Ring<E>;
   using QT = typename E::QT;
-  constexpr int kThreads = E::kWarps * 32, TILE = E::kTile, S = R::kStages;
+  constexpr int W = E::kWarps, kThreads = W * 32, TILE = E::kTile, S = R::kStages;
+  static_assert(W <= 16, "the pieces of a block's warps fit one warp's lanes");
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t before[kThreads];     // tiles of the sequences before this thread's
-  __shared__ int64_t warp_sum[E::kWarps];
+  __shared__ int64_t before[kThreads];  // tiles of the sequences before this thread's
+  __shared__ int64_t warp_sum[W];
+  __shared__ Left left[2 * W];
+  __shared__ int order[2 * W], group0[2 * W + 1], groups;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   dependency_release();
 
@@ -765,154 +805,229 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
     if (lane >= off) scan += x;
   }
   if (lane == 31) warp_sum[warp] = scan;
+  if (tid < 2 * W) left[tid].any = false;
   __syncthreads();
   int64_t total = 0, mine = 0;
 #pragma unroll
-  for (int w = 0; w < E::kWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) mine += warp_sum[w];
     total += warp_sum[w];
   }
   before[tid] = mine + scan - sum;
   __syncthreads();
 
+  // a sequence of no keys: zeros, from one block each
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Seq s = seq_of(a, b);
+    if (s.bad || s.tiles) continue;
+    for (int i = tid; i < a.Hq * a.dv; i += kThreads)
+      from_float(static_cast<QT*>(a.out) + (size_t)b * a.Hq * a.dv + i, 0.0f);
+    if (a.lse)
+      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)b * a.Hq + i] = -INFINITY;
+  }
+
   const int units = a.Hkv * a.nhb;
   total *= units;
-  const int64_t run = run_length(a, total);
-  const int gw = warp * gridDim.x + blockIdx.x;  // runs spread over the SMs first
+  // tiles per run: at least one, so that a short cache still spreads
+  const int64_t run = max((total + a.warps - 1) / a.warps, (int64_t)1);
+  const int gw = blockIdx.x * W + warp;
   const int64_t start = gw * run, end = min(start + run, total);
-  if (start >= end) return;
 
-  Cursor cc;
-  {
-    int lo = 0, hi = kThreads;  // the last thread whose sequences begin at or before start
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (before[mid] * units <= start)
-        lo = mid;
-      else
-        hi = mid;
+  if (start < end) {
+    Cursor cc;
+    {
+      int lo = 0, hi = kThreads;  // the last thread whose sequences begin at or before start
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] * units <= start)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      int64_t rem = start - before[lo] * units;
+      cc.b = lo * per;
+      cc.s = seq_of(a, cc.b);
+      while (cc.b + 1 < a.B && rem >= (int64_t)cc.s.tiles * units) {
+        rem -= (int64_t)cc.s.tiles * units;
+        cc.s = seq_of(a, ++cc.b);
+      }
+      cc.u = (int)(rem / cc.s.tiles);
+      cc.t = (int)(rem - (int64_t)cc.u * cc.s.tiles);
     }
-    int64_t rem = start - before[lo] * units;
-    cc.b = lo * per;
-    cc.s = seq_of(a, cc.b);
-    while (cc.b + 1 < a.B && rem >= (int64_t)cc.s.tiles * units) {
-      rem -= (int64_t)cc.s.tiles * units;
-      cc.s = seq_of(a, ++cc.b);
+    Cursor pc = cc;
+
+    uint8_t* ring = smem + warp * R::kWarpBytes;
+    const uint32_t ring_u = smem_u32(ring);
+    E eng;
+    eng.init(ring + R::kStage * S);
+
+    const int row = lane & (TILE - 1);
+    auto look = [&](const Cursor& c) {
+      Lookup p;
+      const int pos = c.s.first + c.t * TILE + row;
+      p.in = pos < c.s.len;
+      const int idx = page_of(a, pos);
+      p.slot = pos - idx * a.page_size;
+      p.page = p.in ? __ldg(a.table + (int64_t)c.b * a.table_stride + idx) : 0;
+      p.g = a.nhb == 1 ? c.u : c.u / a.nhb;
+      return p;
+    };
+    auto issue = [&](int stage, const Lookup& p) {
+      bool live = p.in;
+      if (live && (p.page < 0 || p.page >= a.num_pages)) {
+        report_error(a.err, kDevErrBadPage);
+        live = false;
+      }
+      const uint32_t mask = __ballot_sync(0xffffffffu, live) & ((1u << TILE) - 1u);
+      const uint32_t page = live ? p.page : 0, slot = live ? p.slot : 0;
+      const uint32_t ko = page * a.kpg + slot * a.ksl + p.g * a.khd;
+      const uint32_t vo = page * a.vpg + slot * a.vsl + p.g * a.vhd;
+      const uint32_t dst = ring_u + stage * R::kStage;
+      constexpr int kc = E::kKRow / 16, vc = E::kVRow / 16;  // chunks per row
+#pragma unroll
+      for (int i = 0; i < TILE * kc / 32; ++i) {
+        const int r = i * (32 / kc) + lane / kc, c = lane % kc;
+        const uint32_t off = __shfl_sync(0xffffffffu, ko, r) + c;
+        copy16(dst + chunk_at<E::kKRow>(r, c), a.k + (uint64_t)off * 16, (mask >> r) & 1u);
+      }
+#pragma unroll
+      for (int i = 0; i < TILE * vc / 32; ++i) {
+        const int r = i * (32 / vc) + lane / vc, c = lane % vc;
+        const uint32_t off = __shfl_sync(0xffffffffu, vo, r) + c;
+        copy16(dst + R::kK + chunk_at<E::kVRow>(r, c), a.v + (uint64_t)off * 16, (mask >> r) & 1u);
+      }
+      if constexpr (E::kQuant) {  // lanes 0 .. 15 the keys' scales, 16 .. 31 the values'
+        const int64_t at = ((int64_t)page * a.Hkv + p.g) * a.page_size + slot;
+        copy4(dst + R::kK + R::kV + lane * 4, (lane < TILE ? a.ks : a.vs) + at, live);
+      }
+      if (lane == 0)
+        *reinterpret_cast<uint32_t*>(ring + stage * R::kStage + R::kK + R::kV + 2 * R::kScale) =
+            mask;
+    };
+
+    const int count = (int)(end - start);
+    int issued = 0;
+    Lookup pend = look(pc);
+    auto feed = [&](int stage) {
+      if (issued < count) {
+        issue(stage, pend);
+        if (++issued < count) {
+          pc.next(a, units);
+          pend = look(pc);
+        }
+      }
+      copy_commit();
+    };
+#pragma unroll 1
+    for (int s = 0; s < S - 1; ++s) feed(s);
+
+    int stage = 0, seg_t = cc.t;
+    bool first_seg = true;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      if (i == 0 || cc.t == 0) {  // a new unit
+        const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
+        const int h0 = g * a.G + blk * E::kHeads;
+        eng.begin(static_cast<const QT*>(a.q) + ((size_t)cc.b * a.Hq + h0) * E::kD,
+                  min(E::kHeads, a.G - blk * E::kHeads), a.scale);
+        seg_t = cc.t;
+      }
+      copy_wait<S - 2>();
+      __syncwarp();  // every lane's copies of this tile have landed, and the last tile is read
+      feed(stage == 0 ? S - 1 : stage - 1);
+      const uint8_t* st = ring + stage * R::kStage;
+      TileAt t;
+      t.k = ring_u + stage * R::kStage;
+      t.v = t.k + R::kK;
+      t.ks = reinterpret_cast<const float*>(st + R::kK + R::kV);
+      t.vs = reinterpret_cast<const float*>(st + R::kK + R::kV + R::kScale);
+      t.mask = *reinterpret_cast<const uint32_t*>(st + R::kK + R::kV + 2 * R::kScale);
+      eng.tile(t);
+      if (++stage == S) stage = 0;
+      const bool unit_done = cc.t + 1 == cc.s.tiles;
+      if (unit_done || i + 1 == count) {
+        const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
+        const size_t orow = (size_t)cc.b * a.Hq + g * a.G + blk * E::kHeads;
+        const int slot = first_seg ? 0 : 1;
+        const size_t piece = ((size_t)gw * 2 + slot) * a.hb;
+        Sink<QT> out;
+        out.partial = !(unit_done && seg_t == 0);
+        out.out = static_cast<QT*>(a.out) + orow * a.dv;
+        out.lse = a.lse ? a.lse + orow : nullptr;
+        out.part = a.warp.part + piece * a.dv;
+        out.ml = a.warp.ml + piece * 2;
+        eng.finish(out);
+        if (out.partial && lane == 0)
+          left[2 * warp + slot] = Left{start + i - cc.t, cc.b, cc.u, cc.s.tiles, true};
+        first_seg = false;
+      }
+      if (i + 1 < count) cc.next(a, units);
     }
-    cc.u = (int)(rem / cc.s.tiles);
-    cc.t = (int)(rem - (int64_t)cc.u * cc.s.tiles);
+    copy_wait<0>();
   }
-  Cursor pc = cc;
 
-  uint8_t* ring = smem + warp * R::kWarpBytes;
-  const uint32_t ring_u = smem_u32(ring);
-  E eng;
-  eng.init(ring + R::kStage * S);
-
-  const int row = lane & (TILE - 1);
-  auto look = [&](const Cursor& c) {
-    Lookup p;
-    const int pos = c.s.first + c.t * TILE + row;
-    p.in = pos < c.s.len;
-    const int idx = pos / a.page_size;
-    p.slot = pos - idx * a.page_size;
-    p.page = p.in ? __ldg(a.table + (int64_t)c.b * a.table_stride + idx) : 0;
-    p.g = c.u / a.nhb;
-    return p;
-  };
-  auto issue = [&](int stage, const Lookup& p) {
-    bool live = p.in;
-    if (live && (p.page < 0 || p.page >= a.num_pages)) {
-      report_error(a.err, kDevErrBadPage);
-      live = false;
+  // ---- the pieces of this block's warps, joined per unit
+  __syncthreads();
+  if (warp == 0) {  // lane p: piece p, in the order of the tiles
+    const bool any = lane < 2 * W && left[lane].any;
+    const uint32_t valid = __ballot_sync(0xffffffffu, any);
+    const uint32_t below = valid & ((1u << lane) - 1u);
+    const int prev = below ? 31 - __clz(below) : 0;
+    const bool lead = any && (!below || left[lane].from != left[prev].from);
+    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    if (any) order[__popc(below)] = lane;
+    if (lead) group0[__popc(leads & ((1u << lane) - 1u))] = __popc(below);
+    if (lane == 0) {
+      groups = __popc(leads);
+      group0[__popc(leads)] = __popc(valid);
     }
-    uint32_t mask = __ballot_sync(0xffffffffu, live);
-    if (TILE < 32) mask &= (1u << (TILE & 31)) - 1u;
-    const int64_t page = live ? p.page : 0, slot = live ? p.slot : 0;
-    const int64_t ko = page * a.kpg + slot * a.ksl + p.g * a.khd;
-    const int64_t vo = page * a.vpg + slot * a.vsl + p.g * a.vhd;
-    const uint32_t dst = ring_u + stage * R::kStage;
-    constexpr int kc = E::kKRow / 16, vc = E::kVRow / 16;  // chunks per row
-#pragma unroll
-    for (int i = 0; i < TILE * kc / 32; ++i) {
-      const int r = i * (32 / kc) + lane / kc, c = lane % kc;
-      const int64_t off = __shfl_sync(0xffffffffu, ko, r);
-      copy16(dst + chunk_at<E::kKRow>(r, c), a.k + off + c * 16, (mask >> r) & 1u);
+  }
+  __syncthreads();
+  const int64_t block_start = (int64_t)blockIdx.x * W * run, block_end = block_start + W * run;
+  const int cols = a.dv >> 2, per_group = a.hb * cols;
+  for (int item = tid; item < groups * per_group; item += kThreads) {
+    const int gi = item / per_group, rest = item - gi * per_group;
+    const int h = rest / cols, c4 = rest - h * cols;
+    const int p0 = group0[gi], n = group0[gi + 1] - p0;
+    const Left f = left[order[p0]];
+    const int g = f.u / a.nhb, blk = f.u - g * a.nhb;
+    if (h >= a.G - blk * E::kHeads) continue;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f, mx = -INFINITY;
+    auto row = [&](int i) { return ((size_t)blockIdx.x * 2 * W + order[p0 + i]) * a.hb + h; };
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) mx = fmaxf(mx, a.warp.ml[row(i) * 2]);
+    const float base = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const size_t p = row(i);
+      add_piece(o, l, *reinterpret_cast<const float2*>(a.warp.ml + p * 2),
+                *reinterpret_cast<const float4*>(a.warp.part + p * a.dv + c4 * 4), base);
     }
-#pragma unroll
-    for (int i = 0; i < TILE * vc / 32; ++i) {
-      const int r = i * (32 / vc) + lane / vc, c = lane % vc;
-      const int64_t off = __shfl_sync(0xffffffffu, vo, r);
-      copy16(dst + R::kK + chunk_at<E::kVRow>(r, c), a.v + off + c * 16, (mask >> r) & 1u);
+    if (f.from >= block_start && f.from + f.tiles <= block_end) {
+      const size_t orow = (size_t)f.b * a.Hq + g * a.G + blk * E::kHeads + h;
+      const float r = inverse_sum(l);
+      const float y[4] = {o.x * r, o.y * r, o.z * r, o.w * r};
+      store_quad(static_cast<QT*>(a.out) + orow * a.dv + c4 * 4, y);
+      if (a.lse && c4 == 0) a.lse[orow] = log_sum(mx, l);
+    } else {
+      const size_t p = ((size_t)blockIdx.x * 2 + (f.from < block_start ? 0 : 1)) * a.hb + h;
+      *reinterpret_cast<float4*>(a.block.part + p * a.dv + c4 * 4) = o;
+      if (c4 == 0) *reinterpret_cast<float2*>(a.block.ml + p * 2) = make_float2(mx, l);
     }
-    if constexpr (E::kQuant) {
-      const int64_t at = (page * a.Hkv + p.g) * a.page_size + slot;
-      if (lane < TILE) {
-        copy4(dst + R::kK + R::kV + lane * 4, a.ks + at, live);
-        copy4(dst + R::kK + R::kV + R::kScale + lane * 4, a.vs + at, live);
+  }
+  if (tid == 0) {  // only the last unit of the block can begin in it and go on
+    Shared s = {0, 0, 0, 0};
+    if (groups) {
+      const Left f = left[order[group0[groups] - 1]];
+      if (f.from >= block_start && f.from + f.tiles > block_end) {
+        s.b = f.b;
+        s.u = f.u;
+        s.blocks = (int)((f.from + f.tiles - 1) / (W * run)) - blockIdx.x + 1;
       }
     }
-    if (lane == 0)
-      *reinterpret_cast<uint32_t*>(ring + stage * R::kStage + R::kK + R::kV + 2 * R::kScale) = mask;
-  };
-
-  const int64_t count = end - start;
-  int64_t issued = 0;
-  Lookup pend = look(pc);
-  auto feed = [&](int stage) {
-    if (issued < count) {
-      issue(stage, pend);
-      if (++issued < count) {
-        pc.next(a, units);
-        pend = look(pc);
-      }
-    }
-    copy_commit();
-  };
-#pragma unroll 1
-  for (int s = 0; s < S - 1; ++s) feed(s);
-
-  int stage = 0, seg_t = cc.t;
-  bool first_seg = true;
-#pragma unroll 1
-  for (int64_t i = 0; i < count; ++i) {
-    if (i == 0 || cc.t == 0) {  // a new unit
-      const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
-      const int h0 = g * a.G + blk * E::kHeads;
-      eng.begin(static_cast<const QT*>(a.q) + ((size_t)cc.b * a.Hq + h0) * E::kD,
-                min(E::kHeads, a.G - blk * E::kHeads), a.scale);
-      seg_t = cc.t;
-    }
-    copy_wait<S - 2>();
-    __syncwarp();  // every lane's copies of this tile have landed, and the last tile is read
-    feed(stage == 0 ? S - 1 : stage - 1);
-    const uint8_t* st = ring + stage * R::kStage;
-    TileAt t;
-    t.k = ring_u + stage * R::kStage;
-    t.v = t.k + R::kK;
-    t.ks = reinterpret_cast<const float*>(st + R::kK + R::kV);
-    t.vs = reinterpret_cast<const float*>(st + R::kK + R::kV + R::kScale);
-    t.mask = *reinterpret_cast<const uint32_t*>(st + R::kK + R::kV + 2 * R::kScale);
-    eng.tile(t);
-    if (++stage == S) stage = 0;
-    const bool unit_done = cc.t + 1 == cc.s.tiles;
-    if (unit_done || i + 1 == count) {
-      const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
-      const int h0 = g * a.G + blk * E::kHeads;
-      Sink<QT> out;
-      out.partial = !(unit_done && seg_t == 0);
-      const size_t orow = (size_t)cc.b * a.Hq + h0;
-      out.out = static_cast<QT*>(a.out) + orow * a.dv;
-      out.lse = a.lse ? a.lse + orow : nullptr;
-      const size_t piece = (size_t)gw * 2 + (first_seg ? 0 : 1);
-      out.part = a.part + piece * a.hb * a.dv;
-      out.ml = a.ml + piece * a.hb * 2;
-      eng.finish(out);
-      first_seg = false;
-    }
-    if (i + 1 < count) cc.next(a, units);
+    a.shared[blockIdx.x] = s;
   }
-  copy_wait<0>();
 }
 
 template <typename E>

@@ -545,7 +545,9 @@ LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *b
  *
  * q          [B][H_q][d] of element type dtype, dense, 16-byte aligned.
  * cache, block_table, table_stride, max_pages   as for lt_kv_cache_read; the
- *            cache's type is dtype's own or 8 bits.
+ *            cache's type is dtype's own or 8 bits, and each pool spans at
+ *            most 64 GiB (LT_ERR_INVALID_ARG otherwise, and for B * H_q times
+ *            the tiles of max_pages pages above 2^40).
  * seq_lens   [B] int32 device.  A negative length, or one over max_pages
  *            pages, is reported (LT_ERR_DEVICE_BAD_SEQLENS) and its rows of
  *            out and lse are left as they were.  A page outside the pool is
@@ -559,11 +561,11 @@ LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *b
  * workspace  as for lt_qk_norm_rope_bwd, with lt_paged_attn_decode_plan's bytes.
  * Evaluation: the tiles of all (sequence, KV head) pairs are dealt out evenly
  * to the warps of one persistent launch, whatever the lengths; each warp
- * keeps a running maximum and sum in fp32, and a second launch joins the
- * pieces of a pair that several warps share, in their order.  Scores, sums
- * and accumulators are fp32; the weights are rounded to the cache's 16-bit
- * type (fp16 for 8-bit caches) for the tensor cores, and not at all for
- * LT_F32.
+ * keeps a running maximum and sum in fp32, and the pieces of a pair that
+ * several warps share are joined in their order, by a second launch where
+ * they lie in several blocks.  Scores, sums and accumulators are fp32; for
+ * the tensor cores the weights are two terms of the cache's 16-bit type (one
+ * fp16 term for an 8-bit cache under LT_BF16), and not rounded for LT_F32.
  * Returns as lt_kv_cache_write.
  */
 LT_API lt_status_t lt_paged_attn_decode(const void *q, const lt_kv_cache_t *cache,
