@@ -7,62 +7,72 @@ namespace lt {
 namespace paged {
 namespace {
 
-// Block (x, h): head h of the unit that begins in block x of the first launch
-// and goes on in others, if there is one.  Its pieces are weighted by
-// exp2(their maximum - the largest) and added in the order of the blocks:
-// four columns per lane, groups of lanes taking the pieces in turn.
-constexpr int kJoin = 256;
+// Block (x, y): entry x of shared[], query heads y per .. y per + per - 1, with
+// kJoin / per threads each.  A head's pieces are weighted by exp2(their maximum
+// - the largest) and added in the order of the blocks: four columns per lane,
+// groups of lanes taking the pieces in turn.  One head per block where the
+// entries are few (one long sequence has a piece in every block of the first
+// launch), eight where they are many (and mostly of two or three pieces).
+constexpr int kJoin = 256, kJoinHeads = 8;
+
+struct JoinArgs {
+  DecodeArgs a;
+  int per;  // query heads per block
+};
 
 template <typename T>
 __device__ __forceinline__ void store4(void* out, size_t at, const float* f) {
   store_quad(static_cast<T*>(out) + at, f);
 }
 
-__global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const DecodeArgs a) {
-  __shared__ float fred[kJoin / 32];
+__global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const JoinArgs j) {
   __shared__ float4 acc_s[kJoin];
-  __shared__ float l_s[kJoin];
-  const int x = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  __shared__ float l_s[kJoin], m_s[kJoin];
+  const DecodeArgs& a = j.a;
+  const int share = kJoin / j.per, tid = threadIdx.x % share;
+  const int h = blockIdx.y * j.per + threadIdx.x / share;
+  const int lanes = a.dv >> 2, groups = share / lanes, c4 = tid % lanes, grp = tid / lanes;
   // every block waits, so that this launch ends after the first one has
   dependency_wait();
-  const Shared s = a.shared[x];
-  const int n = s.blocks, g = s.u / a.nhb, blk = s.u - g * a.nhb;
-  if (n == 0 || h >= a.G - blk * a.hb) return;
-  const int lanes = a.dv >> 2, groups = kJoin / lanes, c4 = tid % lanes, grp = tid / lanes;
-  // the first piece is the second of its block, the others the first of theirs
-  auto row = [&](int i) { return ((size_t)(x + i) * 2 + (i == 0 ? 1 : 0)) * a.hb + h; };
-  float mx = -INFINITY;
-  for (int i = tid; i < n; i += kJoin) mx = fmaxf(mx, a.block.ml[row(i) * 2]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  if ((tid & 31) == 0) fred[tid >> 5] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoin / 32; ++w) mx = fmaxf(mx, fred[w]);
-  const float base = mx == -INFINITY ? 0.0f : mx;
+  const Shared s = a.shared[blockIdx.x];
+  const int n = s.blocks;
+  if (n == 0) return;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float l = 0.0f;
+  float l = 0.0f, mx = -INFINITY;
+  if (h < a.Hq) {
+    const int g = h / a.G, hh = h - g * a.G, blk = hh / a.hb;
+    const int units = a.Hkv * a.nhb, u = g * a.nhb + blk;
+    // the first piece is the second of its block, the others the first of theirs
+    auto row = [&](int i) {
+      return (((size_t)(s.block + i) * 2 + (i == 0 ? 1 : 0)) * units + u) * a.hb + hh - blk * a.hb;
+    };
+    // each group by its own maximum
 #pragma unroll 4
-  for (int i = grp; i < n; i += groups) {
-    const size_t p = row(i);
-    add_piece(o, l, *reinterpret_cast<const float2*>(a.block.ml + p * 2),
-              *reinterpret_cast<const float4*>(a.block.part + p * a.dv + c4 * 4), base);
+    for (int i = grp; i < n; i += groups) mx = fmaxf(mx, a.block.ml[row(i) * 2]);
+    const float base = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll 4
+    for (int i = grp; i < n; i += groups) {
+      const size_t p = row(i);
+      add_piece(o, l, *reinterpret_cast<const float2*>(a.block.ml + p * 2),
+                *reinterpret_cast<const float4*>(a.block.part + p * a.dv + c4 * 4), base);
+    }
   }
-  acc_s[tid] = o;
-  l_s[tid] = l;
+  acc_s[threadIdx.x] = o;
+  l_s[threadIdx.x] = l;
+  m_s[threadIdx.x] = mx;
   __syncthreads();
-  if (grp != 0) return;
-  for (int q = 1; q < groups; ++q) {
-    const float4 y = acc_s[q * lanes + c4];
-    o.x += y.x;
-    o.y += y.y;
-    o.z += y.z;
-    o.w += y.w;
-    l += l_s[q * lanes + c4];
-  }
+  if (grp != 0 || h >= a.Hq) return;
+  const int at0 = threadIdx.x;  // this column's groups are `lanes` apart
+  for (int q = 1; q < groups; ++q) mx = fmaxf(mx, m_s[at0 + q * lanes]);
+  const float base = mx == -INFINITY ? 0.0f : mx;
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  l = 0.0f;
+  for (int q = 0; q < groups; ++q)
+    add_piece(o, l, make_float2(m_s[at0 + q * lanes], l_s[at0 + q * lanes]), acc_s[at0 + q * lanes],
+              base);
   const float f = inverse_sum(l);
   const float y[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
-  const size_t orow = (size_t)s.b * a.Hq + g * a.G + blk * a.hb + h;
+  const size_t orow = (size_t)s.b * a.Hq + h;
   const size_t at = orow * a.dv + c4 * 4;
   if (a.dtype == LT_F32)
     store4<float>(a.out, at, y);
@@ -79,22 +89,30 @@ bool pools_within(const lt_kv_cache_t* c, size_t bytes) {
   return s[0].n <= bytes && s[1].n <= bytes;
 }
 
-// query heads per unit, and warps (runs) on a device: the engines' kHeads and
-// kWarps
+// query heads per unit and warps per block: the engines' kHeads and kWarps
 int heads_per_unit(lt_dtype_t t, int G) {
   const int most = t == LT_F32 ? 8 : 16;
   return G < most ? G : most;
 }
-int run_count(lt_dtype_t t, lt_kv_dtype_t kv, int G, int sms) {
-  return sms * (t == LT_F32 ? 4 : eight_bit(kv) && G <= 8 ? 16 : 8);
+int block_warps(lt_dtype_t t, lt_kv_dtype_t kv, int G) {
+  return t == LT_F32 ? 4 : eight_bit(kv) && G <= 8 ? 16 : 8;
 }
 
-// bytes of the pieces of n owners (two each), and the whole workspace
-size_t piece_bytes(int n, int hb, int dv) { return (size_t)n * 2 * hb * (dv + 2) * sizeof(float); }
-size_t workspace_of(lt_dtype_t t, lt_kv_dtype_t kv, int G, int dv, int sms) {
-  const int hb = heads_per_unit(t, G);
-  return piece_bytes(run_count(t, kv, G, sms), hb, dv) + piece_bytes(sms, hb, dv) +
-         (size_t)sms * sizeof(Shared);
+// the workspace, one block of the first launch per SM: pieces of its warps
+// (two each), of its units (two each), and an entry for the second launch
+struct Sizes {
+  size_t warp, block;  // pieces
+  size_t floats;       // of a piece
+  size_t bytes;
+};
+Sizes sizes_of(lt_dtype_t t, lt_kv_dtype_t kv, int H_q, int H_kv, int dv, int sms) {
+  const int G = H_q / H_kv, hb = heads_per_unit(t, G), nhb = (G + hb - 1) / hb;
+  Sizes z;
+  z.warp = (size_t)sms * block_warps(t, kv, G) * 2;
+  z.block = (size_t)sms * 2 * H_kv * nhb;
+  z.floats = (size_t)hb * (dv + 2);
+  z.bytes = (z.warp + z.block) * z.floats * sizeof(float) + (size_t)sms * sizeof(Shared);
+  return z;
 }
 
 }  // namespace
@@ -114,7 +132,7 @@ extern "C" lt_status_t lt_paged_attn_decode_plan(int H_q, int H_kv, int d, int d
     return LT_ERR_INVALID_ARG;
   if (num_sms <= 0) num_sms = device_sm_count();
   if (num_sms <= 0) return LT_ERR_CUDA;
-  *workspace_bytes = workspace_of(dtype, kv_dtype, H_q / H_kv, dv, num_sms);
+  *workspace_bytes = sizes_of(dtype, kv_dtype, H_q, H_kv, dv, num_sms).bytes;
   return LT_OK;
 }
 
@@ -166,11 +184,9 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.G = H_q / cache->H_kv;
   a.hb = heads_per_unit(dtype, a.G);
   a.nhb = (a.G + a.hb - 1) / a.hb;
-  a.warps = run_count(dtype, cache->dtype, a.G, sms);
+  const Sizes z = sizes_of(dtype, cache->dtype, H_q, cache->H_kv, cache->dv, sms);
   Workspace w;
-  const lt_status_t sw =
-      w.take(workspace, workspace_bytes,
-             workspace_of(dtype, cache->dtype, a.G, cache->dv, sms), (cudaStream_t)stream);
+  const lt_status_t sw = w.take(workspace, workspace_bytes, z.bytes, (cudaStream_t)stream);
   if (sw != LT_OK) return sw;
   a.q = q;
   a.k = static_cast<const uint8_t*>(cache->k);
@@ -203,18 +219,23 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.dtype = (int)dtype;
   float* p = static_cast<float*>(w.p);
   a.warp.part = p;
-  a.warp.ml = p + (size_t)a.warps * 2 * a.hb * a.dv;
-  p += piece_bytes(a.warps, a.hb, a.dv) / sizeof(float);
+  a.warp.ml = p + z.warp * a.hb * a.dv;
+  p += z.warp * z.floats;
   a.block.part = p;
-  a.block.ml = p + (size_t)sms * 2 * a.hb * a.dv;
-  a.shared = reinterpret_cast<Shared*>(p + piece_bytes(sms, a.hb, a.dv) / sizeof(float));
+  a.block.ml = p + z.block * a.hb * a.dv;
+  a.shared = reinterpret_cast<Shared*>(p + z.block * z.floats);
+  a.by_seq = B <= sms && B <= 128;  // (at most one sequence per thread of any engine)
   a.err = err;
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = dtype == LT_BF16  ? launch_bf16(a, cache->dtype, cache->d, sms, s)
                   : dtype == LT_F16 ? launch_f16(a, cache->dtype, cache->d, sms, s)
                                     : launch_f32(a, cache->dtype, cache->d, sms, s);
-  if (e == cudaSuccess)
-    e = launch_dependent(lt_paged_join_kernel, dim3(sms, a.hb), kJoin, 0, s, a);
+  if (e == cudaSuccess) {
+    const int entries = a.by_seq ? B : sms;
+    const JoinArgs j = {a, entries * H_q <= 4 * sms ? 1 : kJoinHeads};
+    e = launch_dependent(lt_paged_join_kernel, dim3(entries, (H_q + j.per - 1) / j.per), kJoin, 0,
+                         s, j);
+  }
   const cudaError_t f = w.release();
   if (e == cudaSuccess) e = f;
   return e == cudaSuccess ? LT_OK : LT_ERR_CUDA;

@@ -11,15 +11,17 @@
 // Bound by memory: every key and value is read once, for G <= 16 query heads,
 // 2G flops per byte of a 16-bit cache.
 //
-// Split: the cache of all (sequence, KV head) pairs, cut into tiles of kTokens
-// tokens and laid end to end, is dealt out in equal runs to the warps of one
-// launch with one block per SM, whatever the lengths: a batch of very
-// different sequences and one long sequence load the SMs alike, and the
-// workspace does not grow with either.  A warp owns its run: its own ring of
-// tiles in shared memory, filled with 16-byte asynchronous copies, its own
-// running maximum and sum; no barrier between warps.  A pair that lies inside
-// one run is finished by its warp.  Where several warps of a block share a
-// pair, each leaves a piece, and the block joins them at its end; where
+// Split: all sequences' tiles of kTokens tokens, laid end to end, are dealt out
+// in equal runs to the blocks of one launch, one per SM, whatever the lengths:
+// a batch of very different sequences and one long sequence load the SMs
+// alike, and the workspace does not grow with either.  Inside a block the
+// warps share out the units (KV head and block of query heads) of its run, so
+// that the heads of a token, neighbours in memory, are read at about the same
+// time (an 8-bit row is only 64 or 128 bytes).  A warp has its own ring of
+// tiles in shared memory, filled with 16-byte asynchronous copies, and its own
+// running maximum and sum; no barrier between warps.  A unit of a sequence
+// that one warp had whole is finished by it.  Where several warps of a block
+// share it, each leaves a piece, and the block joins them at its end; where
 // several blocks share it, each leaves one, and a second launch (which starts
 // early and waits for the first) joins those.  Pieces are always added in the
 // order of the tiles, so results do not depend on timing.
@@ -59,12 +61,10 @@ struct Pieces {
   float* part;
   float* ml;
 };
-// what a block leaves for the second launch: the unit that begins in it and
-// goes on in the blocks after it
+// A sequence that several blocks share, for the second launch: its first block
+// and their number (0: none here).
 struct Shared {
-  int b, u;    // sequence and unit
-  int blocks;  // blocks that share it, this one first (0: none)
-  int pad;
+  int b, block, blocks, pad;
 };
 
 struct DecodeArgs {
@@ -82,12 +82,12 @@ struct DecodeArgs {
   int num_pages, page_size, max_pages, window;
   uint32_t page_magic;  // floor(2^(31 + page_shift) / page_size) + 1
   int page_shift;       // ceil(log2(page_size))
-  int warps;            // runs that the tiles are dealt to
+  int by_seq;           // shared[] goes by sequence (else by first block)
   float scale;
   void* out;
   float* lse;
-  Pieces warp, block;  // [warps][2] and [blocks][2] pieces of hb heads
-  Shared* shared;      // [blocks]
+  Pieces warp, block;  // [blocks][warps][2] and [blocks][2][units] pieces of hb heads
+  Shared* shared;      // [min(B, blocks)]
   int dv, dtype;
   int* err;
 };
@@ -744,21 +744,12 @@ struct Ring {
   static_assert(kBytes <= 220 * 1024, "shared memory");
 };
 
-// a tile of a run: sequence b, unit u of it (KV head and block of query
-// heads), tile t of the unit
+// A tile of a block's run of columns [c0, c1) (a column: one tile of one
+// sequence, for every unit): unit u, column col, tile t of sequence b.
 struct Cursor {
   int b, u, t;
+  int64_t col;
   Seq s;
-  __device__ __forceinline__ void next(const DecodeArgs& a, int units) {
-    if (++t < s.tiles) return;
-    t = 0;
-    if (++u < units) return;
-    u = 0;
-    while (b + 1 < a.B) {
-      s = seq_of(a, ++b);
-      if (s.tiles) return;
-    }
-  }
 };
 
 // a tile whose table entries have been asked for: lane i holds row i % kTile's
@@ -767,10 +758,10 @@ struct Lookup {
   bool in;
 };
 
-// a warp's pieces of pairs that it shares: [0] the segment that its run began
-// in the middle of, or that fills the run; [1] the one that its run ends in
+// A warp's pieces of units that it shares with others of its block: [0] of the
+// segment that its part began with, [1] of the one that it ended with.
 struct Left {
-  int64_t from;  // the unit's first tile, end to end
+  int64_t from;  // the sequence's first column
   int b, u, tiles;
   bool any;
 };
@@ -783,7 +774,7 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
   constexpr int W = E::kWarps, kThreads = W * 32, TILE = E::kTile, S = R::kStages;
   static_assert(W <= 16, "the pieces of a block's warps fit one warp's lanes");
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t before[kThreads];  // tiles of the sequences before this thread's
+  __shared__ int64_t before[kThreads];  // columns of the sequences before this thread's
   __shared__ int64_t warp_sum[W];
   __shared__ Left left[2 * W];
   __shared__ int order[2 * W], group0[2 * W + 1], groups;
@@ -816,44 +807,60 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
   before[tid] = mine + scan - sum;
   __syncthreads();
 
-  // a sequence of no keys: zeros, from one block each
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const Seq s = seq_of(a, b);
-    if (s.bad || s.tiles) continue;
-    for (int i = tid; i < a.Hq * a.dv; i += kThreads)
-      from_float(static_cast<QT*>(a.out) + (size_t)b * a.Hq * a.dv + i, 0.0f);
-    if (a.lse)
-      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)b * a.Hq + i] = -INFINITY;
+  // the block's columns, and this warp's tiles of them in the order (unit,
+  // column): whole parts of units where the units divide the warps
+  const int units = a.Hkv * a.nhb;
+  const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)1);
+  const int64_t c0 = blockIdx.x * run, c1 = min(c0 + run, total);
+  const int ncol = (int)max(c1 - c0, (int64_t)0);
+  int64_t start, count;
+  if (W % units == 0) {
+    const int k = W / units, p = (ncol + k - 1) / k, sub = warp % k;
+    start = (int64_t)(warp / k) * ncol + sub * p;
+    count = min(p, ncol - sub * p);
+  } else {
+    const int64_t all = (int64_t)units * ncol, p = (all + W - 1) / W;
+    start = warp * p;
+    count = min(p, all - start);
   }
 
-  const int units = a.Hkv * a.nhb;
-  total *= units;
-  // tiles per run: at least one, so that a short cache still spreads
-  const int64_t run = max((total + a.warps - 1) / a.warps, (int64_t)1);
-  const int gw = blockIdx.x * W + warp;
-  const int64_t start = gw * run, end = min(start + run, total);
-
-  if (start < end) {
-    Cursor cc;
-    {
-      int lo = 0, hi = kThreads;  // the last thread whose sequences begin at or before start
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (before[mid] * units <= start)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      int64_t rem = start - before[lo] * units;
-      cc.b = lo * per;
-      cc.s = seq_of(a, cc.b);
-      while (cc.b + 1 < a.B && rem >= (int64_t)cc.s.tiles * units) {
-        rem -= (int64_t)cc.s.tiles * units;
-        cc.s = seq_of(a, ++cc.b);
-      }
-      cc.u = (int)(rem / cc.s.tiles);
-      cc.t = (int)(rem - (int64_t)cc.u * cc.s.tiles);
+  auto locate = [&](int64_t col) {  // the sequence and tile of a column
+    int lo = 0, hi = kThreads;  // the last thread whose sequences begin at or before it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= col)
+        lo = mid;
+      else
+        hi = mid;
     }
+    Cursor c;
+    int64_t rem = col - before[lo];
+    c.b = lo * per;
+    c.s = seq_of(a, c.b);
+    while (c.b + 1 < a.B && rem >= c.s.tiles) {
+      rem -= c.s.tiles;
+      c.s = seq_of(a, ++c.b);
+    }
+    c.t = (int)rem;
+    c.col = col;
+    return c;
+  };
+  auto next = [&](Cursor& c) {
+    ++c.t;
+    if (++c.col == c1) {
+      const int u = c.u + 1;
+      c = locate(c0);
+      c.u = u;
+    } else if (c.t == c.s.tiles) {
+      c.t = 0;
+      do c.s = seq_of(a, ++c.b);
+      while (c.s.tiles == 0 && c.b + 1 < a.B);
+    }
+  };
+
+  if (count > 0) {
+    Cursor cc = locate(c0 + start % ncol);
+    cc.u = (int)(start / ncol);
     Cursor pc = cc;
 
     uint8_t* ring = smem + warp * R::kWarpBytes;
@@ -905,14 +912,14 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
             mask;
     };
 
-    const int count = (int)(end - start);
+    const int n = (int)count;
     int issued = 0;
     Lookup pend = look(pc);
     auto feed = [&](int stage) {
-      if (issued < count) {
+      if (issued < n) {
         issue(stage, pend);
-        if (++issued < count) {
-          pc.next(a, units);
+        if (++issued < n) {
+          next(pc);
           pend = look(pc);
         }
       }
@@ -921,16 +928,17 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
 #pragma unroll 1
     for (int s = 0; s < S - 1; ++s) feed(s);
 
-    int stage = 0, seg_t = cc.t;
+    int stage = 0;
+    int64_t seg = cc.col;  // the segment's first column
     bool first_seg = true;
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      if (i == 0 || cc.t == 0) {  // a new unit
+    for (int i = 0; i < n; ++i) {
+      if (i == 0 || cc.t == 0 || cc.col == c0) {  // a new unit or sequence
         const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
         const int h0 = g * a.G + blk * E::kHeads;
         eng.begin(static_cast<const QT*>(a.q) + ((size_t)cc.b * a.Hq + h0) * E::kD,
                   min(E::kHeads, a.G - blk * E::kHeads), a.scale);
-        seg_t = cc.t;
+        seg = cc.col;
       }
       copy_wait<S - 2>();
       __syncwarp();  // every lane's copies of this tile have landed, and the last tile is read
@@ -944,36 +952,78 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
       t.mask = *reinterpret_cast<const uint32_t*>(st + R::kK + R::kV + 2 * R::kScale);
       eng.tile(t);
       if (++stage == S) stage = 0;
-      const bool unit_done = cc.t + 1 == cc.s.tiles;
-      if (unit_done || i + 1 == count) {
+      const bool seq_done = cc.t + 1 == cc.s.tiles;
+      if (seq_done || cc.col + 1 == c1 || i + 1 == n) {
+        const int64_t from = cc.col - cc.t, to = from + cc.s.tiles;
+        const bool had_block = seg == max(from, c0) && cc.col + 1 == min(to, c1);
         const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
         const size_t orow = (size_t)cc.b * a.Hq + g * a.G + blk * E::kHeads;
-        const int slot = first_seg ? 0 : 1;
-        const size_t piece = ((size_t)gw * 2 + slot) * a.hb;
         Sink<QT> out;
-        out.partial = !(unit_done && seg_t == 0);
+        out.partial = !(had_block && from >= c0 && to <= c1);
         out.out = static_cast<QT*>(a.out) + orow * a.dv;
         out.lse = a.lse ? a.lse + orow : nullptr;
-        out.part = a.warp.part + piece * a.dv;
-        out.ml = a.warp.ml + piece * 2;
+        const int slot = first_seg ? 0 : 1;
+        const Pieces to_where = had_block ? a.block : a.warp;
+        const size_t piece =
+            (had_block ? ((size_t)blockIdx.x * 2 + (from < c0 ? 0 : 1)) * units + cc.u
+                       : ((size_t)blockIdx.x * W + warp) * 2 + slot) * a.hb;
+        out.part = to_where.part + piece * a.dv;
+        out.ml = to_where.ml + piece * 2;
         eng.finish(out);
-        if (out.partial && lane == 0)
-          left[2 * warp + slot] = Left{start + i - cc.t, cc.b, cc.u, cc.s.tiles, true};
+        if (!had_block && lane == 0)
+          left[2 * warp + slot] = Left{from, cc.b, cc.u, cc.s.tiles, true};
         first_seg = false;
       }
-      if (i + 1 < count) cc.next(a, units);
+      if (i + 1 < n) next(cc);
     }
     copy_wait<0>();
   }
 
-  // ---- the pieces of this block's warps, joined per unit
+  // sequences of no keys: zeros, from one block each
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Seq s = seq_of(a, b);
+    if (s.bad || s.tiles) continue;
+    for (int i = tid; i < a.Hq * a.dv; i += kThreads)
+      from_float(static_cast<QT*>(a.out) + (size_t)b * a.Hq * a.dv + i, 0.0f);
+    if (a.lse)
+      for (int i = tid; i < a.Hq; i += kThreads) a.lse[(size_t)b * a.Hq + i] = -INFINITY;
+  }
+
+  // what the second launch has to do: by sequence (block b says it of sequence
+  // b), or by block, of the sequence that begins in its columns and goes on
+  if (tid == 0) {
+    Shared s = {0, 0, 0, 0};
+    int64_t from = 0, to = 0;
+    if (a.by_seq) {
+      s.b = blockIdx.x;
+      if (s.b < a.B) {
+        from = before[s.b];  // (one sequence per thread here)
+        to = from + seq_of(a, s.b).tiles;
+      }
+    } else if (ncol) {
+      const Cursor c = locate(c1 - 1);
+      s.b = c.b;
+      from = c.col - c.t;
+      to = from + c.s.tiles;
+      if (from < c0) to = from;
+    }
+    if (to > from) {
+      s.block = (int)(from / run);
+      s.blocks = (int)((to - 1) / run) - s.block + 1;
+      if (s.blocks == 1) s.blocks = 0;
+    }
+    if (!a.by_seq || blockIdx.x < a.B) a.shared[blockIdx.x] = s;
+  }
+
+  // ---- the pieces of this block's warps, joined
   __syncthreads();
   if (warp == 0) {  // lane p: piece p, in the order of the tiles
     const bool any = lane < 2 * W && left[lane].any;
     const uint32_t valid = __ballot_sync(0xffffffffu, any);
     const uint32_t below = valid & ((1u << lane) - 1u);
     const int prev = below ? 31 - __clz(below) : 0;
-    const bool lead = any && (!below || left[lane].from != left[prev].from);
+    const bool lead = any && (!below || left[lane].from != left[prev].from ||
+                              left[lane].u != left[prev].u);
     const uint32_t leads = __ballot_sync(0xffffffffu, lead);
     if (any) order[__popc(below)] = lane;
     if (lead) group0[__popc(leads & ((1u << lane) - 1u))] = __popc(below);
@@ -983,12 +1033,11 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
     }
   }
   __syncthreads();
-  const int64_t block_start = (int64_t)blockIdx.x * W * run, block_end = block_start + W * run;
   const int cols = a.dv >> 2, per_group = a.hb * cols;
   for (int item = tid; item < groups * per_group; item += kThreads) {
     const int gi = item / per_group, rest = item - gi * per_group;
     const int h = rest / cols, c4 = rest - h * cols;
-    const int p0 = group0[gi], n = group0[gi + 1] - p0;
+    const int p0 = group0[gi], np = group0[gi + 1] - p0;
     const Left f = left[order[p0]];
     const int g = f.u / a.nhb, blk = f.u - g * a.nhb;
     if (h >= a.G - blk * E::kHeads) continue;
@@ -996,37 +1045,26 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
     float l = 0.0f, mx = -INFINITY;
     auto row = [&](int i) { return ((size_t)blockIdx.x * 2 * W + order[p0 + i]) * a.hb + h; };
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) mx = fmaxf(mx, a.warp.ml[row(i) * 2]);
+    for (int i = 0; i < np; ++i) mx = fmaxf(mx, a.warp.ml[row(i) * 2]);
     const float base = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < np; ++i) {
       const size_t p = row(i);
       add_piece(o, l, *reinterpret_cast<const float2*>(a.warp.ml + p * 2),
                 *reinterpret_cast<const float4*>(a.warp.part + p * a.dv + c4 * 4), base);
     }
-    if (f.from >= block_start && f.from + f.tiles <= block_end) {
+    if (f.from >= c0 && f.from + f.tiles <= c1) {
       const size_t orow = (size_t)f.b * a.Hq + g * a.G + blk * E::kHeads + h;
       const float r = inverse_sum(l);
       const float y[4] = {o.x * r, o.y * r, o.z * r, o.w * r};
       store_quad(static_cast<QT*>(a.out) + orow * a.dv + c4 * 4, y);
       if (a.lse && c4 == 0) a.lse[orow] = log_sum(mx, l);
     } else {
-      const size_t p = ((size_t)blockIdx.x * 2 + (f.from < block_start ? 0 : 1)) * a.hb + h;
+      const size_t p =
+          (((size_t)blockIdx.x * 2 + (f.from < c0 ? 0 : 1)) * units + f.u) * a.hb + h;
       *reinterpret_cast<float4*>(a.block.part + p * a.dv + c4 * 4) = o;
       if (c4 == 0) *reinterpret_cast<float2*>(a.block.ml + p * 2) = make_float2(mx, l);
     }
-  }
-  if (tid == 0) {  // only the last unit of the block can begin in it and go on
-    Shared s = {0, 0, 0, 0};
-    if (groups) {
-      const Left f = left[order[group0[groups] - 1]];
-      if (f.from >= block_start && f.from + f.tiles > block_end) {
-        s.b = f.b;
-        s.u = f.u;
-        s.blocks = (int)((f.from + f.tiles - 1) / (W * run)) - blockIdx.x + 1;
-      }
-    }
-    a.shared[blockIdx.x] = s;
   }
 }
 
