@@ -8,12 +8,13 @@ namespace paged {
 namespace {
 
 // Block (x, y): entry x of shared[], query heads y per .. y per + per - 1, with
-// kJoin / per threads each.  A head's pieces are weighted by exp2(their maximum
+// an equal share of the threads each.  A head's pieces are weighted by exp2(their maximum
 // - the largest) and added in the order of the blocks: four columns per lane,
-// groups of lanes taking the pieces in turn.  One head per block where the
-// entries are few (one long sequence has a piece in every block of the first
-// launch), eight where they are many (and mostly of two or three pieces).
-constexpr int kJoin = 256, kJoinHeads = 8;
+// groups of lanes taking the pieces in turn.  One head per block of 1024 where
+// the entries are few (one long sequence has a piece in every block of the
+// first launch), eight per block of 256 where they are many (and mostly of two
+// or three pieces).
+constexpr int kJoin = 1024;  // threads, at most
 
 struct JoinArgs {
   DecodeArgs a;
@@ -29,7 +30,7 @@ __global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const JoinArgs j) 
   __shared__ float4 acc_s[kJoin];
   __shared__ float l_s[kJoin], m_s[kJoin];
   const DecodeArgs& a = j.a;
-  const int share = kJoin / j.per, tid = threadIdx.x % share;
+  const int share = blockDim.x / j.per, tid = threadIdx.x % share;
   const int h = blockIdx.y * j.per + threadIdx.x / share;
   const int lanes = a.dv >> 2, groups = share / lanes, c4 = tid % lanes, grp = tid / lanes;
   // every block waits, so that this launch ends after the first one has
@@ -89,14 +90,14 @@ bool pools_within(const lt_kv_cache_t* c, size_t bytes) {
   return s[0].n <= bytes && s[1].n <= bytes;
 }
 
-// query heads per unit and warps per block: the engines' kHeads and kWarps
+// query heads per unit, warps per block and tokens per tile: the engines'
+// kHeads, kWarps and kTile
 int heads_per_unit(lt_dtype_t t, int G) {
   const int most = t == LT_F32 ? 8 : 16;
   return G < most ? G : most;
 }
-int block_warps(lt_dtype_t t, lt_kv_dtype_t kv, int G) {
-  return t == LT_F32 ? 4 : eight_bit(kv) && G <= 8 ? 16 : 8;
-}
+int block_warps(lt_dtype_t t) { return t == LT_F32 ? 4 : 8; }
+int tile_tokens(lt_dtype_t t, lt_kv_dtype_t kv) { return t != LT_F32 && eight_bit(kv) ? 32 : 16; }
 
 // the workspace, one block of the first launch per SM: pieces of its warps
 // (two each), of its units (two each), and an entry for the second launch
@@ -105,10 +106,10 @@ struct Sizes {
   size_t floats;       // of a piece
   size_t bytes;
 };
-Sizes sizes_of(lt_dtype_t t, lt_kv_dtype_t kv, int H_q, int H_kv, int dv, int sms) {
+Sizes sizes_of(lt_dtype_t t, int H_q, int H_kv, int dv, int sms) {
   const int G = H_q / H_kv, hb = heads_per_unit(t, G), nhb = (G + hb - 1) / hb;
   Sizes z;
-  z.warp = (size_t)sms * block_warps(t, kv, G) * 2;
+  z.warp = (size_t)sms * block_warps(t) * 2;
   z.block = (size_t)sms * 2 * H_kv * nhb;
   z.floats = (size_t)hb * (dv + 2);
   z.bytes = (z.warp + z.block) * z.floats * sizeof(float) + (size_t)sms * sizeof(Shared);
@@ -132,7 +133,7 @@ extern "C" lt_status_t lt_paged_attn_decode_plan(int H_q, int H_kv, int d, int d
     return LT_ERR_INVALID_ARG;
   if (num_sms <= 0) num_sms = device_sm_count();
   if (num_sms <= 0) return LT_ERR_CUDA;
-  *workspace_bytes = sizes_of(dtype, kv_dtype, H_q, H_kv, dv, num_sms).bytes;
+  *workspace_bytes = sizes_of(dtype, H_q, H_kv, dv, num_sms).bytes;
   return LT_OK;
 }
 
@@ -157,7 +158,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
     return LT_ERR_INVALID_ARG;
   // pools are addressed in 32 bits of 16 bytes, and a warp's tiles counted in 31
   const int64_t most = (int64_t)max_pages * cache->page_size;
-  const int64_t tiles = ((most < 0x7fffffff ? most : 0x7fffffff) / kTokens + 1) * H_q;
+  const int64_t tiles = ((most < 0x7fffffff ? most : 0x7fffffff) / 16 + 1) * H_q;
   if (!pools_within(cache, (size_t)64 << 30) || tiles > ((int64_t)1 << 40) / B)
     return LT_ERR_INVALID_ARG;
   const size_t es = dtype_size(dtype);
@@ -184,7 +185,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.G = H_q / cache->H_kv;
   a.hb = heads_per_unit(dtype, a.G);
   a.nhb = (a.G + a.hb - 1) / a.hb;
-  const Sizes z = sizes_of(dtype, cache->dtype, H_q, cache->H_kv, cache->dv, sms);
+  const Sizes z = sizes_of(dtype, H_q, cache->H_kv, cache->dv, sms);
   Workspace w;
   const lt_status_t sw = w.take(workspace, workspace_bytes, z.bytes, (cudaStream_t)stream);
   if (sw != LT_OK) return sw;
@@ -200,6 +201,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.vpg = (uint32_t)(cache->v_page_stride * ks / 16);
   a.vsl = (uint32_t)(cache->v_slot_stride * ks / 16);
   a.vhd = (uint32_t)(cache->v_head_stride * ks / 16);
+  a.same = a.kpg == a.vpg && a.ksl == a.vsl && a.khd == a.vhd;
   a.table = block_table;
   a.table_stride = table_stride;
   a.lens = seq_lens;
@@ -212,6 +214,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
   a.page_magic = (uint32_t)(((uint64_t)1 << (31 + a.page_shift)) / a.page_size + 1);
   a.window = window;
+  a.tile = tile_tokens(dtype, cache->dtype);
   a.scale = scale;
   a.out = out;
   a.lse = lse;
@@ -232,9 +235,10 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
                                     : launch_f32(a, cache->dtype, cache->d, sms, s);
   if (e == cudaSuccess) {
     const int entries = a.by_seq ? B : sms;
-    const JoinArgs j = {a, entries * H_q <= 4 * sms ? 1 : kJoinHeads};
-    e = launch_dependent(lt_paged_join_kernel, dim3(entries, (H_q + j.per - 1) / j.per), kJoin, 0,
-                         s, j);
+    const bool few = entries * H_q <= 2 * sms;
+    const JoinArgs j = {a, few ? 1 : 8};
+    e = launch_dependent(lt_paged_join_kernel, dim3(entries, (H_q + j.per - 1) / j.per),
+                         few ? kJoin : 256, 0, s, j);
   }
   const cudaError_t f = w.release();
   if (e == cudaSuccess) e = f;

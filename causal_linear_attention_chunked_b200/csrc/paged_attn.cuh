@@ -11,7 +11,7 @@
 // Bound by memory: every key and value is read once, for G <= 16 query heads,
 // 2G flops per byte of a 16-bit cache.
 //
-// Split: all sequences' tiles of kTokens tokens, laid end to end, are dealt out
+// Split: all sequences' tiles of 16 or 32 tokens, laid end to end, are dealt out
 // in equal runs to the blocks of one launch, one per SM, whatever the lengths:
 // a batch of very different sequences and one long sequence load the SMs
 // alike, and the workspace does not grow with either.  Inside a block the
@@ -46,7 +46,6 @@ namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kTokens = 16;  // tokens per tile, in every engine
 
 struct E4M3 {
   uint8_t b;
@@ -74,6 +73,7 @@ struct DecodeArgs {
   const float* ks;
   const float* vs;
   uint32_t kpg, ksl, khd, vpg, vsl, vhd;  // pool strides, in 16 bytes
+  int same;                               // the two pools' strides are the same
   const int32_t* table;
   int64_t table_stride;
   const int32_t* lens;
@@ -82,6 +82,7 @@ struct DecodeArgs {
   int num_pages, page_size, max_pages, window;
   uint32_t page_magic;  // floor(2^(31 + page_shift) / page_size) + 1
   int page_shift;       // ceil(log2(page_size))
+  int tile;             // tokens per tile (the engine's kTile)
   int by_seq;           // shared[] goes by sequence (else by first block)
   float scale;
   void* out;
@@ -105,7 +106,7 @@ __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b) {
   s.bad = s.len < 0 || (int64_t)s.len > min((int64_t)a.max_pages * a.page_size, (int64_t)0x7fffff00);
   if (s.bad) s.len = 0;
   s.first = a.window ? max(0, s.len - a.window) : 0;
-  s.tiles = (s.len - s.first + kTokens - 1) / kTokens;
+  s.tiles = (s.len - s.first + a.tile - 1) / a.tile;
   return s;
 }
 
@@ -117,6 +118,9 @@ __device__ __forceinline__ int page_of(const DecodeArgs& a, int pos) {
 }
 
 // --------------------------------------------------------------- copies
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   const int n = live ? 16 : 0;  // the rest of the 16 bytes is zero-filled
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
@@ -142,12 +146,27 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   constexpr int kMask = (RB >= 128 ? 8 : RB / 16) - 1;  // chunks permuted among
   return (uint32_t)(r * RB + ((c ^ ((r / kPer) & kMask)) << 4));
 }
+// chunk c + dc of the same row, at being chunk c's address and dc a multiple of
+// a power of two above c: the permutation is an exclusive or, so one suffices
+// (tiles begin at multiples of 128 bytes)
+__device__ __forceinline__ uint32_t chunk_on(uint32_t at, int dc) {
+  return (at ^ ((dc & 7) << 4)) + ((dc & ~7) << 4);
+}
+// A warp copies a tile 512 bytes at a time: row and chunk of this lane in the
+// first step, and step i's address from the first one's.
+template <int RB>
+__device__ __forceinline__ uint32_t step_at(uint32_t first, int i) {
+  constexpr int kRows = 512 / RB;  // rows per step
+  constexpr int kPer = RB >= 128 ? 1 : 128 / RB;
+  constexpr int kMask = (RB >= 128 ? 8 : RB / 16) - 1;
+  return (first ^ (((i * kRows / kPer) & kMask) << 4)) + i * 512;
+}
 
 __device__ __forceinline__ float exp2_fast(float x) { return ex2_approx(x); }
 
 // What an engine is told of a tile in shared memory.
 struct TileAt {
-  uint32_t k, v;     // shared addresses of the two tiles
+  uint32_t k, v;     // shared addresses of the two tiles (multiples of 128)
   const float* ks;   // scales of the tile's tokens (8-bit caches)
   const float* vs;
   uint32_t mask;     // tokens that take part
@@ -335,9 +354,11 @@ struct MmaEngine {
   static constexpr bool kQuant = Kv::kQuant;
   static constexpr bool kHalf = !__is_same(MT, __nv_bfloat16);
   static constexpr bool kSplit = !kQuant || __is_same(QT, __half);
-  // 8-bit tiles are half the bytes and as many instructions: twice the warps
-  // (which the registers of one block of heads allow) hide their latency
-  static constexpr int kD = D, kHeads = 8 * kNB, kTile = kTokens, kWarps = kQuant && kNB == 1 ? 16 : 8;
+  // 8 KB per tile at width 128 for either size of element: 32 tokens of 8 bits
+  // share a tile's bookkeeping (16 of them, with 16 warps, issued a third more
+  // instructions per token)
+  static constexpr int kD = D, kHeads = 8 * kNB, kTile = kQuant ? 32 : 16, kWarps = 8;
+  static constexpr int kHalves = kTile / 16;
   static constexpr int kKRow = D * Kv::kBytes, kVRow = DV * Kv::kBytes;  // bytes
   static constexpr int kExtra = 0;  // shared bytes per warp beside the ring
   static constexpr float kShift = kHalf ? 12.0f : 0.0f;
@@ -400,8 +421,10 @@ struct MmaEngine {
     }
   }
 
+  using Scores = float[kNB][kHalves][4];
+
   // the maximum (and A) moved: what is summed so far goes by the new ones
-  __device__ __forceinline__ void rescale(const float (*s)[4], uint32_t top) {
+  __device__ __forceinline__ void rescale(const Scores& s, uint32_t top) {
     top = __reduce_max_sync(0xffffffffu, top);
     const float fa = kQuant ? __uint_as_float(vtop) * __uint_as_float(0x7f000000u - top) : 1.0f;
     vtop = top;
@@ -409,7 +432,9 @@ struct MmaEngine {
     for (int b = 0; b < kNB; ++b)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(m[b][e], fmaxf(s[b][e], s[b][2 + e]));
+        float mx = m[b][e];
+#pragma unroll
+        for (int y = 0; y < kHalves; ++y) mx = fmaxf(mx, fmaxf(s[b][y][e], s[b][y][2 + e]));
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -425,9 +450,9 @@ struct MmaEngine {
       }
   }
 
-  __device__ __forceinline__ void tile(const TileAt& t) {
-    const int lane = threadIdx.x & 31, r = lane >> 2;
-    float s[kNB][4], s2[kNB][4];  // even and odd steps: two chains of products
+  // S^T of 16 tokens, times the heads' factors; `at`: see tile()
+  __device__ __forceinline__ void scores(float (*s)[4], uint32_t at) {
+    float s2[kNB][4];  // even and odd steps: two chains of products
 #pragma unroll
     for (int b = 0; b < kNB; ++b)
 #pragma unroll
@@ -436,11 +461,11 @@ struct MmaEngine {
     for (int i = 0; i < D / 16; i += 2) {
       uint32_t a0[4], a1[4];
       if constexpr (!kQuant) {
-        ldsm4(a0, t.k + chunk_at<kKRow>(lane & 15, 2 * i + (lane >> 4)));
-        ldsm4(a1, t.k + chunk_at<kKRow>(lane & 15, 2 * i + 2 + (lane >> 4)));
+        ldsm4(a0, chunk_on(at, 2 * i));
+        ldsm4(a1, chunk_on(at, 2 * i + 2));
       } else {
         uint32_t w[4];
-        ldsm4(w, t.k + chunk_at<kKRow>(lane & 15, i + (lane >> 4)));
+        ldsm4(w, chunk_on(at, i));
         widen4<false>(w[0], a0[0], a0[2], KT());
         widen4<false>(w[1], a0[1], a0[3], KT());
         widen4<false>(w[2], a1[0], a1[2], KT());
@@ -452,71 +477,24 @@ struct MmaEngine {
         mma<MT>(s2[b], a1, qf[b][i + 1][0], qf[b][i + 1][1]);
       }
     }
-    // scores in units of log 2; tokens that take no part get -infinity
-    const bool live0 = (t.mask >> r) & 1u, live1 = (t.mask >> (r + 8)) & 1u;
-    float k0 = 1.0f, k1 = 1.0f, v0 = 1.0f, v1 = 1.0f;
-    uint32_t top = vtop;
-    if constexpr (kQuant) {
-      k0 = t.ks[r];
-      k1 = t.ks[r + 8];
-      v0 = t.vs[r];
-      v1 = t.vs[r + 8];
-      // A: the next power of two of the largest scale, within 2^-126 .. 2^126
-      // (the scales of tokens that take no part are zeros)
-      uint32_t v = max(__float_as_uint(v0) & 0x7fffffffu, __float_as_uint(v1) & 0x7fffffffu);
-      v = v >= 0x7e800000u ? 0x7e800000u : (v + 0x7fffffu) & 0x7f800000u;
-      top = max(top, v);
-    }
-    bool moved = top != vtop;
 #pragma unroll
     for (int b = 0; b < kNB; ++b)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[b][e] = live0 ? (s[b][e] + s2[b][e]) * (sl2[b][e] * k0) : -INFINITY;
-        s[b][2 + e] = live1 ? (s[b][2 + e] + s2[b][2 + e]) * (sl2[b][e] * k1) : -INFINITY;
-        moved |= fmaxf(s[b][e], s[b][2 + e]) > m[b][e];
-      }
-    if (__any_sync(0xffffffffu, moved)) rescale(s, top);
-    if constexpr (kQuant) {
-      const float inv_a = __uint_as_float(0x7f000000u - vtop);
-      v0 *= inv_a;
-      v1 *= inv_a;
-    }
-    uint32_t hi[kNB][2], lo[kNB][2];
-#pragma unroll
-    for (int b = 0; b < kNB; ++b) {
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float base = (m[b][e] == -INFINITY ? 0.0f : m[b][e]) - kShift;
-        p[e] = exp2_fast(s[b][e] - base);
-        p[2 + e] = exp2_fast(s[b][2 + e] - base);
-        l[b][e] += p[e] + p[2 + e];
-        if constexpr (kQuant) {
-          p[e] *= v0;
-          p[2 + e] *= v1;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t w = pack2<MT>(p[2 * u], p[2 * u + 1]);
-        hi[b][u] = transpose8(w);
-        if constexpr (kSplit) {
-          const float2 x = unpack2<MT>(w);
-          lo[b][u] = transpose8(pack2<MT>(p[2 * u] - x.x, p[2 * u + 1] - x.y));
-        }
-      }
-    }
+      for (int e = 0; e < 4; ++e) s[b][e] = (s[b][e] + s2[b][e]) * sl2[b][e & 1];
+  }
+
+  // O^T += V^T P^T of 16 tokens, their weights' tiles hi (and lo)
+  __device__ __forceinline__ void values(uint32_t at, const uint32_t (*hi)[2],
+                                         const uint32_t (*lo)[2]) {
 #pragma unroll
     for (int j = 0; j < DV / 16; j += 2) {
       uint32_t a0[4], a1[4];
       if constexpr (!kQuant) {
-        const int row = (lane & 7) + ((lane >> 4) << 3), ch = 2 * j + ((lane >> 3) & 1);
-        ldsm4t(a0, t.v + chunk_at<kVRow>(row, ch));
-        ldsm4t(a1, t.v + chunk_at<kVRow>(row, ch + 2));
+        ldsm4t(a0, chunk_on(at, 2 * j));
+        ldsm4t(a1, chunk_on(at, 2 * j + 2));
       } else {
         uint32_t w[4];
-        ldsm4t(w, t.v + chunk_at<kVRow>(lane & 15, j + (lane >> 4)));
+        ldsm4t(w, chunk_on(at, j));
         widen4<true>(w[0], a0[0], a0[1], KT());
         widen4<true>(w[1], a0[2], a0[3], KT());
         widen4<true>(w[2], a1[0], a1[1], KT());
@@ -532,6 +510,92 @@ struct MmaEngine {
         }
       }
     }
+  }
+
+  __device__ __forceinline__ void tile(const TileAt& t) {
+    const int lane = threadIdx.x & 31, r = lane >> 2;
+    // where this lane points the loads of four 8 x 8 tiles: tokens of the first
+    // two chunks of K's rows, and of V's (its 16-bit tiles turned token-first)
+    const uint32_t k_at = t.k + chunk_at<kKRow>(lane & 15, lane >> 4);
+    const uint32_t v_at =
+        t.v + (kQuant ? chunk_at<kVRow>(lane & 15, lane >> 4)
+                      : chunk_at<kVRow>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
+    Scores s;  // in units of log 2
+    float vs[kHalves][2];
+    uint32_t top = vtop;
+#pragma unroll
+    for (int y = 0; y < kHalves; ++y) {
+      float x[kNB][4];
+      scores(x, k_at + y * 16 * kKRow);
+      if constexpr (kQuant) {
+        const float k0 = t.ks[16 * y + r], k1 = t.ks[16 * y + r + 8];
+#pragma unroll
+        for (int b = 0; b < kNB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[b][e] *= e < 2 ? k0 : k1;
+        vs[y][0] = t.vs[16 * y + r];
+        vs[y][1] = t.vs[16 * y + r + 8];
+        // (the scales of tokens that take no part are zeros)
+        top = max(top, __float_as_uint(vs[y][0]) & 0x7fffffffu);
+        top = max(top, __float_as_uint(vs[y][1]) & 0x7fffffffu);
+      }
+#pragma unroll
+      for (int b = 0; b < kNB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[b][y][e] = x[b][e];
+    }
+    if constexpr (kQuant)  // A: the next power of two, within 2^-126 .. 2^126
+      top = top >= 0x7e800000u ? 0x7e800000u : (top + 0x7fffffu) & 0x7f800000u;
+    if (t.mask != (kTile == 32 ? 0xffffffffu : (1u << (kTile & 31)) - 1u)) {
+      // tokens that take no part get -infinity
+#pragma unroll
+      for (int y = 0; y < kHalves; ++y)
+#pragma unroll
+        for (int b = 0; b < kNB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!((t.mask >> (16 * y + r + (e & 2 ? 8 : 0))) & 1u)) s[b][y][e] = -INFINITY;
+    }
+    bool moved = top != vtop;
+#pragma unroll
+    for (int b = 0; b < kNB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(s[b][0][e], s[b][0][2 + e]);
+#pragma unroll
+        for (int y = 1; y < kHalves; ++y) mx = fmaxf(mx, fmaxf(s[b][y][e], s[b][y][2 + e]));
+        moved |= mx > m[b][e];
+      }
+    if (__any_sync(0xffffffffu, moved)) rescale(s, top);
+    const float inv_a = __uint_as_float(0x7f000000u - vtop);
+    uint32_t hi[kHalves][kNB][2], lo[kHalves][kNB][2];
+#pragma unroll
+    for (int b = 0; b < kNB; ++b) {
+      const float base[2] = {(m[b][0] == -INFINITY ? 0.0f : m[b][0]) - kShift,
+                             (m[b][1] == -INFINITY ? 0.0f : m[b][1]) - kShift};
+#pragma unroll
+      for (int y = 0; y < kHalves; ++y)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {  // token r, token r + 8
+          float p0 = exp2_fast(s[b][y][2 * u] - base[0]);
+          float p1 = exp2_fast(s[b][y][2 * u + 1] - base[1]);
+          l[b][0] += p0;
+          l[b][1] += p1;
+          if constexpr (kQuant) {
+            const float f = vs[y][u] * inv_a;
+            p0 *= f;
+            p1 *= f;
+          }
+          const uint32_t w = pack2<MT>(p0, p1);
+          hi[y][b][u] = transpose8(w);
+          if constexpr (kSplit) {
+            const float2 x = unpack2<MT>(w);
+            lo[y][b][u] = transpose8(pack2<MT>(p0 - x.x, p1 - x.y));
+          }
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < kHalves; ++y) values(v_at + y * 16 * kVRow, hi[y], lo[y]);
   }
 
   __device__ __forceinline__ void finish(const Sink<QT>& out) {
@@ -600,7 +664,7 @@ template <typename KT, int D, int DV>
 struct FmaEngine {
   using QT = float;
   static constexpr int kBytes = sizeof(KT);
-  static constexpr int kD = D, kHeads = 8, kTile = kTokens, kWarps = 4;
+  static constexpr int kD = D, kHeads = 8, kTile = 16, kWarps = 4;
   static constexpr int kKRow = D * kBytes, kVRow = DV * kBytes;
   static constexpr bool kQuant = kBytes == 1;
   static constexpr int kExtra = kHeads * (D + kTile) * 4;  // queries, weights
@@ -745,10 +809,9 @@ struct Ring {
 };
 
 // A tile of a block's run of columns [c0, c1) (a column: one tile of one
-// sequence, for every unit): unit u, column col, tile t of sequence b.
+// sequence, for every unit): unit u, column c0 + col, tile t of sequence b.
 struct Cursor {
-  int b, u, t;
-  int64_t col;
+  int b, u, t, col;
   Seq s;
 };
 
@@ -842,12 +905,12 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
       c.s = seq_of(a, ++c.b);
     }
     c.t = (int)rem;
-    c.col = col;
+    c.col = (int)(col - c0);
     return c;
   };
   auto next = [&](Cursor& c) {
     ++c.t;
-    if (++c.col == c1) {
+    if (++c.col == ncol) {
       const int u = c.u + 1;
       c = locate(c0);
       c.u = u;
@@ -869,6 +932,11 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
     eng.init(ring + R::kStage * S);
 
     const int row = lane & (TILE - 1);
+    constexpr uint32_t kFull = TILE == 32 ? 0xffffffffu : (1u << (TILE & 31)) - 1u;
+    constexpr int kc = E::kKRow / 16, vc = E::kVRow / 16;  // chunks per row
+    const uint8_t *k_lane = a.k + lane % kc * 16, *v_lane = a.v + lane % vc * 16;
+    const uint32_t k_first = chunk_at<E::kKRow>(lane / kc, lane % kc);
+    const uint32_t v_first = chunk_at<E::kVRow>(lane / vc, lane % vc);
     auto look = [&](const Cursor& c) {
       Lookup p;
       const int pos = c.s.first + c.t * TILE + row;
@@ -885,27 +953,39 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
         report_error(a.err, kDevErrBadPage);
         live = false;
       }
-      const uint32_t mask = __ballot_sync(0xffffffffu, live) & ((1u << TILE) - 1u);
+      const uint32_t mask = __ballot_sync(0xffffffffu, live) & kFull;
       const uint32_t page = live ? p.page : 0, slot = live ? p.slot : 0;
       const uint32_t ko = page * a.kpg + slot * a.ksl + p.g * a.khd;
-      const uint32_t vo = page * a.vpg + slot * a.vsl + p.g * a.vhd;
+      const uint32_t vo = a.same ? ko : page * a.vpg + slot * a.vsl + p.g * a.vhd;
       const uint32_t dst = ring_u + stage * R::kStage;
-      constexpr int kc = E::kKRow / 16, vc = E::kVRow / 16;  // chunks per row
+      if (mask == kFull && a.same && E::kKRow == E::kVRow) {  // nearly always
 #pragma unroll
-      for (int i = 0; i < TILE * kc / 32; ++i) {
-        const int r = i * (32 / kc) + lane / kc, c = lane % kc;
-        const uint32_t off = __shfl_sync(0xffffffffu, ko, r) + c;
-        copy16(dst + chunk_at<E::kKRow>(r, c), a.k + (uint64_t)off * 16, (mask >> r) & 1u);
-      }
+        for (int i = 0; i < TILE * kc / 32; ++i) {
+          const int r = i * (32 / kc) + lane / kc;
+          const uint64_t off = (uint64_t)__shfl_sync(0xffffffffu, ko, r) * 16;
+          copy16(step_at<E::kKRow>(dst + k_first, i), k_lane + off);
+          copy16(step_at<E::kKRow>(dst + k_first, i) + R::kK, v_lane + off);
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < TILE * vc / 32; ++i) {
-        const int r = i * (32 / vc) + lane / vc, c = lane % vc;
-        const uint32_t off = __shfl_sync(0xffffffffu, vo, r) + c;
-        copy16(dst + R::kK + chunk_at<E::kVRow>(r, c), a.v + (uint64_t)off * 16, (mask >> r) & 1u);
+        for (int i = 0; i < TILE * kc / 32; ++i) {
+          const int r = i * (32 / kc) + lane / kc;
+          const uint64_t off = (uint64_t)__shfl_sync(0xffffffffu, ko, r) * 16;
+          copy16(step_at<E::kKRow>(dst + k_first, i), k_lane + off, (mask >> r) & 1u);
+        }
+#pragma unroll
+        for (int i = 0; i < TILE * vc / 32; ++i) {
+          const int r = i * (32 / vc) + lane / vc;
+          const uint64_t off = (uint64_t)__shfl_sync(0xffffffffu, vo, r) * 16;
+          copy16(step_at<E::kVRow>(dst + R::kK + v_first, i), v_lane + off, (mask >> r) & 1u);
+        }
       }
-      if constexpr (E::kQuant) {  // lanes 0 .. 15 the keys' scales, 16 .. 31 the values'
+      if constexpr (E::kQuant) {
         const int64_t at = ((int64_t)page * a.Hkv + p.g) * a.page_size + slot;
-        copy4(dst + R::kK + R::kV + lane * 4, (lane < TILE ? a.ks : a.vs) + at, live);
+        if (lane < TILE) {
+          copy4(dst + R::kK + R::kV + lane * 4, a.ks + at, live);
+          copy4(dst + R::kK + R::kV + R::kScale + lane * 4, a.vs + at, live);
+        }
       }
       if (lane == 0)
         *reinterpret_cast<uint32_t*>(ring + stage * R::kStage + R::kK + R::kV + 2 * R::kScale) =
@@ -929,11 +1009,11 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
     for (int s = 0; s < S - 1; ++s) feed(s);
 
     int stage = 0;
-    int64_t seg = cc.col;  // the segment's first column
+    int seg = cc.col;  // the segment's first column
     bool first_seg = true;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      if (i == 0 || cc.t == 0 || cc.col == c0) {  // a new unit or sequence
+      if (i == 0 || cc.t == 0 || cc.col == 0) {  // a new unit or sequence
         const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
         const int h0 = g * a.G + blk * E::kHeads;
         eng.begin(static_cast<const QT*>(a.q) + ((size_t)cc.b * a.Hq + h0) * E::kD,
@@ -953,9 +1033,9 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
       eng.tile(t);
       if (++stage == S) stage = 0;
       const bool seq_done = cc.t + 1 == cc.s.tiles;
-      if (seq_done || cc.col + 1 == c1 || i + 1 == n) {
-        const int64_t from = cc.col - cc.t, to = from + cc.s.tiles;
-        const bool had_block = seg == max(from, c0) && cc.col + 1 == min(to, c1);
+      if (seq_done || cc.col + 1 == ncol || i + 1 == n) {
+        const int64_t from = c0 + cc.col - cc.t, to = from + cc.s.tiles;
+        const bool had_block = c0 + seg == max(from, c0) && c0 + cc.col + 1 == min(to, c1);
         const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
         const size_t orow = (size_t)cc.b * a.Hq + g * a.G + blk * E::kHeads;
         Sink<QT> out;
@@ -1003,7 +1083,7 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
     } else if (ncol) {
       const Cursor c = locate(c1 - 1);
       s.b = c.b;
-      from = c.col - c.t;
+      from = c1 - 1 - c.t;
       to = from + c.s.tiles;
       if (from < c0) to = from;
     }
@@ -1070,6 +1150,7 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
 
 template <typename E>
 cudaError_t launch_engine(const DecodeArgs& a, int sms, cudaStream_t stream) {
+  if (a.tile != E::kTile) return cudaErrorInvalidValue;  // the workspace's sizes go by them
   auto kern = lt_paged_decode_kernel<E>;
   constexpr int smem = Ring<E>::kBytes;
   const cudaError_t e =

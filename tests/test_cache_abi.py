@@ -155,7 +155,7 @@ def test_plans():
     # 16 query heads per unit at most: four units of one KV head
     assert n.value == 148 * ((8 + 4) * 2 * 16 * (128 + 2) * 4 + 16)
     assert lib.lt_paged_attn_decode_plan(8, 8, 64, 128, 1, 3, 148, ctypes.byref(n)) == 0
-    assert n.value == 148 * ((16 + 8) * 2 * 1 * (128 + 2) * 4 + 16)
+    assert n.value == 148 * ((8 + 8) * 2 * 1 * (128 + 2) * 4 + 16)
     for args, st in (((32, 5, 128, 128, 1, 1, 148), 1), ((32, 8, 96, 128, 1, 1, 148), 2),
                      ((32, 8, 128, 128, 1, 2, 148), 2), ((32, 8, 128, 128, 3, 3, 148), 2),
                      ((0, 8, 128, 128, 1, 1, 148), 1)):
