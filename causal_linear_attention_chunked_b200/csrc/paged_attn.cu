@@ -47,15 +47,11 @@ __global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const JoinArgs j) 
     auto row = [&](int i) {
       return (((size_t)(s.block + i) * 2 + (i == 0 ? 1 : 0)) * units + u) * a.hb + hh - blk * a.hb;
     };
-    // each group by its own maximum
-#pragma unroll 4
-    for (int i = grp; i < n; i += groups) mx = fmaxf(mx, a.block.ml[row(i) * 2]);
-    const float base = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll 4
     for (int i = grp; i < n; i += groups) {
       const size_t p = row(i);
-      add_piece(o, l, *reinterpret_cast<const float2*>(a.block.ml + p * 2),
-                *reinterpret_cast<const float4*>(a.block.part + p * a.dv + c4 * 4), base);
+      add_piece(o, l, mx, *reinterpret_cast<const float2*>(a.block.ml + p * 2),
+                *reinterpret_cast<const float4*>(a.block.part + p * a.dv + c4 * 4));
     }
   }
   acc_s[threadIdx.x] = o;
@@ -64,13 +60,9 @@ __global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const JoinArgs j) 
   __syncthreads();
   if (grp != 0 || h >= a.Hq) return;
   const int at0 = threadIdx.x;  // this column's groups are `lanes` apart
-  for (int q = 1; q < groups; ++q) mx = fmaxf(mx, m_s[at0 + q * lanes]);
-  const float base = mx == -INFINITY ? 0.0f : mx;
-  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  l = 0.0f;
-  for (int q = 0; q < groups; ++q)
-    add_piece(o, l, make_float2(m_s[at0 + q * lanes], l_s[at0 + q * lanes]), acc_s[at0 + q * lanes],
-              base);
+  for (int q = 1; q < groups; ++q)
+    add_piece(o, l, mx, make_float2(m_s[at0 + q * lanes], l_s[at0 + q * lanes]),
+              acc_s[at0 + q * lanes]);
   const float f = inverse_sum(l);
   const float y[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
   const size_t orow = (size_t)s.b * a.Hq + h;

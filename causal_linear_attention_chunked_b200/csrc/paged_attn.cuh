@@ -258,14 +258,17 @@ __device__ __forceinline__ float log_sum(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// one more piece (maximum and sum ml, values x) relative to 2^base
-__device__ __forceinline__ void add_piece(float4& o, float& l, float2 ml, float4 x, float base) {
-  const float f = exp2f(ml.x - base);
-  l = fmaf(f, ml.y, l);
-  o.x = fmaf(f, x.x, o.x);
-  o.y = fmaf(f, x.y, o.y);
-  o.z = fmaf(f, x.z, o.z);
-  o.w = fmaf(f, x.w, o.w);
+// one more piece: values x, maximum and sum ml; what is joined so far (o, l,
+// relative to 2^mx) and the piece both go by the larger maximum
+__device__ __forceinline__ void add_piece(float4& o, float& l, float& mx, float2 ml, float4 x) {
+  const float top = fmaxf(mx, ml.x), base = top == -INFINITY ? 0.0f : top;
+  const float f = exp2f(mx - base), g = exp2f(ml.x - base);
+  mx = top;
+  l = fmaf(g, ml.y, f * l);
+  o.x = fmaf(g, x.x, f * o.x);
+  o.y = fmaf(g, x.y, f * o.y);
+  o.z = fmaf(g, x.z, f * o.z);
+  o.w = fmaf(g, x.w, f * o.w);
 }
 
 // --------------------------------------------------- engine: tensor cores
@@ -1125,13 +1128,10 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
     float l = 0.0f, mx = -INFINITY;
     auto row = [&](int i) { return ((size_t)blockIdx.x * 2 * W + order[p0 + i]) * a.hb + h; };
 #pragma unroll 4
-    for (int i = 0; i < np; ++i) mx = fmaxf(mx, a.warp.ml[row(i) * 2]);
-    const float base = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll 4
     for (int i = 0; i < np; ++i) {
       const size_t p = row(i);
-      add_piece(o, l, *reinterpret_cast<const float2*>(a.warp.ml + p * 2),
-                *reinterpret_cast<const float4*>(a.warp.part + p * a.dv + c4 * 4), base);
+      add_piece(o, l, mx, *reinterpret_cast<const float2*>(a.warp.ml + p * 2),
+                *reinterpret_cast<const float4*>(a.warp.part + p * a.dv + c4 * 4));
     }
     if (f.from >= c0 && f.from + f.tiles <= c1) {
       const size_t orow = (size_t)f.b * a.Hq + g * a.G + blk * E::kHeads + h;

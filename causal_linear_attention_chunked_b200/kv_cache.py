@@ -81,6 +81,10 @@ def _tokens(t, name):
     return n, H, w, step if n > 1 else H * w
 
 
+def _dense_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _given(t, shape, dtype, name):
     """Checks an output that the caller passed."""
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
@@ -142,8 +146,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
         with ctx:
             return qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved,
                                 q_out, k_out)
-    q_out = q.new_empty(q.shape) if q_out is None else _given(q_out, q.shape, q.dtype, "q_out")
-    k_out = k.new_empty(k.shape) if k_out is None else _given(k_out, k.shape, q.dtype, "k_out")
+    q_out = _dense_like(q) if q_out is None else _given(q_out, q.shape, q.dtype, "q_out")
+    k_out = _dense_like(k) if k_out is None else _given(k_out, k.shape, q.dtype, "k_out")
     _check(lib.lt_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions), n_pos,
         _ptr(inv_freq), rot, 1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), n, Hq,
@@ -171,13 +175,13 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positio
                                     eps, interleaved, dq, dk)
     dq_step, dk_step = Hq * d, Hkv * d
     if dq is None:
-        dq = q.new_empty(q.shape)
+        dq = _dense_like(q)
     elif dq.shape != q.shape or dq.dtype != q.dtype:
         raise ValueError("dq must have q's shape and dtype")
     else:
         dq_step = _tokens(dq, "dq")[3]
     if dk is None:
-        dk = k.new_empty(k.shape)
+        dk = _dense_like(k)
     elif dk.shape != k.shape or dk.dtype != q.dtype:
         raise ValueError("dk must have k's shape and dtype")
     else:
