@@ -157,42 +157,65 @@ __device__ __forceinline__ uint32_t top_bits(const Chunk<float>& c) {
   }
   return m;
 }
-template <typename T>
-__device__ __forceinline__ uint32_t top_bits(const Chunk<T>& c) {
-  // 16-bit magnitudes order as integers, NaN last, like fp32's; two at a time
-  const uint32_t k = 0x7fff7fffu;
-  const uint32_t m = __vmaxu2(__vmaxu2(c.r.x & k, c.r.y & k), __vmaxu2(c.r.z & k, c.r.w & k));
-  const uint16_t top = (uint16_t)max(m & 0xffffu, m >> 16);
-  if constexpr (sizeof(T) == 2) {
-    T x;
-    *reinterpret_cast<uint16_t*>(&x) = top;
-    return __float_as_uint(to_float(x)) & 0x7fffffffu;
-  }
+__device__ __forceinline__ uint32_t top_bits(const Chunk<__nv_bfloat16>& c) {
+  const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&c.r);
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(w[0]), __habs2(w[1])),
+                                       __hmax2_nan(__habs2(w[2]), __habs2(w[3])));
+  return __float_as_uint(to_float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)))) &
+         0x7fffffffu;
+}
+__device__ __forceinline__ uint32_t top_bits(const Chunk<__half>& c) {
+  const __half2* w = reinterpret_cast<const __half2*>(&c.r);
+  const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(w[0]), __habs2(w[1])),
+                                __hmax2_nan(__habs2(w[2]), __habs2(w[3])));
+  return __float_as_uint(to_float(__hmax_nan(__low2half(m), __high2half(m)))) & 0x7fffffffu;
 }
 
-// y[0..3] / scale, each quotient correctly rounded.  With v the correctly
-// rounded reciprocal, q = x v is within two steps of x / scale; one correction
-// q + (x - q scale) v brings it within one, and Markstein's theorem (P. Markstein,
+// Correctly rounded quotients by multiplication.  With v the correctly rounded
+// reciprocal of b, q = x v is within two steps of x / b; one correction q + (x -
+// q b) v brings it within one, and Markstein's theorem (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990) makes the second, whose remainder is exact, the rounded quotient.  The
-// remainder is exact while it stays above fp32's smallest numbers: for scales
-// within 2^-80 .. 2^80 and quotients that do not round to code 0 anyway.
-// Rows outside divide.
-__device__ __forceinline__ void quotients(F2* y, float scale) {
-  if (scale >= 8.2718061e-25f && scale <= 1.2089258e+24f) {
-    const float v = __frcp_rn(scale);
-    const F2 v2 = pack_f2(v, v), n2 = pack_f2(-scale, -scale);
+// remainder is exact while it stays above fp32's smallest numbers: for a row's
+// largest magnitude within 2^-60 .. 2^60 that holds for the scale, and for
+// every quotient that does not round to code 0 anyway.  Other rows divide.
+struct Divisor {
+  float b, v;
+  bool exact;  // by multiplication
+};
+__device__ __forceinline__ F2 quotient(F2 x, const Divisor& d) {
+  const F2 v = pack_f2(d.v, d.v), n = pack_f2(-d.b, -d.b);
+  F2 q = mul2(x, v);
+  q = fma2(fma2(q, n, x), v, q);
+  return fma2(fma2(q, n, x), v, q);
+}
+// a row's scale from the bits of its largest magnitude
+template <typename KV>
+__device__ __forceinline__ Divisor scale_of(uint32_t top) {
+  constexpr float kMax = KvMax<KV>::value;
+  Divisor d;
+  d.exact = top - 0x21800000u <= 0x5d800000u - 0x21800000u;  // 2^-60 .. 2^60
+  const float x = __uint_as_float(top);
+  if (d.exact) {
+    constexpr float v = 1.0f / kMax;  // rounded by the compiler
+    float q = x * v;
+    q = fmaf(fmaf(q, -kMax, x), v, q);
+    d.b = fmaf(fmaf(q, -kMax, x), v, q);
+  } else {
+    d.b = fmaxf(__fdiv_rn(x, kMax), kTiny);
+  }
+  d.v = __frcp_rn(d.b);
+  return d;
+}
+__device__ __forceinline__ void quotients(F2* y, const Divisor& d) {
+  if (d.exact) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      F2 q = mul2(y[e], v2);
-      q = fma2(fma2(q, n2, y[e]), v2, q);
-      y[e] = fma2(fma2(q, n2, y[e]), v2, q);
-    }
+    for (int e = 0; e < 4; ++e) y[e] = quotient(y[e], d);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 x = unpack_f2(y[e]);
-      y[e] = pack_f2(__fdiv_rn(x.x, scale), __fdiv_rn(x.y, scale));
+      y[e] = pack_f2(__fdiv_rn(x.x, d.b), __fdiv_rn(x.y, d.b));
     }
   }
 }
@@ -281,117 +304,151 @@ __device__ __forceinline__ void check_offsets(const CacheArgs& a) {
 }
 
 // ----------------------------------------------------------------- kernels
-// blockIdx.y: 0 keys, 1 values
-template <typename T, typename KV>
-__global__ void __launch_bounds__(kT) lt_kv_quant_kernel(const CacheArgs a) {
+// A block's rows: every thread group's (token, head) list.  L lanes per row.
+template <int L>
+struct Rows {
+  static constexpr int kGroups = kT / L;
+  int grp, j, n;
+  RowAt at;
+  __device__ __forceinline__ Rows(int tokens, int heads)
+      : grp(threadIdx.x / L), j(threadIdx.x % L), n(tokens * heads),
+        at(threadIdx.x / L, kGroups, heads) {}
+};
+
+template <typename T, typename KV, int WIDTH>
+__device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool, const T* in,
+                                           int64_t stride, const Place* place, int nt) {
   constexpr int kU = 2;  // rows in flight per thread
-  __shared__ Place place[kMaxTok];
-  const int which = blockIdx.y;
-  const Pool pool = a.pool[which];
-  const int64_t t0 = (int64_t)blockIdx.x * a.tok;
-  const int nt = (int)min((int64_t)a.tok, a.tokens - t0);
-  if (threadIdx.x < nt) place[threadIdx.x] = place_of_slot(a, t0 + threadIdx.x);
-  __syncthreads();
-  const int half = pool.w >> 1, L = pool.w >> 4, RG = kT / L;  // lanes per row, rows at a time
-  const int grp = threadIdx.x / L, j = threadIdx.x % L;
-  const int rows = nt * a.H;
-  const T* in = static_cast<const T*>(a.in[which]) + t0 * a.stride[which] + j * 8;
+  constexpr int L = WIDTH / 16, HALF = WIDTH / 2, RG = Rows<L>::kGroups;
+  Rows<L> rows(nt, a.H);
+  in += rows.j * 8;
   const int first = (threadIdx.x & ~31) / L;  // warps stay converged for the shuffles
-  RowAt at(grp, RG, a.H);
 #pragma unroll 1
-  for (int r = grp, rw = first; rw < rows; r += RG * kU, rw += RG * kU) {
+  for (int r = rows.grp, rw = first; rw < rows.n; r += RG * kU, rw += RG * kU) {
     Chunk<T> x[kU][2];
     Place pl[kU];
     int hd[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       pl[u].page = -1;
-      hd[u] = at.h;
+      hd[u] = rows.at.h;
       x[u][0] = x[u][1] = Chunk<T>{};
-      if (r + u * RG < rows) {
-        pl[u] = place[at.tt];
-        const T* p = in + at.tt * a.stride[which] + at.h * pool.w;
+      if (r + u * RG < rows.n) {
+        pl[u] = place[rows.at.tt];
+        const T* p = in + rows.at.tt * stride + rows.at.h * WIDTH;
         x[u][0] = load_chunk(p);
-        x[u][1] = load_chunk(p + half);
+        x[u][1] = load_chunk(p + HALF);
       }
-      at.next();
+      rows.at.next();
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       uint32_t top = max(top_bits(x[u][0]), top_bits(x[u][1]));
-      for (int o = L >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const bool finite = top < 0x7f800000u;
-      const float scale = fmaxf(__fdiv_rn(__uint_as_float(top), KvMax<KV>::value), kTiny);
-      if (pl[u].page < 0) continue;
-      uint8_t* out = static_cast<uint8_t*>(pool.p) + (int64_t)pl[u].page * pool.page +
-                     (int64_t)pl[u].slot * pool.slot + (int64_t)hd[u] * pool.head + j * 8;
+      const Divisor d = scale_of<KV>(top);
+      uint2 code[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         F2 y[4];
         widen8(x[u][c], y);
-        quotients(y, scale);
-        const uint2 code = encode(y, KV());
-        *reinterpret_cast<uint2*>(out + c * half) = finite ? code : make_uint2(0, 0);
+        quotients(y, d);
+        code[c] = encode(y, KV());
       }
-      if (j == 0)
-        pool.scale[((int64_t)pl[u].page * a.H + hd[u]) * a.page_size + pl[u].slot] =
-            finite ? scale : __uint_as_float(0x7fc00000u);
+      if (pl[u].page >= 0) {
+        uint8_t* out = static_cast<uint8_t*>(pool.p) + (int64_t)pl[u].page * pool.page +
+                       (int64_t)pl[u].slot * pool.slot + (int64_t)hd[u] * pool.head + rows.j * 8;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<uint2*>(out + c * HALF) = finite ? code[c] : make_uint2(0, 0);
+        if (rows.j == 0)
+          pool.scale[((int64_t)pl[u].page * a.H + hd[u]) * a.page_size + pl[u].slot] =
+              finite ? d.b : __uint_as_float(0x7fc00000u);
+      }
     }
   }
 }
 
-template <typename T, typename KV>
-__global__ void __launch_bounds__(kT) lt_kv_dequant_kernel(const CacheArgs a) {
+template <typename T, typename KV, int WIDTH>
+__device__ __forceinline__ void dequant_rows(const CacheArgs& a, const Pool& pool, T* out,
+                                             const Place* place, int nt) {
   constexpr int kU = 4;
-  __shared__ Place place[kMaxTok];
-  const int which = blockIdx.y;
-  const Pool pool = a.pool[which];
-  const int t0 = blockIdx.x * a.tok;
-  const int nt = min(a.tok, a.N - t0);
-  if (blockIdx.x == 0 && which == 0) check_offsets(a);
-  if (threadIdx.x < nt) place[threadIdx.x] = place_of_row(a, t0 + threadIdx.x);
-  __syncthreads();
-  const int half = pool.w >> 1, L = pool.w >> 4, RG = kT / L;
-  const int grp = threadIdx.x / L, j = threadIdx.x % L;
-  const int rows = nt * a.H;
-  T* out = static_cast<T*>(a.out[which]) + (int64_t)t0 * a.H * pool.w + j * 8;
-  RowAt at(grp, RG, a.H);
+  constexpr int L = WIDTH / 16, HALF = WIDTH / 2, RG = Rows<L>::kGroups;
+  Rows<L> rows(nt, a.H);
+  out += rows.j * 8;
 #pragma unroll 1
-  for (int r = grp; r < rows; r += RG * kU) {
+  for (int r = rows.grp; r < rows.n; r += RG * kU) {
     uint2 code[kU][2];
     float scale[kU];
     bool live[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       live[u] = false;
-      if (r + u * RG < rows) {
-        const Place pl = place[at.tt];
+      if (r + u * RG < rows.n) {
+        const Place pl = place[rows.at.tt];
         live[u] = pl.page >= 0;
         if (live[u]) {
           const uint8_t* p = static_cast<const uint8_t*>(pool.p) + (int64_t)pl.page * pool.page +
-                             (int64_t)pl.slot * pool.slot + (int64_t)at.h * pool.head + j * 8;
+                             (int64_t)pl.slot * pool.slot + (int64_t)rows.at.h * pool.head +
+                             rows.j * 8;
           code[u][0] = __ldg(reinterpret_cast<const uint2*>(p));
-          code[u][1] = __ldg(reinterpret_cast<const uint2*>(p + half));
-          scale[u] = __ldg(&pool.scale[((int64_t)pl.page * a.H + at.h) * a.page_size + pl.slot]);
+          code[u][1] = __ldg(reinterpret_cast<const uint2*>(p + HALF));
+          scale[u] =
+              __ldg(&pool.scale[((int64_t)pl.page * a.H + rows.at.h) * a.page_size + pl.slot]);
         }
       }
-      at.next();
+      rows.at.next();
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (!live[u]) continue;
       const F2 s2 = pack_f2(scale[u], scale[u]);
-      T* o = out + (int64_t)(r + u * RG) * pool.w;
+      T* o = out + (int64_t)(r + u * RG) * WIDTH;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         F2 y[4];
         decode(code[u][c], y, KV());
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], s2);
-        store8(o + c * half, y);
+        store8(o + c * HALF, y);
       }
     }
   }
+}
+
+// blockIdx.y: 0 keys, 1 values
+template <typename T, typename KV>
+__global__ void __launch_bounds__(kT) lt_kv_quant_kernel(const CacheArgs a) {
+  __shared__ Place place[kMaxTok];
+  const int which = blockIdx.y;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tok;
+  const int nt = (int)min((int64_t)a.tok, a.tokens - t0);
+  if (threadIdx.x < nt) place[threadIdx.x] = place_of_slot(a, t0 + threadIdx.x);
+  __syncthreads();
+  const Pool pool = a.pool[which];
+  const T* in = static_cast<const T*>(a.in[which]) + t0 * a.stride[which];
+  if (pool.w == 64)
+    quant_rows<T, KV, 64>(a, pool, in, a.stride[which], place, nt);
+  else
+    quant_rows<T, KV, 128>(a, pool, in, a.stride[which], place, nt);
+}
+
+template <typename T, typename KV>
+__global__ void __launch_bounds__(kT) lt_kv_dequant_kernel(const CacheArgs a) {
+  __shared__ Place place[kMaxTok];
+  const int which = blockIdx.y;
+  const int t0 = blockIdx.x * a.tok;
+  const int nt = min(a.tok, a.N - t0);
+  if (blockIdx.x == 0 && which == 0) check_offsets(a);
+  if (threadIdx.x < nt) place[threadIdx.x] = place_of_row(a, t0 + threadIdx.x);
+  __syncthreads();
+  const Pool pool = a.pool[which];
+  T* out = static_cast<T*>(a.out[which]) + (int64_t)t0 * a.H * pool.w;
+  if (pool.w == 64)
+    dequant_rows<T, KV, 64>(a, pool, out, place, nt);
+  else
+    dequant_rows<T, KV, 128>(a, pool, out, place, nt);
 }
 
 // Rows as they are, in 16-byte pieces: into the cache, or out of it.  Strides
@@ -451,17 +508,20 @@ cudaError_t launch_quant(const CacheArgs& a, bool e4m3, bool write, dim3 grid, c
   return cudaGetLastError();
 }
 
-// Tokens per block: enough to share the lookup of their places, few enough
-// that a decode step's tokens spread over the device.
-int token_block(int64_t tokens, int sms) {
+// Tokens per block: enough rows for every group of a block's threads (lanes of
+// a row: see Rows) and to share the lookup of their places, few enough that a
+// decode step's tokens spread over the device.
+int token_block(int64_t tokens, int heads, int lanes, int sms) {
+  const int least = (kT / lanes + heads - 1) / heads;
   const int64_t n = tokens / (4 * sms);
-  return n < 1 ? 1 : n > kMaxTok ? kMaxTok : (int)n;
+  return n < least ? least : n > kMaxTok ? kMaxTok : (int)n;
 }
 
 cudaError_t launch(CacheArgs a, lt_dtype_t t, lt_kv_dtype_t kv, bool write, int sms,
                    cudaStream_t s) {
   const int64_t n = write ? a.tokens : a.N;
-  a.tok = token_block(n, sms);
+  const int row = (a.pool[0].w > a.pool[1].w ? a.pool[0].w : a.pool[1].w) * (int)kv_size(kv);
+  a.tok = token_block(n, a.H, row / 16, sms);
   const dim3 grid((unsigned)((n + a.tok - 1) / a.tok), 2);
   if (eight_bit(kv)) {
     const bool e4m3 = kv == LT_KV_E4M3;

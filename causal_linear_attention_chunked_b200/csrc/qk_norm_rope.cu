@@ -9,13 +9,16 @@
 // turns, so it is formed in turns and reduced in fp64; only the fraction of a
 // turn, at most 1/2, goes to fp32 sine and cosine.
 //
-// Bound by memory and, close behind, by instruction issue, so the layout is
-// chosen to need few of them: a warp takes whole tokens, and its angles stay
-// in registers for all heads.  A row is spread over d/8 lanes (the norm is a
-// 3- or 4-step shuffle); each lane holds two quads of elements, 4j.. and
-// rot/2 + 4j..: whichever way the pairs are laid out, both halves of a pair
-// are in one lane, and no value crosses lanes for the rotation.  Products run
-// two at a time (f32x2).
+// Bound by memory.  A warp takes whole tokens, and its angles stay in
+// registers for all heads.  The heads of a token are contiguous, so a warp
+// moves them in batches of 2 KB with one bulk copy each way, through a ring of
+// its own in shared memory (results overwrite their inputs there): enough
+// bytes in flight without holding them in registers, and few instructions per
+// element, which issue would otherwise bound.  A row is spread over d/8 lanes
+// (the norm is a 3- or 4-step shuffle); each lane holds two quads of elements,
+// 4j.. and rot/2 + 4j..: whichever way the pairs are laid out, both halves of a
+// pair are in one lane, and no value crosses lanes for the rotation.  Products
+// run two at a time (f32x2).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -23,6 +26,7 @@
 #include "../../include/lt_linear_attn.h"
 #include "lt_check.h"
 #include "lt_internal.h"
+#include "lt_ptx.cuh"
 #include "lt_vec.cuh"
 
 namespace lt {
@@ -43,11 +47,11 @@ struct NormArgs {
   const float* inv_freq;
   int rot;
   int parts;       // warps that share a token's heads
-  int per;         // forward: tokens per warp
   int64_t tokens;
   float eps;
   int w_f32;       // gains are fp32
   float* partial;  // backward: [block][2][d] sums of the gains' gradients
+  int* err;
 };
 
 struct GainArgs {
@@ -184,168 +188,205 @@ __device__ __forceinline__ float dot8(const F2* x, const F2* y) {
   return t.x + t.y;
 }
 
-// Rows in flight per lane: with two or three blocks per SM these cover the
-// memory latency of an SM's share of the bandwidth.
-template <typename T>
-constexpr int rows_in_flight() {
-  return sizeof(T) == 2 ? 4 : 2;
-}
+// -------------------------------------------------------------- the batches
+// A warp's ring: kS stages of kIn batches (x; backward also the upstream
+// gradient) of kStep heads, 2 KB each.  The block's warps hold 64 KB (96 KB),
+// so that three (two) blocks per SM keep about 100 KB of loads in flight.
+template <typename T, int D, int kIn>
+struct Ring {
+  static constexpr int kStep = 2048 / (D * (int)sizeof(T));  // heads per batch
+  static constexpr int kBatch = kStep * D;                   // elements
+  static constexpr int kS = kIn == 1 ? 4 : 3;
+  static constexpr int kBytes = kW * kS * kIn * 2048;
+  T* stages;       // [kS][kIn][kBatch]
+  uint64_t* full;  // [kS]
+  __device__ __forceinline__ T* stage(int i) const { return stages + i % kS * kIn * kBatch; }
+};
+constexpr uint64_t kWaitNs = 1000000000ull;  // a wait gives up after 1 s
 
-// A token's heads are walked in batches of RW * kU, queries' then keys'; the
-// parts of a token take every parts-th batch.
-template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(kT, 3) lt_norm_rope_kernel(const NormArgs a) {
-  using LN = Lane<D>;
-  constexpr int kU = rows_in_flight<T>(), STEP = LN::RW * kU;
-  const LN ln(a.rot);
-  const int64_t unit = (int64_t)blockIdx.x * kW + (threadIdx.x >> 5);
-  const int64_t first = unit / a.parts * a.per;
-  const int part = (int)(unit % a.parts);
-  const int nbq = (a.H[0] + STEP - 1) / STEP, nb = nbq + (a.H[1] + STEP - 1) / STEP;
-  F2 w[2][4];
-  load_gain<T>(a.w[0], a.w_f32, ln.qa, ln.qb, w[0]);
-  load_gain<T>(a.w[1], a.w_f32, ln.qa, ln.qb, w[1]);
-#pragma unroll 1
-  for (int64_t t = first; t < min(first + a.per, a.tokens); ++t) {
-    Angles<IL> ang;
-    bool have = false;
-#pragma unroll 1
-    for (int b = part; b < nb; b += a.parts) {
-      const int ph = b >= nbq, H = ph ? a.H[1] : a.H[0];
-      const int h0 = (ph ? b - nbq : b) * STEP + ln.grp;
-      const T* x = static_cast<const T*>(ph ? a.x[1] : a.x[0]) +
-                   t * (ph ? a.stride[1] : a.stride[0]) + h0 * D;
-      T* out = static_cast<T*>(ph ? a.out[1] : a.out[0]) + (t * H + h0) * D;
-      Quad<T> qa[kU], qb[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        qa[u] = qb[u] = Quad<T>{};
-        if (h0 + u * LN::RW < H) {
-          qa[u] = load_quad(x + u * (LN::RW * D) + ln.qa);
-          qb[u] = load_quad(x + u * (LN::RW * D) + ln.qb);
-        }
-      }
-      if (!have) {  // the first rows' loads are under way
-        if (a.rot) angles_of<T, D, IL>(a, ln, t, ang);
-        have = true;
-      }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        F2 y[4];
-        widen2x2(qa[u], y);
-        widen2x2(qb[u], y + 2);
-        const float rr = rsqrtf(LN::row_sum(dot8(y, y)) * (1.0f / D) + a.eps);
-        const F2 r2 = pack_f2(rr, rr);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], r2), ph ? w[1][e] : w[0][e]);
-        if (ln.rotated) turn<IL, false>(y, ang);
-        if (h0 + u * LN::RW < H) {
-          store_quad(out + u * (LN::RW * D) + ln.qa, y[0], y[1]);
-          store_quad(out + u * (LN::RW * D) + ln.qb, y[2], y[3]);
-        }
-      }
+// A warp's batches in order: units (token, part) unit, + step, ..., and of each
+// the token's batches part, + parts, ... (the queries' first, then the keys').
+struct Walk {
+  int64_t unit, t;
+  int part, b;
+  __device__ __forceinline__ void place(const NormArgs& a) {
+    t = a.parts == 1 ? unit : unit / a.parts;
+    part = (int)(unit - t * a.parts);
+    b = part;
+  }
+  __device__ __forceinline__ void next(const NormArgs& a, int nb, int64_t step) {
+    b += a.parts;
+    if (b >= nb) {
+      unit += step;
+      place(a);
     }
   }
-}
+};
 
-// A warp walks units (token, part) in steps of the launch's warps; each lane
-// sums its eight columns' gain gradients over its rows, the block's rows of
-// lanes are added in order at the end, and the launch below adds the blocks
-// in order.
-template <typename T, int D, bool IL>
-__global__ void __launch_bounds__(kT, 2) lt_norm_rope_bwd_kernel(const NormArgs a) {
+// Batch b of token t: queries or keys (ph), its first head and their number.
+template <int STEP>
+struct Batch {
+  int ph, h0, n;
+  __device__ __forceinline__ Batch(const NormArgs& a, int b, int nbq) {
+    ph = b >= nbq;
+    h0 = (ph ? b - nbq : b) * STEP;
+    n = min(STEP, (ph ? a.H[1] : a.H[0]) - h0);
+  }
+};
+
+// Forward (kBack false) and backward.  Backward, each lane also sums its eight
+// columns' gain gradients over its rows; the block's rows of lanes are added in
+// order at the end, and the launch below adds the blocks in order.
+template <typename T, int D, bool IL, bool kBack>
+__global__ void __launch_bounds__(kT, kBack ? 2 : 3) lt_norm_rope_kernel(const NormArgs a) {
   using LN = Lane<D>;
-  constexpr int kU = rows_in_flight<T>(), STEP = LN::RW * kU, RG = kW * LN::RW;
-  __shared__ float red[RG][D];
+  using R = Ring<T, D, kBack ? 2 : 1>;
+  constexpr int STEP = R::kStep, kU = STEP / LN::RW, RG = kW * LN::RW, S = R::kS;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kW][S];
+  __shared__ volatile int abort_flag;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  R ring{reinterpret_cast<T*>(smem) + warp * (S * (kBack ? 2 : 1) * R::kBatch), bars[warp]};
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&ring.full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+
   const LN ln(a.rot);
+  const int nbq = (a.H[0] + STEP - 1) / STEP, nb = nbq + (a.H[1] + STEP - 1) / STEP;
+  const int64_t units = a.tokens * a.parts, step = (int64_t)gridDim.x * kW;
+  Walk use, load;
+  use.unit = (int64_t)warp * gridDim.x + blockIdx.x;
+  use.place(a);
+  load = use;
+
+  // ask for batch i of this warp, the next of `load` (every lane keeps count,
+  // the first one issues)
+  int issued = 0;
+  auto fetch = [&](int i) {
+    if (load.unit >= units) return;
+    if (lane == 0) {
+      const Batch<STEP> bt(a, load.b, nbq);
+      const uint32_t bytes = (uint32_t)(bt.n * D * sizeof(T));
+      uint64_t* bar = &ring.full[i % S];
+      mbar_arrive_expect_tx(bar, kBack ? 2 * bytes : bytes);
+      bulk_load(ring.stage(i),
+                static_cast<const T*>(bt.ph ? a.x[1] : a.x[0]) +
+                    load.t * (bt.ph ? a.stride[1] : a.stride[0]) + bt.h0 * D,
+                bytes, bar);
+      if (kBack)
+        bulk_load(ring.stage(i) + R::kBatch,
+                  static_cast<const T*>(bt.ph ? a.g[1] : a.g[0]) +
+                      (load.t * (bt.ph ? a.H[1] : a.H[0]) + bt.h0) * D,
+                  bytes, bar);
+    }
+    ++issued;
+    load.next(a, nb, step);
+  };
+  for (int i = 0; i < S - 1; ++i) fetch(i);
+
   F2 w[2][4], dw[2][4];
   load_gain<T>(a.w[0], a.w_f32, ln.qa, ln.qb, w[0]);
   load_gain<T>(a.w[1], a.w_f32, ln.qa, ln.qb, w[1]);
 #pragma unroll
   for (int e = 0; e < 4; ++e) dw[0][e] = dw[1][e] = F2{0};
-  const int64_t units = a.tokens * a.parts;
+
+  Angles<IL> ang;
+  int64_t have = -1;  // the token whose angles `ang` holds
+  int i = 0;
 #pragma unroll 1
-  for (int64_t unit = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x; unit < units;
-       unit += (int64_t)gridDim.x * kW) {
-    const int64_t t = unit / a.parts;
-    const int part = (int)(unit - t * a.parts);
-    Angles<IL> ang;
-    bool have = false;
+  for (; use.unit < units; ++i) {
+    const Batch<STEP> bt(a, use.b, nbq);
+    if (a.rot && have != use.t) angles_of<T, D, IL>(a, ln, use.t, ang);
+    have = use.t;
+    if (!__all_sync(0xffffffffu,
+                    mbar_wait(&ring.full[i % S], (i / S) & 1, &abort_flag, a.err, kWaitNs)))
+      break;
+    T* const xs = ring.stage(i) + ln.grp * D;
 #pragma unroll
-    for (int ph = 0; ph < 2; ++ph) {
-      const int H = a.H[ph];
-      // the parts share out the batches of both phases in one count
-      const int skip = ph ? (a.H[0] + STEP - 1) / STEP % a.parts : 0;
-      const int b0 = part >= skip ? part - skip : part - skip + a.parts;
-      const T* x = static_cast<const T*>(a.x[ph]) + t * a.stride[ph];
-      const T* g = static_cast<const T*>(a.g[ph]) + t * H * D;
-      T* out = static_cast<T*>(a.out[ph]) + t * a.ostride[ph];
-#pragma unroll 1
-      for (int h0 = b0 * STEP + ln.grp, hw = b0 * STEP; hw < H;
-           h0 += a.parts * STEP, hw += a.parts * STEP) {
-        Quad<T> xa[kU], xb[kU], ga[kU], gb[kU];
+    for (int u = 0; u < kU; ++u) {
+      if (u * LN::RW >= bt.n) break;  // (the same for the whole warp)
+      // heads past the last are whatever the stage held: computed, not stored
+      T* const row = xs + u * (LN::RW * D);
+      F2 x[4];
+      widen2x2(*reinterpret_cast<const Quad<T>*>(row + ln.qa), x);
+      widen2x2(*reinterpret_cast<const Quad<T>*>(row + ln.qb), x + 2);
+      const float rr = rsqrtf(LN::row_sum(dot8(x, x)) * (1.0f / D) + a.eps);
+      const F2 r2 = pack_f2(rr, rr);
+      if constexpr (!kBack) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          xa[u] = xb[u] = ga[u] = gb[u] = Quad<T>{};
-          const int h = h0 + u * LN::RW;
-          if (h < H) {
-            xa[u] = load_quad(x + h * D + ln.qa);
-            xb[u] = load_quad(x + h * D + ln.qb);
-            ga[u] = load_quad(g + h * D + ln.qa);
-            gb[u] = load_quad(g + h * D + ln.qb);
-          }
+        for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], r2), bt.ph ? w[1][e] : w[0][e]);
+        if (ln.rotated) turn<IL, false>(x, ang);
+      } else {
+        const T* const grow = row + R::kBatch;
+        F2 g[4], u4[4];
+        widen2x2(*reinterpret_cast<const Quad<T>*>(grow + ln.qa), g);
+        widen2x2(*reinterpret_cast<const Quad<T>*>(grow + ln.qb), g + 2);
+        if (ln.rotated) turn<IL, true>(g, ang);
+        const bool live = u * LN::RW + ln.grp < bt.n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = mul2(x[e], r2);  // n = x r
+          u4[e] = mul2(g[e], bt.ph ? w[1][e] : w[0][e]);
         }
-        if (!have) {
-          if (a.rot) angles_of<T, D, IL>(a, ln, t, ang);
-          have = true;
-        }
+        // dx = r (u - n mean(u n)), dw += g n
+        const float m = -(LN::row_sum(dot8(u4, x)) * (1.0f / D));
+        const F2 m2 = pack_f2(m, m);
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          F2 xv[4], gv[4], uv[4];
-          widen2x2(xa[u], xv);
-          widen2x2(xb[u], xv + 2);
-          widen2x2(ga[u], gv);
-          widen2x2(gb[u], gv + 2);
-          if (ln.rotated) turn<IL, true>(gv, ang);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) uv[e] = mul2(gv[e], w[ph][e]);
-          const float ss = LN::row_sum(dot8(xv, xv)), ux = LN::row_sum(dot8(uv, xv));
-          const float rr = rsqrtf(ss * (1.0f / D) + a.eps);
-          // n = x r: dx = r (u - n mean(u n)), dw += g n
-          const float m = -(ux * rr * (1.0f / D));
-          const F2 r2 = pack_f2(rr, rr), m2 = pack_f2(m, m);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const F2 n = mul2(xv[e], r2);
-            dw[ph][e] = fma2(gv[e], n, dw[ph][e]);  // adds zeros past the last head
-            uv[e] = mul2(r2, fma2(n, m2, uv[e]));
-          }
-          const int h = h0 + u * LN::RW;
-          if (h < H) {
-            store_quad(out + h * D + ln.qa, uv[0], uv[1]);
-            store_quad(out + h * D + ln.qb, uv[2], uv[3]);
+        for (int e = 0; e < 4; ++e) {
+          const F2 n = x[e];
+          x[e] = mul2(r2, fma2(n, m2, u4[e]));
+          if (live) {
+            if (bt.ph)
+              dw[1][e] = fma2(g[e], n, dw[1][e]);
+            else
+              dw[0][e] = fma2(g[e], n, dw[0][e]);
           }
         }
       }
+      store_quad(row + ln.qa, x[0], x[1]);
+      store_quad(row + ln.qb, x[2], x[3]);
     }
+    fence_proxy_async_smem();  // the results, before the copy unit reads them
+    __syncwarp();
+    if (lane == 0) {
+      const int64_t os = kBack ? (bt.ph ? a.ostride[1] : a.ostride[0])
+                               : (int64_t)(bt.ph ? a.H[1] : a.H[0]) * D;
+      bulk_store(static_cast<T*>(bt.ph ? a.out[1] : a.out[0]) + use.t * os + bt.h0 * D,
+                 ring.stage(i), (uint32_t)(bt.n * D * sizeof(T)));
+      bulk_commit_group();
+      bulk_wait_read_but_last();  // the batch before this one has left its stage
+    }
+    use.next(a, nb, step);
+    fetch(i + S - 1);
   }
-  dependency_release();
-  if (!a.partial) return;
-  const int grp = (threadIdx.x >> 5) * LN::RW + ln.grp;
+  // a wait that gave up: the loads still under way must land before the block ends
+  for (; i < issued; ++i) {
+    int none = 0;
+    mbar_wait(&ring.full[i % S], (i / S) & 1, &none, nullptr, kWaitNs);
+  }
+  if (lane == 0) bulk_wait_all();  // the stores read shared memory
+  if constexpr (kBack) {
+    dependency_release();
+    if (!a.partial) return;
+    __shared__ __align__(16) float red[RG][D];  // (written two floats at a time)
+    const int grp = warp * LN::RW + ln.grp;
 #pragma unroll
-  for (int ph = 0; ph < 2; ++ph) {
-    __syncthreads();
+    for (int ph = 0; ph < 2; ++ph) {
+      __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 s = unpack_f2(dw[ph][e]);
-      *reinterpret_cast<float2*>(&red[grp][(e < 2 ? ln.qa : ln.qb) + 2 * (e & 1)]) = s;
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < D; c += kT) {
-      float s = 0.0f;
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<float2*>(&red[grp][(e < 2 ? ln.qa : ln.qb) + 2 * (e & 1)]) =
+            unpack_f2(dw[ph][e]);
+      __syncthreads();
+      for (int c = threadIdx.x; c < D; c += kT) {
+        float s = 0.0f;
 #pragma unroll
-      for (int q = 0; q < RG; ++q) s += red[q][c];
-      a.partial[((size_t)blockIdx.x * 2 + ph) * D + c] = s;
+        for (int q = 0; q < RG; ++q) s += red[q][c];
+        a.partial[((size_t)blockIdx.x * 2 + ph) * D + c] = s;
+      }
     }
   }
 }
@@ -376,43 +417,46 @@ __global__ void __launch_bounds__(1024) lt_norm_rope_gain_kernel(const GainArgs 
   }
 }
 
-template <typename T, int D, bool IL>
-cudaError_t launch_t(const NormArgs& a, int blocks, bool bwd, cudaStream_t stream) {
-  if (bwd)
-    lt_norm_rope_bwd_kernel<T, D, IL><<<blocks, kT, 0, stream>>>(a);
-  else
-    lt_norm_rope_kernel<T, D, IL><<<blocks, kT, 0, stream>>>(a);
+template <typename T, int D, bool IL, bool kBack>
+cudaError_t launch_t(const NormArgs& a, int blocks, cudaStream_t stream) {
+  constexpr int smem = Ring<T, D, kBack ? 2 : 1>::kBytes;
+  auto kern = lt_norm_rope_kernel<T, D, IL, kBack>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<blocks, kT, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_d(const NormArgs& a, int blocks, int d, int il, bool bwd, cudaStream_t s) {
+template <typename T, bool kBack>
+cudaError_t launch_d(const NormArgs& a, int blocks, int d, int il, cudaStream_t s) {
   if (d == 64)
-    return il ? launch_t<T, 64, true>(a, blocks, bwd, s) : launch_t<T, 64, false>(a, blocks, bwd, s);
-  return il ? launch_t<T, 128, true>(a, blocks, bwd, s) : launch_t<T, 128, false>(a, blocks, bwd, s);
+    return il ? launch_t<T, 64, true, kBack>(a, blocks, s)
+              : launch_t<T, 64, false, kBack>(a, blocks, s);
+  return il ? launch_t<T, 128, true, kBack>(a, blocks, s)
+            : launch_t<T, 128, false, kBack>(a, blocks, s);
 }
 
-cudaError_t launch(const NormArgs& a, int blocks, int d, int il, bool bwd, lt_dtype_t dtype,
+template <bool kBack>
+cudaError_t launch(const NormArgs& a, int blocks, int d, int il, lt_dtype_t dtype,
                    cudaStream_t s) {
-  return dtype == LT_BF16  ? launch_d<__nv_bfloat16>(a, blocks, d, il, bwd, s)
-         : dtype == LT_F16 ? launch_d<__half>(a, blocks, d, il, bwd, s)
-                           : launch_d<float>(a, blocks, d, il, bwd, s);
+  return dtype == LT_BF16  ? launch_d<__nv_bfloat16, kBack>(a, blocks, d, il, s)
+         : dtype == LT_F16 ? launch_d<__half, kBack>(a, blocks, d, il, s)
+                           : launch_d<float, kBack>(a, blocks, d, il, s);
 }
 
 // Warps that share a token's heads: one where the tokens alone fill the
-// device's warps, more where they are few (a decode step), up to a batch of
-// rows each.
+// device's warps, more where they are few (a decode step), up to one per batch.
 int token_parts(int64_t tokens, int H_q, int H_kv, int d, lt_dtype_t dtype, int sms) {
-  const int step = 32 / (d / 8) * (dtype == LT_F32 ? 2 : 4);  // RW * kU
+  const int step = 2048 / (d * (int)dtype_size(dtype));  // Ring::kStep
   const int batches = (H_q + step - 1) / step + (H_kv + step - 1) / step;
   const int64_t want = (int64_t)sms * kW / tokens;
   return want < 1 ? 1 : want > batches ? batches : (int)want;
 }
 
-// blocks of the backward launch: two per SM, at most one per eight units
-int64_t bwd_blocks(int64_t units, int sms) {
-  const int64_t n = (units + kW - 1) / kW;
-  return n < 2 * sms ? n : 2 * sms;
+// blocks of a launch: at most `most` per SM; few units take a block each
+int64_t block_count(int64_t units, int sms, int most) {
+  return units < most * sms ? units : most * sms;
 }
 
 // the checks that forward and backward share, without any CUDA call
@@ -430,8 +474,7 @@ lt_status_t check(const void* q, const void* k, const void* qw, const void* kw,
   if (rot > 0 && (!positions || !inv_freq || n_pos < 1 || tokens % n_pos != 0))
     return LT_ERR_INVALID_ARG;
   const size_t es = dtype_size(dtype);
-  // (a block index is 32 bits)
-  if (tokens > (int64_t)kW * 0x7fffffff || !stride_ok(tokens, q_stride, H_q, d, es) ||
+  if (tokens > ((int64_t)1 << 40) || !stride_ok(tokens, q_stride, H_q, d, es) ||
       !stride_ok(tokens, k_stride, H_kv, d, es))
     return LT_ERR_INVALID_ARG;
   if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(qw, 16) || !aligned_to(kw, 16) ||
@@ -513,11 +556,10 @@ extern "C" lt_status_t lt_qk_norm_rope(const void* q, const void* k, const void*
   a.eps = eps;
   a.w_f32 = w_dtype == LT_F32;
   a.parts = token_parts(tokens, H_q, H_kv, d, dtype, sms);
-  // four tokens per warp share the loaded gains where that leaves a few waves
-  // of blocks to even out the load
-  a.per = tokens >= (int64_t)16 * sms * kW ? 4 : 1;
-  const int64_t blocks = ((tokens + a.per - 1) / a.per * a.parts + kW - 1) / kW;
-  return launch(a, (int)blocks, d, interleaved, false, dtype, (cudaStream_t)stream) == cudaSuccess
+  a.err = device_error_word_current();
+  if (!a.err) return LT_ERR_CUDA;
+  const int blocks = (int)block_count(tokens * a.parts, sms, 3);
+  return launch<false>(a, blocks, d, interleaved, dtype, (cudaStream_t)stream) == cudaSuccess
              ? LT_OK
              : LT_ERR_CUDA;
 }
@@ -576,8 +618,10 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
     return LT_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return LT_ERR_CUDA;
+  int* err = device_error_word_current();
+  if (!err) return LT_ERR_CUDA;
   const int parts = token_parts(tokens, H_q, H_kv, d, dtype, sms);
-  const int64_t blocks = bwd_blocks(tokens * parts, sms);
+  const int64_t blocks = block_count(tokens * parts, sms, 2);
   Workspace w;
   if (gains) {
     const lt_status_t sw = w.take(workspace, workspace_bytes,
@@ -607,8 +651,9 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
   a.eps = eps;
   a.w_f32 = w_dtype == LT_F32;
   a.parts = parts;
+  a.err = err;
   a.partial = static_cast<float*>(w.p);
-  cudaError_t e = launch(a, (int)blocks, d, interleaved, true, dtype, (cudaStream_t)stream);
+  cudaError_t e = launch<true>(a, (int)blocks, d, interleaved, dtype, (cudaStream_t)stream);
   if (e == cudaSuccess && gains) {
     GainArgs ga = {};
     ga.partial = a.partial;
