@@ -12,9 +12,9 @@
 // multiplication and two corrections that round them exactly (see quotients).
 // A row is spread over w/16 lanes (the maximum is a 2- or 3-step shuffle);
 // each lane moves two chunks of 8 elements, w/2 apart, so that both the 16-bit
-// and the 8-bit side are accessed in whole runs.  A block looks up its tokens'
-// slots (or the sequences they belong to) once, in shared memory, for all
-// heads.
+// and the 8-bit side are accessed in whole runs.  A block walks tiles of tokens;
+// it looks up a tile's slots (or the sequences they belong to) once, in shared
+// memory, for all heads, while the rows of the tile before are under way.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -29,7 +29,7 @@ namespace lt {
 namespace {
 
 constexpr int kT = 256;      // threads
-constexpr int kMaxTok = 64;  // tokens per block, at most
+constexpr int kMaxTok = 64;  // tokens per tile, at most
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 struct Pool {
@@ -42,7 +42,7 @@ struct Pool {
 struct CacheArgs {
   Pool pool[2];  // keys, values
   int num_pages, page_size, H;
-  int tok;  // tokens per block
+  int tok;  // tokens per tile
   // write
   const void* in[2];
   int64_t stride[2];
@@ -304,42 +304,50 @@ __device__ __forceinline__ void check_offsets(const CacheArgs& a) {
 }
 
 // ----------------------------------------------------------------- kernels
-// A block's rows: every thread group's (token, head) list.  L lanes per row.
-template <int L>
-struct Rows {
-  static constexpr int kGroups = kT / L;
-  int grp, j, n;
-  RowAt at;
-  __device__ __forceinline__ Rows(int tokens, int heads)
-      : grp(threadIdx.x / L), j(threadIdx.x % L), n(tokens * heads),
-        at(threadIdx.x / L, kGroups, heads) {}
-};
+// A block walks the tiles blockIdx.x, + gridDim.x, ... of `n` tokens: `look`
+// gives a token's place, `work` does a tile's rows (its first token, tokens and
+// places).
+template <typename Look, typename Work>
+__device__ __forceinline__ void walk_tiles(int64_t n, int tok, const Look& look,
+                                           const Work& work) {
+  __shared__ Place place[2][kMaxTok];
+  int64_t t0 = (int64_t)blockIdx.x * tok;
+  const int64_t step = (int64_t)gridDim.x * tok;
+  if (threadIdx.x < tok && t0 + threadIdx.x < n) place[0][threadIdx.x] = look(t0 + threadIdx.x);
+  __syncthreads();
+  for (int buf = 0; t0 < n; t0 += step, buf ^= 1) {
+    const int64_t t1 = t0 + step + threadIdx.x;
+    if (threadIdx.x < tok && t1 < n) place[buf ^ 1][threadIdx.x] = look(t1);
+    work(t0, (int)min((int64_t)tok, n - t0), place[buf]);
+    __syncthreads();
+  }
+}
 
 template <typename T, typename KV, int WIDTH>
 __device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool, const T* in,
-                                           int64_t stride, const Place* place, int nt) {
+                                           int64_t stride, const Place* place, int nt, RowAt at) {
   constexpr int kU = 2;  // rows in flight per thread
-  constexpr int L = WIDTH / 16, HALF = WIDTH / 2, RG = Rows<L>::kGroups;
-  Rows<L> rows(nt, a.H);
-  in += rows.j * 8;
-  const int first = (threadIdx.x & ~31) / L;  // warps stay converged for the shuffles
+  constexpr int L = WIDTH / 16, HALF = WIDTH / 2, RG = kT / L;  // lanes per row, rows at a time
+  const int j = threadIdx.x % L, n = nt * a.H;
+  in += j * 8;
 #pragma unroll 1
-  for (int r = rows.grp, rw = first; rw < rows.n; r += RG * kU, rw += RG * kU) {
+  for (int r = threadIdx.x / L, rw = (threadIdx.x & ~31) / L; rw < n;
+       r += RG * kU, rw += RG * kU) {  // warps stay converged for the shuffles
     Chunk<T> x[kU][2];
     Place pl[kU];
     int hd[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       pl[u].page = -1;
-      hd[u] = rows.at.h;
+      hd[u] = at.h;
       x[u][0] = x[u][1] = Chunk<T>{};
-      if (r + u * RG < rows.n) {
-        pl[u] = place[rows.at.tt];
-        const T* p = in + rows.at.tt * stride + rows.at.h * WIDTH;
+      if (r + u * RG < n) {
+        pl[u] = place[at.tt];
+        const T* p = in + at.tt * stride + at.h * WIDTH;
         x[u][0] = load_chunk(p);
         x[u][1] = load_chunk(p + HALF);
       }
-      rows.at.next();
+      at.next();
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -358,11 +366,11 @@ __device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool,
       }
       if (pl[u].page >= 0) {
         uint8_t* out = static_cast<uint8_t*>(pool.p) + (int64_t)pl[u].page * pool.page +
-                       (int64_t)pl[u].slot * pool.slot + (int64_t)hd[u] * pool.head + rows.j * 8;
+                       (int64_t)pl[u].slot * pool.slot + (int64_t)hd[u] * pool.head + j * 8;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           *reinterpret_cast<uint2*>(out + c * HALF) = finite ? code[c] : make_uint2(0, 0);
-        if (rows.j == 0)
+        if (j == 0)
           pool.scale[((int64_t)pl[u].page * a.H + hd[u]) * a.page_size + pl[u].slot] =
               finite ? d.b : __uint_as_float(0x7fc00000u);
       }
@@ -372,33 +380,33 @@ __device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool,
 
 template <typename T, typename KV, int WIDTH>
 __device__ __forceinline__ void dequant_rows(const CacheArgs& a, const Pool& pool, T* out,
-                                             const Place* place, int nt) {
+                                             const Place* place, int nt, RowAt at) {
   constexpr int kU = 4;
-  constexpr int L = WIDTH / 16, HALF = WIDTH / 2, RG = Rows<L>::kGroups;
-  Rows<L> rows(nt, a.H);
-  out += rows.j * 8;
+  constexpr int L = WIDTH / 16, HALF = WIDTH / 2, RG = kT / L;
+  const int j = threadIdx.x % L, n = nt * a.H;
+  out += j * 8;
 #pragma unroll 1
-  for (int r = rows.grp; r < rows.n; r += RG * kU) {
+  for (int r = threadIdx.x / L; r < n; r += RG * kU) {
     uint2 code[kU][2];
     float scale[kU];
     bool live[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       live[u] = false;
-      if (r + u * RG < rows.n) {
-        const Place pl = place[rows.at.tt];
+      if (r + u * RG < n) {
+        const Place pl = place[at.tt];
         live[u] = pl.page >= 0;
         if (live[u]) {
           const uint8_t* p = static_cast<const uint8_t*>(pool.p) + (int64_t)pl.page * pool.page +
-                             (int64_t)pl.slot * pool.slot + (int64_t)rows.at.h * pool.head +
-                             rows.j * 8;
+                             (int64_t)pl.slot * pool.slot + (int64_t)at.h * pool.head +
+                             j * 8;
           code[u][0] = __ldg(reinterpret_cast<const uint2*>(p));
           code[u][1] = __ldg(reinterpret_cast<const uint2*>(p + HALF));
           scale[u] =
-              __ldg(&pool.scale[((int64_t)pl.page * a.H + rows.at.h) * a.page_size + pl.slot]);
+              __ldg(&pool.scale[((int64_t)pl.page * a.H + at.h) * a.page_size + pl.slot]);
         }
       }
-      rows.at.next();
+      at.next();
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -418,37 +426,46 @@ __device__ __forceinline__ void dequant_rows(const CacheArgs& a, const Pool& poo
 }
 
 // blockIdx.y: 0 keys, 1 values
+template <typename T, typename KV, int WIDTH>
+__device__ __forceinline__ void quant_walk(const CacheArgs& a, const Pool& pool, int which) {
+  const T* in = static_cast<const T*>(a.in[which]);
+  const int64_t stride = a.stride[which];
+  constexpr int L = WIDTH / 16;
+  const RowAt at(threadIdx.x / L, kT / L, a.H);
+  walk_tiles(
+      a.tokens, a.tok, [&](int64_t t) { return place_of_slot(a, t); },
+      [&](int64_t t0, int nt, const Place* place) {
+        quant_rows<T, KV, WIDTH>(a, pool, in + t0 * stride, stride, place, nt, at);
+      });
+}
 template <typename T, typename KV>
 __global__ void __launch_bounds__(kT) lt_kv_quant_kernel(const CacheArgs a) {
-  __shared__ Place place[kMaxTok];
-  const int which = blockIdx.y;
-  const int64_t t0 = (int64_t)blockIdx.x * a.tok;
-  const int nt = (int)min((int64_t)a.tok, a.tokens - t0);
-  if (threadIdx.x < nt) place[threadIdx.x] = place_of_slot(a, t0 + threadIdx.x);
-  __syncthreads();
-  const Pool pool = a.pool[which];
-  const T* in = static_cast<const T*>(a.in[which]) + t0 * a.stride[which];
+  const Pool pool = a.pool[blockIdx.y];
   if (pool.w == 64)
-    quant_rows<T, KV, 64>(a, pool, in, a.stride[which], place, nt);
+    quant_walk<T, KV, 64>(a, pool, blockIdx.y);
   else
-    quant_rows<T, KV, 128>(a, pool, in, a.stride[which], place, nt);
+    quant_walk<T, KV, 128>(a, pool, blockIdx.y);
 }
 
+template <typename T, typename KV, int WIDTH>
+__device__ __forceinline__ void dequant_walk(const CacheArgs& a, const Pool& pool, int which) {
+  T* out = static_cast<T*>(a.out[which]);
+  constexpr int L = WIDTH / 16;
+  const RowAt at(threadIdx.x / L, kT / L, a.H);
+  walk_tiles(
+      a.N, a.tok, [&](int64_t t) { return place_of_row(a, (int)t); },
+      [&](int64_t t0, int nt, const Place* place) {
+        dequant_rows<T, KV, WIDTH>(a, pool, out + t0 * a.H * WIDTH, place, nt, at);
+      });
+}
 template <typename T, typename KV>
 __global__ void __launch_bounds__(kT) lt_kv_dequant_kernel(const CacheArgs a) {
-  __shared__ Place place[kMaxTok];
-  const int which = blockIdx.y;
-  const int t0 = blockIdx.x * a.tok;
-  const int nt = min(a.tok, a.N - t0);
-  if (blockIdx.x == 0 && which == 0) check_offsets(a);
-  if (threadIdx.x < nt) place[threadIdx.x] = place_of_row(a, t0 + threadIdx.x);
-  __syncthreads();
-  const Pool pool = a.pool[which];
-  T* out = static_cast<T*>(a.out[which]) + (int64_t)t0 * a.H * pool.w;
+  const Pool pool = a.pool[blockIdx.y];
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
   if (pool.w == 64)
-    dequant_rows<T, KV, 64>(a, pool, out, place, nt);
+    dequant_walk<T, KV, 64>(a, pool, blockIdx.y);
   else
-    dequant_rows<T, KV, 128>(a, pool, out, place, nt);
+    dequant_walk<T, KV, 128>(a, pool, blockIdx.y);
 }
 
 // Rows as they are, in 16-byte pieces: into the cache, or out of it.  Strides
@@ -456,45 +473,45 @@ __global__ void __launch_bounds__(kT) lt_kv_dequant_kernel(const CacheArgs a) {
 template <bool kWrite>
 __global__ void __launch_bounds__(kT) lt_kv_copy_kernel(const CacheArgs a) {
   constexpr int kU = 4;
-  __shared__ Place place[kMaxTok];
   const int which = blockIdx.y;
   const Pool pool = a.pool[which];
-  const int64_t t0 = (int64_t)blockIdx.x * a.tok;
-  const int nt = (int)min((int64_t)a.tok, (kWrite ? a.tokens : (int64_t)a.N) - t0);
   if (!kWrite && blockIdx.x == 0 && which == 0) check_offsets(a);
-  if (threadIdx.x < nt)
-    place[threadIdx.x] =
-        kWrite ? place_of_slot(a, t0 + threadIdx.x) : place_of_row(a, (int)t0 + threadIdx.x);
-  __syncthreads();
-  const int L = pool.w >> 4, RG = kT / L;
+  const int L = pool.w >> 4, RG = kT / L;  // lanes per row, rows at a time
   const int grp = threadIdx.x / L, j = threadIdx.x % L;
-  const int rows = nt * a.H;
-  const uint8_t* in = static_cast<const uint8_t*>(a.in[which]) + t0 * a.stride[which] + j * 16;
-  uint8_t* out = static_cast<uint8_t*>(a.out[which]) + t0 * a.H * pool.w + j * 16;
-  RowAt at(grp, RG, a.H);
+  const int64_t stride = a.stride[which];
+  const RowAt first(grp, RG, a.H);
+  walk_tiles(
+      kWrite ? a.tokens : (int64_t)a.N, a.tok,
+      [&](int64_t t) { return kWrite ? place_of_slot(a, t) : place_of_row(a, (int)t); },
+      [&](int64_t t0, int nt, const Place* place) {
+        const int n = nt * a.H;
+        const uint8_t* in = static_cast<const uint8_t*>(a.in[which]) + t0 * stride + j * 16;
+        uint8_t* out = static_cast<uint8_t*>(a.out[which]) + t0 * a.H * pool.w + j * 16;
+        RowAt at = first;
 #pragma unroll 1
-  for (int r = grp; r < rows; r += RG * kU) {
-    uint4 x[kU];
-    uint8_t* dst[kU];
+        for (int r = grp; r < n; r += RG * kU) {
+          uint4 x[kU];
+          uint8_t* dst[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      dst[u] = nullptr;
-      if (r + u * RG < rows) {
-        const Place pl = place[at.tt];
-        if (pl.page >= 0) {
-          uint8_t* row = static_cast<uint8_t*>(pool.p) + (int64_t)pl.page * pool.page +
-                         (int64_t)pl.slot * pool.slot + (int64_t)at.h * pool.head + j * 16;
-          const uint8_t* src = kWrite ? in + at.tt * a.stride[which] + at.h * pool.w : row;
-          dst[u] = kWrite ? row : out + (int64_t)(r + u * RG) * pool.w;
-          x[u] = __ldg(reinterpret_cast<const uint4*>(src));
+          for (int u = 0; u < kU; ++u) {
+            dst[u] = nullptr;
+            if (r + u * RG < n) {
+              const Place pl = place[at.tt];
+              if (pl.page >= 0) {
+                uint8_t* row = static_cast<uint8_t*>(pool.p) + (int64_t)pl.page * pool.page +
+                               (int64_t)pl.slot * pool.slot + (int64_t)at.h * pool.head + j * 16;
+                const uint8_t* src = kWrite ? in + at.tt * stride + at.h * pool.w : row;
+                dst[u] = kWrite ? row : out + (int64_t)(r + u * RG) * pool.w;
+                x[u] = __ldg(reinterpret_cast<const uint4*>(src));
+              }
+            }
+            at.next();
+          }
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+            if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = x[u];
         }
-      }
-      at.next();
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-      if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = x[u];
-  }
+      });
 }
 
 template <typename T>
@@ -508,21 +525,28 @@ cudaError_t launch_quant(const CacheArgs& a, bool e4m3, bool write, dim3 grid, c
   return cudaGetLastError();
 }
 
-// Tokens per block: enough rows for every group of a block's threads (lanes of
-// a row: see Rows) and to share the lookup of their places, few enough that a
-// decode step's tokens spread over the device.
-int token_block(int64_t tokens, int heads, int lanes, int sms) {
+// Tokens per tile: enough rows for every group of a block's threads and to
+// share the lookup of their places, few enough that a decode step's tokens
+// spread over the device.
+int tile_tokens(int64_t tokens, int heads, int lanes, int most, int sms) {
   const int least = (kT / lanes + heads - 1) / heads;
   const int64_t n = tokens / (4 * sms);
-  return n < least ? least : n > kMaxTok ? kMaxTok : (int)n;
+  return n < least ? (least < most ? least : most) : n > most ? most : (int)n;
 }
 
 cudaError_t launch(CacheArgs a, lt_dtype_t t, lt_kv_dtype_t kv, bool write, int sms,
                    cudaStream_t s) {
   const int64_t n = write ? a.tokens : a.N;
   const int row = (a.pool[0].w > a.pool[1].w ? a.pool[0].w : a.pool[1].w) * (int)kv_size(kv);
-  a.tok = token_block(n, a.H, row / 16, sms);
-  const dim3 grid((unsigned)((n + a.tok - 1) / a.tok), 2);
+  // Quantising, a block's set-up costs as much as two of its tiles: four blocks
+  // stay on each SM (two for keys, two for values) and walk (32768 tokens of 8
+  // heads of 128: 47 us; a block per tile 55 of 55 tokens, 80 of 13).  The
+  // others hide a tile's lookup behind other blocks' rows instead (64 ragged
+  // sequences read back: 134 us; walking 176).
+  const bool walk = eight_bit(kv) && write;
+  a.tok = tile_tokens(n, a.H, row / 16, walk ? 32 : kMaxTok, sms);
+  const int64_t tiles = (n + a.tok - 1) / a.tok;
+  const dim3 grid((unsigned)(walk && tiles > 2 * sms ? 2 * sms : tiles), 2);
   if (eight_bit(kv)) {
     const bool e4m3 = kv == LT_KV_E4M3;
     return t == LT_BF16  ? launch_quant<__nv_bfloat16>(a, e4m3, write, grid, s)

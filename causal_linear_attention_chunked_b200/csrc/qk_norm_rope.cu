@@ -75,10 +75,13 @@ struct Lane {
     qa = rotated ? 4 * j : 8 * j;
     qb = rotated ? (rot >> 1) + 4 * j : 8 * j + 4;
   }
-  __device__ __forceinline__ static float row_sum(float x) {
+  // each row's sum over its lanes, of N rows
+  template <int N>
+  __device__ __forceinline__ static void row_sums(float* x) {
 #pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    return x;
+    for (int off = L / 2; off > 0; off >>= 1)
+#pragma unroll
+      for (int v = 0; v < N; ++v) x[v] += __shfl_xor_sync(0xffffffffu, x[v], off);
   }
 };
 
@@ -87,7 +90,7 @@ struct Lane {
 // neighbours: c[p] = (cos, cos), s[p] = (-sin, sin) of pair p.
 template <bool IL>
 struct Angles {
-  F2 c[IL ? 4 : 2], s[IL ? 4 : 2];
+  F2 c[IL ? 4 : 2], s[IL ? 4 : 2], n[IL ? 4 : 2];  // n = -s
 };
 
 // sine and cosine of a fraction of a turn, |t| <= 1/2.  16-bit outputs: the
@@ -135,17 +138,17 @@ __device__ __forceinline__ void angles_of(const NormArgs& a, const Lane<D>& ln, 
     for (int p = 0; p < 4; ++p) {
       out.c[p] = pack_f2(c[p], c[p]);
       out.s[p] = pack_f2(-s[p], s[p]);
+      out.n[p] = pack_f2(s[p], -s[p]);
     }
   } else {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       out.c[p] = pack_f2(c[2 * p], c[2 * p + 1]);
       out.s[p] = pack_f2(s[2 * p], s[2 * p + 1]);
+      out.n[p] = pack_f2(-s[2 * p], -s[2 * p + 1]);
     }
   }
 }
-
-__device__ __forceinline__ F2 negate2(F2 a) { return F2{a.v ^ 0x8000000080000000ull}; }
 
 // turn the lane's eight values y[0..3] (pairs of neighbours in registers);
 // kBack: by the negative angle
@@ -154,13 +157,13 @@ __device__ __forceinline__ void turn(F2* y, const Angles<IL>& g) {
   if constexpr (IL) {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
-      y[p] = fma2(swap2(y[p]), kBack ? negate2(g.s[p]) : g.s[p], mul2(y[p], g.c[p]));
+      y[p] = fma2(swap2(y[p]), kBack ? g.n[p] : g.s[p], mul2(y[p], g.c[p]));
   } else {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const F2 A = y[p], B = y[2 + p], n = negate2(g.s[p]);
-      y[p] = fma2(B, kBack ? g.s[p] : n, mul2(A, g.c[p]));
-      y[2 + p] = fma2(A, kBack ? n : g.s[p], mul2(B, g.c[p]));
+      const F2 A = y[p], B = y[2 + p];
+      y[p] = fma2(B, kBack ? g.s[p] : g.n[p], mul2(A, g.c[p]));
+      y[2 + p] = fma2(A, kBack ? g.n[p] : g.s[p], mul2(B, g.c[p]));
     }
   }
 }
@@ -189,18 +192,20 @@ __device__ __forceinline__ float dot8(const F2* x, const F2* y) {
 }
 
 // -------------------------------------------------------------- the batches
-// A warp's ring: kS stages of kIn batches (x; backward also the upstream
-// gradient) of kStep heads, 2 KB each.  The block's warps hold 64 KB (96 KB),
-// so that three (two) blocks per SM keep about 100 KB of loads in flight.
-template <typename T, int D, int kIn>
+constexpr int kBatchBytes = 2048, kStages = 3, kBlocks = 2;  // (blocks per SM)
+constexpr int kRows = 2;  // rows of a warp's lanes worked on at a time
+// A warp's ring: kStages stages of kIn batches (x; backward also the upstream
+// gradient) of kStep heads.  More bytes under way do not pay: at 2 x 16384
+// tokens of 32 + 8 bf16 heads of 128, 16 warps per SM with 2 KB x 3 stages
+// take 113 us, 4 KB x 3 128, 8 KB x 3 141 (and 2 KB x 4 with 24 warps 129):
+// reads and writes of DRAM then alternate in longer bursts.
+template <typename T, int D, bool kBack>
 struct Ring {
-  static constexpr int kStep = 2048 / (D * (int)sizeof(T));  // heads per batch
-  static constexpr int kBatch = kStep * D;                   // elements
-  static constexpr int kS = kIn == 1 ? 4 : 3;
-  static constexpr int kBytes = kW * kS * kIn * 2048;
-  T* stages;       // [kS][kIn][kBatch]
-  uint64_t* full;  // [kS]
-  __device__ __forceinline__ T* stage(int i) const { return stages + i % kS * kIn * kBatch; }
+  static constexpr int kIn = kBack ? 2 : 1;
+  static constexpr int kStep = kBatchBytes / (D * (int)sizeof(T));  // heads per batch
+  static constexpr int kBatch = kStep * D;                          // elements
+  static constexpr int kWarp = kStages * kIn * kBatch;
+  static constexpr int kBytes = kW * kWarp * (int)sizeof(T);
 };
 constexpr uint64_t kWaitNs = 1000000000ull;  // a wait gives up after 1 s
 
@@ -238,18 +243,20 @@ struct Batch {
 // columns' gain gradients over its rows; the block's rows of lanes are added in
 // order at the end, and the launch below adds the blocks in order.
 template <typename T, int D, bool IL, bool kBack>
-__global__ void __launch_bounds__(kT, kBack ? 2 : 3) lt_norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kT, kBlocks) lt_norm_rope_kernel(const NormArgs a) {
   using LN = Lane<D>;
-  using R = Ring<T, D, kBack ? 2 : 1>;
-  constexpr int STEP = R::kStep, kU = STEP / LN::RW, RG = kW * LN::RW, S = R::kS;
+  using R = Ring<T, D, kBack>;
+  constexpr int STEP = R::kStep, RG = kW * LN::RW, S = kStages, kV = kRows;
+  static_assert(STEP % (kV * LN::RW) == 0, "rows at a time stay inside a batch");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[kW][S];
   __shared__ volatile int abort_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  R ring{reinterpret_cast<T*>(smem) + warp * (S * (kBack ? 2 : 1) * R::kBatch), bars[warp]};
+  T* const ring = reinterpret_cast<T*>(smem) + warp * R::kWarp;
+  uint64_t* const full = bars[warp];
   if (threadIdx.x == 0) abort_flag = 0;
   if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&ring.full[s], 1);
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -262,30 +269,30 @@ __global__ void __launch_bounds__(kT, kBack ? 2 : 3) lt_norm_rope_kernel(const N
   use.place(a);
   load = use;
 
-  // ask for batch i of this warp, the next of `load` (every lane keeps count,
-  // the first one issues)
-  int issued = 0;
-  auto fetch = [&](int i) {
+  // ask for the next batch of `load` (every lane keeps count, the first issues)
+  int issued = 0, lstage = 0;
+  auto fetch = [&]() {
     if (load.unit >= units) return;
     if (lane == 0) {
       const Batch<STEP> bt(a, load.b, nbq);
       const uint32_t bytes = (uint32_t)(bt.n * D * sizeof(T));
-      uint64_t* bar = &ring.full[i % S];
-      mbar_arrive_expect_tx(bar, kBack ? 2 * bytes : bytes);
-      bulk_load(ring.stage(i),
+      T* const dst = ring + lstage * (R::kIn * R::kBatch);
+      mbar_arrive_expect_tx(&full[lstage], kBack ? 2 * bytes : bytes);
+      bulk_load(dst,
                 static_cast<const T*>(bt.ph ? a.x[1] : a.x[0]) +
                     load.t * (bt.ph ? a.stride[1] : a.stride[0]) + bt.h0 * D,
-                bytes, bar);
+                bytes, &full[lstage]);
       if (kBack)
-        bulk_load(ring.stage(i) + R::kBatch,
+        bulk_load(dst + R::kBatch,
                   static_cast<const T*>(bt.ph ? a.g[1] : a.g[0]) +
                       (load.t * (bt.ph ? a.H[1] : a.H[0]) + bt.h0) * D,
-                  bytes, bar);
+                  bytes, &full[lstage]);
     }
     ++issued;
+    if (++lstage == S) lstage = 0;
     load.next(a, nb, step);
   };
-  for (int i = 0; i < S - 1; ++i) fetch(i);
+  for (int i = 0; i < S - 1; ++i) fetch();
 
   F2 w[2][4], dw[2][4];
   load_gain<T>(a.w[0], a.w_f32, ln.qa, ln.qb, w[0]);
@@ -295,77 +302,116 @@ __global__ void __launch_bounds__(kT, kBack ? 2 : 3) lt_norm_rope_kernel(const N
 
   Angles<IL> ang;
   int64_t have = -1;  // the token whose angles `ang` holds
-  int i = 0;
+  int done = 0, stage = 0, parity = 0;
 #pragma unroll 1
-  for (; use.unit < units; ++i) {
+  for (; use.unit < units; ++done) {
     const Batch<STEP> bt(a, use.b, nbq);
-    if (a.rot && have != use.t) angles_of<T, D, IL>(a, ln, use.t, ang);
-    have = use.t;
-    if (!__all_sync(0xffffffffu,
-                    mbar_wait(&ring.full[i % S], (i / S) & 1, &abort_flag, a.err, kWaitNs)))
+    if (a.rot && have != use.t) {
+      angles_of<T, D, IL>(a, ln, use.t, ang);
+      have = use.t;
+    }
+    F2 cw[4], cd[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      cw[e] = bt.ph ? w[1][e] : w[0][e];
+      cd[e] = F2{0};
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], parity, &abort_flag, a.err, kWaitNs)))
       break;
-    T* const xs = ring.stage(i) + ln.grp * D;
+    T* const batch = ring + stage * (R::kIn * R::kBatch);
+    T* row = batch + ln.grp * D;
+    // kV rows at a time: their shuffles and roots overlap.  Heads past the last
+    // are whatever the stage held: computed, not stored.
+#pragma unroll 1
+    for (int h = ln.grp, hw = 0; hw < bt.n;
+         h += kV * LN::RW, hw += kV * LN::RW, row += kV * LN::RW * D) {
+      F2 x[kV][4], g[kV][4];
+      float rr[kV];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      if (u * LN::RW >= bt.n) break;  // (the same for the whole warp)
-      // heads past the last are whatever the stage held: computed, not stored
-      T* const row = xs + u * (LN::RW * D);
-      F2 x[4];
-      widen2x2(*reinterpret_cast<const Quad<T>*>(row + ln.qa), x);
-      widen2x2(*reinterpret_cast<const Quad<T>*>(row + ln.qb), x + 2);
-      const float rr = rsqrtf(LN::row_sum(dot8(x, x)) * (1.0f / D) + a.eps);
-      const F2 r2 = pack_f2(rr, rr);
-      if constexpr (!kBack) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], r2), bt.ph ? w[1][e] : w[0][e]);
-        if (ln.rotated) turn<IL, false>(x, ang);
-      } else {
-        const T* const grow = row + R::kBatch;
-        F2 g[4], u4[4];
-        widen2x2(*reinterpret_cast<const Quad<T>*>(grow + ln.qa), g);
-        widen2x2(*reinterpret_cast<const Quad<T>*>(grow + ln.qb), g + 2);
-        if (ln.rotated) turn<IL, true>(g, ang);
-        const bool live = u * LN::RW + ln.grp < bt.n;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = mul2(x[e], r2);  // n = x r
-          u4[e] = mul2(g[e], bt.ph ? w[1][e] : w[0][e]);
+      for (int v = 0; v < kV; ++v) {
+        const T* const r = row + v * (LN::RW * D);
+        widen2x2(*reinterpret_cast<const Quad<T>*>(r + ln.qa), x[v]);
+        widen2x2(*reinterpret_cast<const Quad<T>*>(r + ln.qb), x[v] + 2);
+        if constexpr (kBack) {
+          widen2x2(*reinterpret_cast<const Quad<T>*>(r + R::kBatch + ln.qa), g[v]);
+          widen2x2(*reinterpret_cast<const Quad<T>*>(r + R::kBatch + ln.qb), g[v] + 2);
         }
-        // dx = r (u - n mean(u n)), dw += g n
-        const float m = -(LN::row_sum(dot8(u4, x)) * (1.0f / D));
-        const F2 m2 = pack_f2(m, m);
+        rr[v] = dot8(x[v], x[v]);
+      }
+      LN::template row_sums<kV>(rr);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const F2 n = x[e];
-          x[e] = mul2(r2, fma2(n, m2, u4[e]));
-          if (live) {
-            if (bt.ph)
-              dw[1][e] = fma2(g[e], n, dw[1][e]);
-            else
-              dw[0][e] = fma2(g[e], n, dw[0][e]);
+      for (int v = 0; v < kV; ++v) {
+        rr[v] = rsqrtf(rr[v] * (1.0f / D) + a.eps);
+        const F2 r2 = pack_f2(rr[v], rr[v]);
+        if constexpr (!kBack) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[v][e] = mul2(mul2(x[v][e], r2), cw[e]);
+          if (ln.rotated) turn<IL, false>(x[v], ang);
+        } else {
+          if (ln.rotated) turn<IL, true>(g[v], ang);
+          const bool live = h + v * LN::RW < bt.n;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[v][e] = mul2(x[v][e], r2);  // n = x r
+            if (live) cd[e] = fma2(g[v][e], x[v][e], cd[e]);
+            g[v][e] = mul2(g[v][e], cw[e]);  // u
           }
         }
       }
-      store_quad(row + ln.qa, x[0], x[1]);
-      store_quad(row + ln.qb, x[2], x[3]);
+      if constexpr (kBack) {
+        // dx = r (u - n mean(u n)), dw += g n
+        float m[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) m[v] = dot8(g[v], x[v]);
+        LN::template row_sums<kV>(m);
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+          m[v] *= -1.0f / D;
+          const F2 m2 = pack_f2(m[v], m[v]), r2 = pack_f2(rr[v], rr[v]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[v][e] = mul2(r2, fma2(x[v][e], m2, g[v][e]));
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < kV; ++v) {
+        store_quad(row + v * (LN::RW * D) + ln.qa, x[v][0], x[v][1]);
+        store_quad(row + v * (LN::RW * D) + ln.qb, x[v][2], x[v][3]);
+      }
     }
     fence_proxy_async_smem();  // the results, before the copy unit reads them
     __syncwarp();
     if (lane == 0) {
       const int64_t os = kBack ? (bt.ph ? a.ostride[1] : a.ostride[0])
                                : (int64_t)(bt.ph ? a.H[1] : a.H[0]) * D;
-      bulk_store(static_cast<T*>(bt.ph ? a.out[1] : a.out[0]) + use.t * os + bt.h0 * D,
-                 ring.stage(i), (uint32_t)(bt.n * D * sizeof(T)));
+      bulk_store(static_cast<T*>(bt.ph ? a.out[1] : a.out[0]) + use.t * os + bt.h0 * D, batch,
+                 (uint32_t)(bt.n * D * sizeof(T)));
       bulk_commit_group();
       bulk_wait_read_but_last();  // the batch before this one has left its stage
     }
+    if constexpr (kBack) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (bt.ph)
+          dw[1][e] = add2(dw[1][e], cd[e]);
+        else
+          dw[0][e] = add2(dw[0][e], cd[e]);
+      }
+    }
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
     use.next(a, nb, step);
-    fetch(i + S - 1);
+    fetch();
   }
   // a wait that gave up: the loads still under way must land before the block ends
-  for (; i < issued; ++i) {
+  for (; done < issued; ++done) {
     int none = 0;
-    mbar_wait(&ring.full[i % S], (i / S) & 1, &none, nullptr, kWaitNs);
+    mbar_wait(&full[stage], parity, &none, nullptr, kWaitNs);
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
   }
   if (lane == 0) bulk_wait_all();  // the stores read shared memory
   if constexpr (kBack) {
@@ -419,7 +465,7 @@ __global__ void __launch_bounds__(1024) lt_norm_rope_gain_kernel(const GainArgs 
 
 template <typename T, int D, bool IL, bool kBack>
 cudaError_t launch_t(const NormArgs& a, int blocks, cudaStream_t stream) {
-  constexpr int smem = Ring<T, D, kBack ? 2 : 1>::kBytes;
+  constexpr int smem = Ring<T, D, kBack>::kBytes;
   auto kern = lt_norm_rope_kernel<T, D, IL, kBack>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -448,15 +494,15 @@ cudaError_t launch(const NormArgs& a, int blocks, int d, int il, lt_dtype_t dtyp
 // Warps that share a token's heads: one where the tokens alone fill the
 // device's warps, more where they are few (a decode step), up to one per batch.
 int token_parts(int64_t tokens, int H_q, int H_kv, int d, lt_dtype_t dtype, int sms) {
-  const int step = 2048 / (d * (int)dtype_size(dtype));  // Ring::kStep
+  const int step = kBatchBytes / (d * (int)dtype_size(dtype));  // Ring::kStep
   const int batches = (H_q + step - 1) / step + (H_kv + step - 1) / step;
   const int64_t want = (int64_t)sms * kW / tokens;
   return want < 1 ? 1 : want > batches ? batches : (int)want;
 }
 
-// blocks of a launch: at most `most` per SM; few units take a block each
-int64_t block_count(int64_t units, int sms, int most) {
-  return units < most * sms ? units : most * sms;
+// blocks of a launch: kBlocks per SM; few units take a block each
+int64_t block_count(int64_t units, int sms) {
+  return units < kBlocks * sms ? units : kBlocks * sms;
 }
 
 // the checks that forward and backward share, without any CUDA call
@@ -558,7 +604,7 @@ extern "C" lt_status_t lt_qk_norm_rope(const void* q, const void* k, const void*
   a.parts = token_parts(tokens, H_q, H_kv, d, dtype, sms);
   a.err = device_error_word_current();
   if (!a.err) return LT_ERR_CUDA;
-  const int blocks = (int)block_count(tokens * a.parts, sms, 3);
+  const int blocks = (int)block_count(tokens * a.parts, sms);
   return launch<false>(a, blocks, d, interleaved, dtype, (cudaStream_t)stream) == cudaSuccess
              ? LT_OK
              : LT_ERR_CUDA;
@@ -570,7 +616,7 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd_plan(int d, int num_sms, size_t* work
   if (num_sms <= 0) num_sms = lt::device_sm_count();
   if (num_sms <= 0) return LT_ERR_CUDA;
   // (a launch has at most two blocks per SM, however a token's heads are shared)
-  *workspace_bytes = (size_t)2 * num_sms * 2 * d * sizeof(float);
+  *workspace_bytes = (size_t)lt::kBlocks * num_sms * 2 * d * sizeof(float);
   return LT_OK;
 }
 
@@ -621,11 +667,11 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
   int* err = device_error_word_current();
   if (!err) return LT_ERR_CUDA;
   const int parts = token_parts(tokens, H_q, H_kv, d, dtype, sms);
-  const int64_t blocks = block_count(tokens * parts, sms, 2);
+  const int64_t blocks = block_count(tokens * parts, sms);
   Workspace w;
   if (gains) {
     const lt_status_t sw = w.take(workspace, workspace_bytes,
-                                  (size_t)2 * sms * 2 * d * sizeof(float), (cudaStream_t)stream);
+                                  (size_t)kBlocks * sms * 2 * d * sizeof(float), (cudaStream_t)stream);
     if (sw != LT_OK) return sw;
   }
   NormArgs a = {};
