@@ -171,23 +171,34 @@ __device__ __forceinline__ uint32_t top_bits(const Chunk<__half>& c) {
   return __float_as_uint(to_float(__hmax_nan(__low2half(m), __high2half(m)))) & 0x7fffffffu;
 }
 
-// Correctly rounded quotients by multiplication.  With v the correctly rounded
-// reciprocal of b, q = x v is within two steps of x / b; one correction q + (x -
-// q b) v brings it within one, and Markstein's theorem (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990) makes the second, whose remainder is exact, the rounded quotient.  The
-// remainder is exact while it stays above fp32's smallest numbers: for a row's
-// largest magnitude within 2^-60 .. 2^60 that holds for the scale, and for
-// every quotient that does not round to code 0 anyway.  Other rows divide.
+// Quotients by multiplication, for codes that are those of the correctly
+// rounded quotients.  With v the correctly rounded reciprocal of b, q = x v is
+// within two steps of x / b; one correction q + (x - q b) v brings it within
+// one, and Markstein's theorem (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990) makes a second, whose
+// remainder is exact, the rounded quotient.  The remainder is exact while it
+// stays above fp32's smallest numbers: for a row's largest magnitude within
+// 2^-60 .. 2^60 that holds for the scale, and for every quotient that does not
+// round to code 0 anyway.  Other rows divide.
+//
+// 16-bit inputs need one correction only: a code goes by two 8-bit (11-bit)
+// significands and the difference of their exponents, and over all of those
+// (22 differences; more give code 0) one correction gives the same codes (none
+// leaves 140 of 352320 bf16 cases different).
+//
+// What is computed is minus the quotient, p = -(x v), p + (x + p b)(-v): so a
+// zero keeps its sign, which x - q b would lose.
 struct Divisor {
   float b, v;
   bool exact;  // by multiplication
 };
-__device__ __forceinline__ F2 quotient(F2 x, const Divisor& d) {
-  const F2 v = pack_f2(d.v, d.v), n = pack_f2(-d.b, -d.b);
-  F2 q = mul2(x, v);
-  q = fma2(fma2(q, n, x), v, q);
-  return fma2(fma2(q, n, x), v, q);
+template <int kCorrections>
+__device__ __forceinline__ F2 minus_quotient(F2 x, const Divisor& d) {
+  const F2 n = pack_f2(-d.v, -d.v), b = pack_f2(d.b, d.b);
+  F2 p = mul2(x, n);
+#pragma unroll
+  for (int i = 0; i < kCorrections; ++i) p = fma2(fma2(p, b, x), n, p);
+  return p;
 }
 // a row's scale from the bits of its largest magnitude
 template <typename KV>
@@ -207,34 +218,37 @@ __device__ __forceinline__ Divisor scale_of(uint32_t top) {
   d.v = __frcp_rn(d.b);
   return d;
 }
-__device__ __forceinline__ void quotients(F2* y, const Divisor& d) {
+template <typename T>
+__device__ __forceinline__ void minus_quotients(F2* y, const Divisor& d) {
   if (d.exact) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = quotient(y[e], d);
+    for (int e = 0; e < 4; ++e) y[e] = minus_quotient<sizeof(T) == 2 ? 1 : 2>(y[e], d);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 x = unpack_f2(y[e]);
-      y[e] = pack_f2(__fdiv_rn(x.x, d.b), __fdiv_rn(x.y, d.b));
+      y[e] = pack_f2(__fdiv_rn(x.x, -d.b), __fdiv_rn(x.y, -d.b));
     }
   }
 }
 
-__device__ __forceinline__ uint2 encode(const F2* y, E4M3) {
+// the codes of -y[0..3]
+__device__ __forceinline__ uint2 encode_minus(const F2* y, E4M3) {
   uint32_t h[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     h[e] = __nv_cvt_float2_to_fp8x2(unpack_f2(y[e]), __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  return make_uint2((h[0] | (h[1] << 16)) ^ 0x80808080u, (h[2] | (h[3] << 16)) ^ 0x80808080u);
 }
-__device__ __forceinline__ uint2 encode(const F2* y, Int8) {
-  // adding 1.5 * 2^23 rounds to an integer, ties to even, and leaves it in the
+__device__ __forceinline__ uint2 encode_minus(const F2* y, Int8) {
+  // 1.5 * 2^23 - y rounds to an integer, ties to even, and leaves it in the
   // low bits as a two's complement number
-  const F2 magic = pack_f2(12582912.0f, 12582912.0f);
+  const F2 magic = pack_f2(12582912.0f, 12582912.0f), minus = pack_f2(-1.0f, -1.0f);
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const float2 a = unpack_f2(add2(y[2 * h], magic)), b = unpack_f2(add2(y[2 * h + 1], magic));
+    const float2 a = unpack_f2(fma2(y[2 * h], minus, magic));
+    const float2 b = unpack_f2(fma2(y[2 * h + 1], minus, magic));
     const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
     const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
     w[h] = __byte_perm(lo, hi, 0x5410);
@@ -338,15 +352,15 @@ __device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool,
     int hd[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      pl[u].page = -1;
-      hd[u] = at.h;
-      x[u][0] = x[u][1] = Chunk<T>{};
-      if (r + u * RG < n) {
-        pl[u] = place[at.tt];
-        const T* p = in + at.tt * stride + at.h * WIDTH;
-        x[u][0] = load_chunk(p);
-        x[u][1] = load_chunk(p + HALF);
-      }
+      // (past the last row: the tile's first again, and nothing stored)
+      const bool live = r + u * RG < n;
+      const int tt = live ? at.tt : 0;
+      hd[u] = live ? at.h : 0;
+      pl[u] = place[tt];
+      if (!live) pl[u].page = -1;
+      const T* p = in + tt * stride + hd[u] * WIDTH;
+      x[u][0] = load_chunk(p);
+      x[u][1] = load_chunk(p + HALF);
       at.next();
     }
 #pragma unroll
@@ -361,8 +375,8 @@ __device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool,
       for (int c = 0; c < 2; ++c) {
         F2 y[4];
         widen8(x[u][c], y);
-        quotients(y, d);
-        code[c] = encode(y, KV());
+        minus_quotients<T>(y, d);
+        code[c] = encode_minus(y, KV());
       }
       if (pl[u].page >= 0) {
         uint8_t* out = static_cast<uint8_t*>(pool.p) + (int64_t)pl[u].page * pool.page +

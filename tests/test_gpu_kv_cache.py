@@ -123,6 +123,32 @@ def test_quantisation_error_and_edges(kv):
     assert bool(((back.double() - k.double()).abs()[~bad] <= tol[~bad]).all())
 
 
+@pytest.mark.parametrize("kv", [E4M3, I8])
+@pytest.mark.parametrize("src,lo,step", [(torch.bfloat16, 128, 1), (torch.float16, 1024, 37)])
+def test_every_quotient_of_short_significands(src, lo, step, kv):
+    """Codes of every pair of bf16 significands (a row's largest value, another
+    value) at 22 differences of exponent, and of a share of fp16's: those of the
+    correctly rounded division, although the kernel multiplies."""
+    import causal_linear_attention_chunked_b200 as L
+    small = torch.arange(lo, 2 * lo, dtype=torch.float32)
+    v = torch.cat([small * 2.0 ** -e for e in range(22 if lo == 128 else 12)])
+    v = v[torch.arange(0, v.numel(), 1 if lo == 128 else 3)]
+    v = torch.cat([v, v.new_zeros(-v.numel() % 127)]).view(-1, 127)
+    for top in range(lo, 2 * lo, 16 * step):
+        rows = []
+        for a in range(top, min(top + 16 * step, 2 * lo), step):
+            x = torch.cat([torch.full((v.shape[0], 1), float(a)), torch.clamp(v, max=float(a))], 1)
+            rows.append(x / 1024)
+        x = torch.cat(rows).to(src)[:, None, :]
+        T = x.shape[0]
+        c = _cache(-(-T // 64), 64, 1, 128, 128, kv)
+        L.kv_cache_write(c, x.cuda(), (-x).cuda(), torch.arange(T, dtype=torch.int32).cuda())
+        for y, pool, scale in ((x, c.k, c.k_scale), (-x, c.v, c.v_scale)):
+            codes, sc = plain.quantise(y, kv)
+            assert torch.equal(_raw(pool.cpu().flatten(0, 1)[:T]), _raw(codes))
+            assert torch.equal(scale.cpu().transpose(1, 2).flatten(0, 1)[:T], sc)
+
+
 def test_bad_slots_are_skipped_and_reported():
     import causal_linear_attention_chunked_b200 as L
     from causal_linear_attention_chunked_b200 import _binding as b
