@@ -35,6 +35,7 @@ __global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const JoinArgs j) 
   const int lanes = a.dv >> 2, groups = share / lanes, c4 = tid % lanes, grp = tid / lanes;
   // every block waits, so that this launch ends after the first one has
   dependency_wait();
+  dependency_release();  // (all blocks of this launch are on the SMs or done by now)
   const Shared s = a.shared[blockIdx.x];
   const int n = s.blocks;
   if (n == 0) return;
@@ -89,7 +90,9 @@ int heads_per_unit(lt_dtype_t t, int G) {
   return G < most ? G : most;
 }
 int block_warps(lt_dtype_t t) { return t == LT_F32 ? 4 : 8; }
-int tile_tokens(lt_dtype_t t, lt_kv_dtype_t kv) { return t != LT_F32 && eight_bit(kv) ? 32 : 16; }
+int tile_tokens(lt_dtype_t t, lt_kv_dtype_t kv, int d, int dv) {
+  return t != LT_F32 && (d + dv) * (int)kv_size(kv) <= 256 ? 32 : 16;
+}
 
 // the workspace, one block of the first launch per SM: pieces of its warps
 // (two each), of its units (two each), and an entry for the second launch
@@ -206,7 +209,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
   a.page_magic = (uint32_t)(((uint64_t)1 << (31 + a.page_shift)) / a.page_size + 1);
   a.window = window;
-  a.tile = tile_tokens(dtype, cache->dtype);
+  a.tile = tile_tokens(dtype, cache->dtype, cache->d, cache->dv);
   a.scale = scale;
   a.out = out;
   a.lse = lse;

@@ -357,10 +357,10 @@ struct MmaEngine {
   static constexpr bool kQuant = Kv::kQuant;
   static constexpr bool kHalf = !__is_same(MT, __nv_bfloat16);
   static constexpr bool kSplit = !kQuant || __is_same(QT, __half);
-  // 8 KB per tile at width 128 for either size of element: 32 tokens of 8 bits
-  // share a tile's bookkeeping (16 of them, with 16 warps, issued a third more
-  // instructions per token)
-  static constexpr int kD = D, kHeads = 8 * kNB, kTile = kQuant ? 32 : 16, kWarps = 8;
+  // 8 KB per tile: short rows share a tile's bookkeeping (e4m3 rows of 128 in
+  // tiles of 16, with 16 warps, issued a third more instructions per token)
+  static constexpr int kD = D, kHeads = 8 * kNB, kWarps = 8;
+  static constexpr int kTile = (D + DV) * Kv::kBytes <= 256 ? 32 : 16;
   static constexpr int kHalves = kTile / 16;
   static constexpr int kKRow = D * Kv::kBytes, kVRow = DV * Kv::kBytes;  // bytes
   static constexpr int kExtra = 0;  // shared bytes per warp beside the ring
@@ -845,7 +845,8 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
   __shared__ Left left[2 * W];
   __shared__ int order[2 * W], group0[2 * W + 1], groups;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  dependency_release();
+  dependency_wait();     // launched early: what came before on the stream is done now
+  dependency_release();  // the second launch may come and wait
 
   // each thread adds a run of sequences' tiles; a scan gives the runs' starts
   const int per = (a.B + kThreads - 1) / kThreads;
@@ -1156,8 +1157,7 @@ cudaError_t launch_engine(const DecodeArgs& a, int sms, cudaStream_t stream) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<sms, E::kWarps * 32, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(sms), E::kWarps * 32, smem, stream, a);
 }
 
 // 16-bit queries: one engine for up to 8 query heads per KV head, one for more

@@ -155,6 +155,19 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
     return q_out, k_out
 
 
+_bwd_bytes = {}
+
+
+def _bwd_workspace(dev, d):
+    """Workspace bytes of qk_norm_rope_bwd for heads of d on the current device."""
+    n = _bwd_bytes.get((dev, d))
+    if n is None:
+        need = ctypes.c_size_t()
+        _check(lib.lt_qk_norm_rope_bwd_plan(d, 0, need))
+        n = _bwd_bytes[(dev, d)] = need.value
+    return n
+
+
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positions=None,
                      inv_freq=None, eps=1e-6, interleaved=False, dq=None, dk=None, stream=None):
     """Gradients (dq, dk, dq_weight, dk_weight) of qk_norm_rope for upstream
@@ -190,9 +203,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positio
     dkw = torch.empty_like(k_weight) if k_weight is not None else None
     ws, ws_bytes = None, 0
     if dqw is not None or dkw is not None:
-        need = ctypes.c_size_t()
-        _check(lib.lt_qk_norm_rope_bwd_plan(d, 0, need))
-        ws_bytes = need.value
+        ws_bytes = _bwd_workspace(dev, d)
         ws = q.new_empty(ws_bytes, dtype=torch.uint8)
     _check(lib.lt_qk_norm_rope_bwd(
         dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), _ptr(q_weight),
