@@ -89,9 +89,9 @@ int heads_per_unit(lt_dtype_t t, int G) {
   const int most = t == LT_F32 ? 8 : 16;
   return G < most ? G : most;
 }
-int block_warps(lt_dtype_t t) { return t == LT_F32 ? 4 : 8; }
-int tile_tokens(lt_dtype_t t, lt_kv_dtype_t kv, int d, int dv) {
-  return t != LT_F32 && (d + dv) * (int)kv_size(kv) <= 256 ? 32 : 16;
+int block_warps(lt_kv_dtype_t kv) { return kv == LT_KV_F32 ? 4 : 8; }
+int tile_tokens(lt_kv_dtype_t kv, int d, int dv) {
+  return (d + dv) * (int)kv_size(kv) <= 256 ? 32 : 16;
 }
 
 // the workspace, one block of the first launch per SM: pieces of its warps
@@ -101,10 +101,10 @@ struct Sizes {
   size_t floats;       // of a piece
   size_t bytes;
 };
-Sizes sizes_of(lt_dtype_t t, int H_q, int H_kv, int dv, int sms) {
+Sizes sizes_of(lt_dtype_t t, lt_kv_dtype_t kv, int H_q, int H_kv, int dv, int sms) {
   const int G = H_q / H_kv, hb = heads_per_unit(t, G), nhb = (G + hb - 1) / hb;
   Sizes z;
-  z.warp = (size_t)sms * block_warps(t) * 2;
+  z.warp = (size_t)sms * block_warps(kv) * 2;
   z.block = (size_t)sms * 2 * H_kv * nhb;
   z.floats = (size_t)hb * (dv + 2);
   z.bytes = (z.warp + z.block) * z.floats * sizeof(float) + (size_t)sms * sizeof(Shared);
@@ -128,7 +128,7 @@ extern "C" lt_status_t lt_paged_attn_decode_plan(int H_q, int H_kv, int d, int d
     return LT_ERR_INVALID_ARG;
   if (num_sms <= 0) num_sms = device_sm_count();
   if (num_sms <= 0) return LT_ERR_CUDA;
-  *workspace_bytes = sizes_of(dtype, H_q, H_kv, dv, num_sms).bytes;
+  *workspace_bytes = sizes_of(dtype, kv_dtype, H_q, H_kv, dv, num_sms).bytes;
   return LT_OK;
 }
 
@@ -180,7 +180,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.G = H_q / cache->H_kv;
   a.hb = heads_per_unit(dtype, a.G);
   a.nhb = (a.G + a.hb - 1) / a.hb;
-  const Sizes z = sizes_of(dtype, H_q, cache->H_kv, cache->dv, sms);
+  const Sizes z = sizes_of(dtype, cache->dtype, H_q, cache->H_kv, cache->dv, sms);
   Workspace w;
   const lt_status_t sw = w.take(workspace, workspace_bytes, z.bytes, (cudaStream_t)stream);
   if (sw != LT_OK) return sw;
@@ -209,7 +209,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
   a.page_magic = (uint32_t)(((uint64_t)1 << (31 + a.page_shift)) / a.page_size + 1);
   a.window = window;
-  a.tile = tile_tokens(dtype, cache->dtype, cache->d, cache->dv);
+  a.tile = tile_tokens(cache->dtype, cache->d, cache->dv);
   a.scale = scale;
   a.out = out;
   a.lse = lse;

@@ -343,6 +343,10 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi, I
 // scaled by a power of two per head into [1, 2), so that no bf16 query leaves
 // fp16's range.
 //
+// fp32 queries (8-bit caches only) are two fp16 terms as well, each head's
+// largest entry at 2^12, so that both terms of all but tiny entries are full
+// precision: 22 bits, two products per step.
+//
 // kShift: fp16 weights are held times 2^12 (it cancels in the division), so
 // that weights down to 2^-26 of the largest keep fp16's full precision; 2^12 *
 // 65504 * 2^31 keys stay inside fp32.  bf16 has fp32's range and needs none.
@@ -356,7 +360,10 @@ struct MmaEngine {
   using MT = typename Kv::Math;
   static constexpr bool kQuant = Kv::kQuant;
   static constexpr bool kHalf = !__is_same(MT, __nv_bfloat16);
-  static constexpr bool kSplit = !kQuant || __is_same(QT, __half);
+  static constexpr bool kWide = __is_same(QT, float);  // fp32 queries
+  static constexpr int kTerms = kWide ? 2 : 1;
+  static constexpr bool kSplit = !kQuant || !__is_same(QT, __nv_bfloat16);
+  static_assert(!kWide || kQuant, "fp32 caches have an engine of their own");
   // 8 KB per tile: short rows share a tile's bookkeeping (e4m3 rows of 128 in
   // tiles of 16, with 16 warps, issued a third more instructions per token)
   static constexpr int kD = D, kHeads = 8 * kNB, kWarps = 8;
@@ -365,7 +372,7 @@ struct MmaEngine {
   static constexpr int kKRow = D * Kv::kBytes, kVRow = DV * Kv::kBytes;  // bytes
   static constexpr int kExtra = 0;  // shared bytes per warp beside the ring
   static constexpr float kShift = kHalf ? 12.0f : 0.0f;
-  uint32_t qf[kNB][D / 16][2];
+  uint32_t qf[kTerms][kNB][D / 16][2];
   float o[kNB][DV / 16][4];
   // per head 2c, 2c + 1 of each block (c the lane's index among four)
   float m[kNB][2], l[kNB][2], sl2[kNB][2];
@@ -390,38 +397,56 @@ struct MmaEngine {
       for (int j = 0; j < DV / 16; ++j) o[b][j][0] = o[b][j][1] = o[b][j][2] = o[b][j][3] = 0.0f;
       const int h = 8 * b + (lane >> 2);
       const bool live = h < nheads;
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(q + (size_t)h * D);
+      const QT* row = q + (size_t)h * D;
+      if constexpr (!kQuant) {
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        // pairs of elements, in words of two
-        const int w0 = kQuant ? 8 * s + 2 * c : 8 * s + c;
-        qf[b][s][0] = live ? __ldg(row + w0) : 0u;
-        qf[b][s][1] = live ? __ldg(row + w0 + (kQuant ? 1 : 4)) : 0u;
-      }
-      if constexpr (kQuant) {
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            qf[0][b][s][e] =
+                live ? __ldg(reinterpret_cast<const uint32_t*>(row + 16 * s + 8 * e + 2 * c)) : 0u;
+      } else {
+        float2 x[D / 16][2];
         float top = 0.0f;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float2 x = unpack2<QT>(qf[b][s][e]);
-            top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+            x[s][e] = live ? load_pair(row + 16 * s + 4 * c + 2 * e) : make_float2(0.0f, 0.0f);
+            top = fmaxf(top, fmaxf(fabsf(x[s][e].x), fabsf(x[s][e].y)));
           }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t ex = min(max(__float_as_uint(top) >> 23, 7u), 247u);
-        const float down = __uint_as_float((254u - ex) << 23), up = __uint_as_float(ex << 23);
+        // times 2^(127 - ex) 2^kUp: the largest entry in [1, 2) 2^kUp
+        constexpr uint32_t kUp = kWide ? 12 : 0;
+        const uint32_t ex = min(max(__float_as_uint(top) >> 23, 13u), 253u);
+        const float down = __uint_as_float((254u + kUp - ex) << 23);
+        const float up = __uint_as_float((ex - kUp) << 23);
 #pragma unroll
         for (int e = 0; e < 2; ++e) sl2[b][e] *= __shfl_sync(0xffffffffu, up, 8 * c + 4 * e);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float2 x = unpack2<QT>(qf[b][s][e]);
-            qf[b][s][e] = pack2<__half>(x.x * down, x.y * down);
+            float2 y = make_float2(x[s][e].x * down, x[s][e].y * down);
+#pragma unroll
+            for (int n = 0; n < kTerms; ++n) {
+              qf[n][b][s][e] = pack2<__half>(y.x, y.y);
+              const float2 z = unpack2<__half>(qf[n][b][s][e]);
+              y.x -= z.x;
+              y.y -= z.y;
+            }
           }
       }
     }
+  }
+
+  // two neighbouring queries
+  __device__ __forceinline__ static float2 load_pair(const QT* p) {
+    if constexpr (kWide)
+      return __ldg(reinterpret_cast<const float2*>(p));
+    else
+      return unpack2<QT>(__ldg(reinterpret_cast<const uint32_t*>(p)));
   }
 
   using Scores = float[kNB][kHalves][4];
@@ -475,10 +500,12 @@ struct MmaEngine {
         widen4<false>(w[3], a1[1], a1[3], KT());
       }
 #pragma unroll
-      for (int b = 0; b < kNB; ++b) {
-        mma<MT>(s[b], a0, qf[b][i][0], qf[b][i][1]);
-        mma<MT>(s2[b], a1, qf[b][i + 1][0], qf[b][i + 1][1]);
-      }
+      for (int n = 0; n < kTerms; ++n)
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+          mma<MT>(s[b], a0, qf[n][b][i][0], qf[n][b][i][1]);
+          mma<MT>(s2[b], a1, qf[n][b][i + 1][0], qf[n][b][i + 1][1]);
+        }
     }
 #pragma unroll
     for (int b = 0; b < kNB; ++b)
@@ -640,159 +667,188 @@ struct MmaEngine {
   }
 };
 
-// ----------------------------------------------------- engine: fp32 FMA
-__device__ __forceinline__ void shared4(uint32_t addr, float* f, float) {
+// ---------------------------------------------------- engine: fp32 caches
+// Tensor cores in tf32, every factor in two terms: x = hi + lo, hi the nearest
+// tf32 value (11 bits) and lo the rest, of which the instruction keeps 11 bits;
+// x y ~ hi hi + hi lo + lo hi is off by about 2^-21 of |x y|, near fp32's own
+// rounding of a sum of d such products.  (Plain fp32 multiplications bound this
+// kernel at 3 TB/s for 4 query heads per KV head.)
+//
+// The same two products as MmaEngine, in steps of 8: S^T = K Q^T with A = K, O^T
+// = V^T P^T with A = V^T.  32-bit tiles have no ldmatrix, so rows and steps are
+// numbered to make a lane's share four neighbouring values, read at once and
+// without bank conflicts: of S^T, row g is token 4 (g & 1) + g / 2 of its eight,
+// and a lane's four d are the two halves of two steps; of V^T, a step's token c
+// is 2 c and c + 4 is 2 c + 1, and rows g and g + 8 of two tiles are a lane's
+// four columns.
+__device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void shared4(uint32_t addr, float* f) {
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
                : "r"(addr)
                : "memory");
 }
-template <typename KT>
-__device__ __forceinline__ void shared4(uint32_t addr, float* f, KT) {
-  uint32_t w, a, b;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
-  widen4<false>(w, a, b, KT());
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  f[0] = x.x;
-  f[1] = x.y;
-  f[2] = y.x;
-  f[3] = y.y;
-}
 
-// fp32 queries: scores with two lanes per token (each half of the row's
-// quads), then the weights through shared memory, each lane owning DV/32
-// columns of the accumulator.  Up to eight query heads share a tile.
-template <typename KT, int D, int DV>
-struct FmaEngine {
+template <int D, int DV>
+struct Tf32Engine {
   using QT = float;
-  static constexpr int kBytes = sizeof(KT);
   static constexpr int kD = D, kHeads = 8, kTile = 16, kWarps = 4;
-  static constexpr int kKRow = D * kBytes, kVRow = DV * kBytes;
-  static constexpr bool kQuant = kBytes == 1;
-  static constexpr int kExtra = kHeads * (D + kTile) * 4;  // queries, weights
-  static constexpr int NC = DV / 32;                       // columns per lane
-  float* qs;  // [kHeads][D]
-  float* ps;  // [kHeads][kTile]
-  float acc[kHeads][NC];
-  float m[kHeads], l[kHeads];
+  static constexpr int kKRow = D * 4, kVRow = DV * 4;  // bytes
+  static constexpr bool kQuant = false;
+  static constexpr int kExtra = 0;
+  uint32_t qh[D / 16][4], ql[D / 16][4];  // of head g = lane / 4, d 16 s + 4 c ..
+  float o[DV / 32][2][4];
+  float m[2], l[2];  // heads 2 c, 2 c + 1
   float sl2;
   int heads;
 
-  __device__ __forceinline__ void init(uint8_t* extra) {
-    qs = reinterpret_cast<float*>(extra);
-    ps = qs + kHeads * D;
-  }
+  __device__ __forceinline__ void init(uint8_t*) {}
 
   __device__ __forceinline__ void begin(const float* q, int nheads, float scale) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     heads = nheads;
     sl2 = scale * kLog2e;
-    __syncwarp();
-    for (int i = lane; i < nheads * D; i += 32) qs[i] = __ldg(q + i);
-    __syncwarp();
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-      m[h] = -INFINITY;
-      l[h] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NC; ++i) acc[h][i] = 0.0f;
+    for (int e = 0; e < 2; ++e) {
+      m[e] = -INFINITY;
+      l[e] = 0.0f;
     }
-  }
-
-  // four values at element e of row r
-  template <int RB>
-  __device__ __forceinline__ static void load4(uint32_t base, int r, int e, float* f) {
-    const int byte = e * kBytes;
-    shared4(base + chunk_at<RB>(r, byte >> 4) + (byte & 15), f, KT());
+#pragma unroll
+    for (int j = 0; j < DV / 32; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[j][e >> 2][e & 3] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const float4 x = g < nheads ? __ldg(reinterpret_cast<const float4*>(q + g * D + 16 * s) + c)
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split_tf32(f[e], qh[s][e], ql[s][e]);
+    }
   }
 
   __device__ __forceinline__ void tile(const TileAt& t) {
-    const int lane = threadIdx.x & 31, tok = lane >> 1, half = lane & 1;
-    float s[kHeads];
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int tok = ((g & 1) << 2) | (g >> 1);  // row g's token, of each eight
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) s[h] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      const int e = 4 * (2 * i + half);
-      float k[4];
-      load4<kKRow>(t.k, tok, e, k);
+    for (int i = 0; i < D / 16; ++i) {
+      float x[4], y[4];  // tokens tok and tok + 8
+      shared4(t.k + chunk_at<kKRow>(tok, 4 * i + c), x);
+      shared4(t.k + chunk_at<kKRow>(tok + 8, 4 * i + c), y);
 #pragma unroll
-      for (int h = 0; h < kHeads; ++h)
-        if (h < heads) {
-          const float4 q = *reinterpret_cast<const float4*>(qs + h * D + e);
-          s[h] = fmaf(q.x, k[0], fmaf(q.y, k[1], fmaf(q.z, k[2], fmaf(q.w, k[3], s[h]))));
-        }
+      for (int u = 0; u < 2; ++u) {  // two steps of 8
+        uint32_t ah[4], al[4];
+        split_tf32(x[2 * u], ah[0], al[0]);
+        split_tf32(y[2 * u], ah[1], al[1]);
+        split_tf32(x[2 * u + 1], ah[2], al[2]);
+        split_tf32(y[2 * u + 1], ah[3], al[3]);
+        mma_tf32(u ? s2 : s, ah, &qh[i][2 * u]);
+        mma_tf32(u ? s2 : s, ah, &ql[i][2 * u]);
+        mma_tf32(u ? s2 : s, al, &qh[i][2 * u]);
+      }
     }
-    const bool live = (t.mask >> tok) & 1u;
-    const float kf = sl2 * (kQuant ? t.ks[tok] : 1.0f), vf = kQuant ? t.vs[tok] : 1.0f;
+    const bool live0 = (t.mask >> tok) & 1u, live1 = (t.mask >> (tok + 8)) & 1u;
+    bool moved = false;
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-      if (h < heads) {
-        float x = s[h] + __shfl_xor_sync(0xffffffffu, s[h], 1);
-        x = live ? x * kf : -INFINITY;
-        float mx = fmaxf(m[h], x);
+    for (int e = 0; e < 2; ++e) {
+      s[e] = live0 ? (s[e] + s2[e]) * sl2 : -INFINITY;
+      s[2 + e] = live1 ? (s[2 + e] + s2[2 + e]) * sl2 : -INFINITY;
+      moved |= fmaxf(s[e], s[2 + e]) > m[e];
+    }
+    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int off = 2; off < 32; off <<= 1)
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(m[e], fmaxf(s[e], s[2 + e]));
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        if (mx > m[h]) {
-          const float f = exp2f(m[h] - mx);
-          l[h] *= f;
+        const float f = mx == m[e] ? 1.0f : exp2f(m[e] - mx);
+        m[e] = mx;
+        l[e] *= f;
 #pragma unroll
-          for (int i = 0; i < NC; ++i) acc[h][i] *= f;
-          m[h] = mx;
-        }
-        const float p = exp2f(x - (mx == -INFINITY ? 0.0f : mx));
-        l[h] += p;
-        // a token that takes no part has zero-filled values, whatever its scale
-        if (half == 0) ps[h * kTile + tok] = live ? p * vf : 0.0f;
+        for (int j = 0; j < DV / 32; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            o[j][y][e] *= f;
+            o[j][y][2 + e] *= f;
+          }
       }
-    __syncwarp();
-#pragma unroll 2
-    for (int j = 0; j < kTile; j += 4) {
-      float v[4][4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if constexpr (NC == 4) {
-          load4<kVRow>(t.v, j + u, 4 * lane, v[u]);
-        } else {  // two columns: this lane's half of a quad
-          float x[4];
-          load4<kVRow>(t.v, j + u, 4 * (lane >> 1), x);
-          v[u][0] = half ? x[2] : x[0];
-          v[u][1] = half ? x[3] : x[1];
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < kHeads; ++h)
-        if (h < heads) {
-          const float4 p = *reinterpret_cast<const float4*>(ps + h * kTile + j);
-#pragma unroll
-          for (int i = 0; i < NC; ++i)
-            acc[h][i] = fmaf(p.x, v[0][i],
-                             fmaf(p.y, v[1][i], fmaf(p.z, v[2][i], fmaf(p.w, v[3][i], acc[h][i]))));
-        }
     }
+    float p[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      p[e] = exp2f(s[e] - (m[e & 1] == -INFINITY ? 0.0f : m[e & 1]));
+      l[e & 1] += p[e];
+    }
+    // the weights of head g and tokens 2 c, 2 c + 1 of each eight, from the
+    // lanes of those tokens' rows (token t is row 2 (t & 3) + t / 4)
+    uint32_t ph[2][2], pl[2][2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const int from = 2 * c + z, src = 4 * (2 * (from & 3) + (from >> 2)) + (g >> 1);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float a = __shfl_sync(0xffffffffu, p[2 * u], src);
+        const float b = __shfl_sync(0xffffffffu, p[2 * u + 1], src);
+        split_tf32(g & 1 ? b : a, ph[u][z], pl[u][z]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < DV / 32; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {  // eight tokens each
+        float x[4], y[4];            // tokens 2 c and 2 c + 1, columns 32 j + 4 g ..
+        shared4(t.v + chunk_at<kVRow>(8 * u + 2 * c, 8 * j + g), x);
+        shared4(t.v + chunk_at<kVRow>(8 * u + 2 * c + 1, 8 * j + g), y);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          uint32_t ah[4], al[4];
+          split_tf32(x[2 * z], ah[0], al[0]);
+          split_tf32(x[2 * z + 1], ah[1], al[1]);
+          split_tf32(y[2 * z], ah[2], al[2]);
+          split_tf32(y[2 * z + 1], ah[3], al[3]);
+          mma_tf32(o[j][z], ah, ph[u]);
+          mma_tf32(o[j][z], ah, pl[u]);
+          mma_tf32(o[j][z], al, ph[u]);
+        }
+      }
   }
 
   __device__ __forceinline__ void finish(const Sink<float>& out) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-      if (h < heads) {
-        float sum = l[h];
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[e];
 #pragma unroll
-        for (int off = 2; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const float f = out.partial ? 1.0f : inverse_sum(sum);
-        float* row = (out.partial ? out.part : out.out) + (size_t)h * DV + NC * lane;
+      for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      const int h = 2 * c + e;
+      if (h >= heads) continue;
+      const float f = out.partial ? 1.0f : inverse_sum(sum);
+      float* row = (out.partial ? out.part : out.out) + (size_t)h * DV + 4 * g;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) row[i] = acc[h][i] * f;
-        if (lane == 0) {
-          if (out.partial)
-            *reinterpret_cast<float2*>(out.ml + 2 * h) = make_float2(m[h], sum);
-          else if (out.lse)
-            out.lse[h] = log_sum(m[h], sum);
-        }
+      for (int j = 0; j < DV / 32; ++j) {
+        const float y[4] = {o[j][0][e] * f, o[j][0][2 + e] * f, o[j][1][e] * f,
+                            o[j][1][2 + e] * f};
+        store_quad(row + 32 * j, y);
       }
+      if (lane < 4) {
+        if (out.partial)
+          *reinterpret_cast<float2*>(out.ml + 2 * h) = make_float2(m[e], sum);
+        else if (out.lse)
+          out.lse[h] = log_sum(m[e], sum);
+      }
+    }
   }
 };
 
@@ -1160,27 +1216,19 @@ cudaError_t launch_engine(const DecodeArgs& a, int sms, cudaStream_t stream) {
   return launch_dependent(kern, dim3(sms), E::kWarps * 32, smem, stream, a);
 }
 
+template <typename QT, typename KT, int NB>
+cudaError_t launch_mma_nb(const DecodeArgs& a, int d, int sms, cudaStream_t s) {
+  if (d == 64)
+    return a.dv == 64 ? launch_engine<MmaEngine<QT, KT, 64, 64, NB>>(a, sms, s)
+                      : launch_engine<MmaEngine<QT, KT, 64, 128, NB>>(a, sms, s);
+  return a.dv == 64 ? launch_engine<MmaEngine<QT, KT, 128, 64, NB>>(a, sms, s)
+                    : launch_engine<MmaEngine<QT, KT, 128, 128, NB>>(a, sms, s);
+}
+
 // 16-bit queries: one engine for up to 8 query heads per KV head, one for more
 template <typename QT, typename KT>
 cudaError_t launch_mma(const DecodeArgs& a, int d, int sms, cudaStream_t s) {
-  auto go = [&](auto nb) {
-    constexpr int NB = decltype(nb)::value;
-    if (d == 64)
-      return a.dv == 64 ? launch_engine<MmaEngine<QT, KT, 64, 64, NB>>(a, sms, s)
-                        : launch_engine<MmaEngine<QT, KT, 64, 128, NB>>(a, sms, s);
-    return a.dv == 64 ? launch_engine<MmaEngine<QT, KT, 128, 64, NB>>(a, sms, s)
-                      : launch_engine<MmaEngine<QT, KT, 128, 128, NB>>(a, sms, s);
-  };
-  return a.G <= 8 ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 2>());
-}
-
-template <typename KT>
-cudaError_t launch_fma(const DecodeArgs& a, int d, int sms, cudaStream_t s) {
-  if (d == 64)
-    return a.dv == 64 ? launch_engine<FmaEngine<KT, 64, 64>>(a, sms, s)
-                      : launch_engine<FmaEngine<KT, 64, 128>>(a, sms, s);
-  return a.dv == 64 ? launch_engine<FmaEngine<KT, 128, 64>>(a, sms, s)
-                    : launch_engine<FmaEngine<KT, 128, 128>>(a, sms, s);
+  return a.G <= 8 ? launch_mma_nb<QT, KT, 1>(a, d, sms, s) : launch_mma_nb<QT, KT, 2>(a, d, sms, s);
 }
 
 // the first launch, one translation unit per query type

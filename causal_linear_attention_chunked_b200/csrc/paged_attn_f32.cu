@@ -3,11 +3,22 @@
 
 namespace lt {
 namespace paged {
+namespace {
+
+cudaError_t launch_tf32(const DecodeArgs& a, int d, int sms, cudaStream_t s) {
+  if (d == 64)
+    return a.dv == 64 ? launch_engine<Tf32Engine<64, 64>>(a, sms, s)
+                      : launch_engine<Tf32Engine<64, 128>>(a, sms, s);
+  return a.dv == 64 ? launch_engine<Tf32Engine<128, 64>>(a, sms, s)
+                    : launch_engine<Tf32Engine<128, 128>>(a, sms, s);
+}
+
+}  // namespace
 
 cudaError_t launch_f32(const DecodeArgs& a, lt_kv_dtype_t kv, int d, int sms, cudaStream_t s) {
-  if (kv == LT_KV_E4M3) return launch_fma<E4M3>(a, d, sms, s);
-  if (kv == LT_KV_INT8) return launch_fma<Int8>(a, d, sms, s);
-  return launch_fma<float>(a, d, sms, s);
+  if (kv == LT_KV_E4M3) return launch_mma_nb<float, E4M3, 1>(a, d, sms, s);
+  if (kv == LT_KV_INT8) return launch_mma_nb<float, Int8, 1>(a, d, sms, s);
+  return launch_tf32(a, d, sms, s);
 }
 
 }  // namespace paged

@@ -133,8 +133,11 @@ def decode(q, k_pool, v_pool, k_scale, v_scale, table, lens, page_size, scale, w
     largest entry, 2^-25 of it.  That moves every weight by a factor within
     e^delta, the quotient by 2 delta W.  The weights for the tensor cores are
     two terms of the cache's 16-bit type, so half a step of it squared (2^-16,
-    2^-22); for 8-bit caches fp16, one term for bf16 queries (2^-11), two for
-    fp16; fp32 queries keep fp32.  Sums over n keys round by n U32 of W, and
+    2^-22); for 8-bit caches fp16, one term for bf16 queries (2^-11), two
+    otherwise; for fp32 caches two terms of tf32, the second cut to 11 bits
+    (2^-21), as are the products' factors (2^-21 of each term's size, 8 U32, in
+    the scores and again in the values).  fp32 queries on 8-bit caches are two
+    fp16 terms (2^-22, 4 U32).  Sums over n keys round by n U32 of W, and
     weights under 2^-26 of the largest lose at most 2^-37 each against the
     largest value row."""
     B, Hq, d = q.shape
@@ -144,8 +147,9 @@ def decode(q, k_pool, v_pool, k_scale, v_scale, table, lens, page_size, scale, w
     bound = torch.zeros(B, Hq, dv, dtype=torch.float64)
     lse_bound = torch.zeros(B, Hq, dtype=torch.float64)
     quant = k_scale is not None
-    weight = 0.0 if q.dtype == torch.float32 else \
-        2.0 ** -11 if quant and q.dtype == torch.bfloat16 else half_step(q.dtype) ** 2
+    wide = q.dtype == torch.float32
+    weight = 2.0 ** -11 if quant and q.dtype == torch.bfloat16 else \
+        2.0 ** -22 if quant else 2.0 ** -20 if wide else half_step(q.dtype) ** 2
     for b in range(B):
         n = int(lens[b])
         K = rows_of(k_pool, k_scale, table[b], n, page_size)
@@ -160,7 +164,8 @@ def decode(q, k_pool, v_pool, k_scale, v_scale, table, lens, page_size, scale, w
             qh = q[b, h].double()
             s = scale * (K[:, g] @ qh)
             size = abs(scale) * (K[:, g].abs() @ qh.abs())
-            delta = ((d + 8) * U32 * size + 8 * U32 * s.abs()).max() + 2.0 ** -21
+            delta = ((d + 8 + (16 if wide else 0)) * U32 * size + 8 * U32 * s.abs()).max() + \
+                2.0 ** -21
             if quant and q.dtype != torch.float32:
                 delta = delta + abs(scale) * qh.abs().max() * 2.0 ** -25 * \
                     K[:, g].abs().sum(-1).max()
