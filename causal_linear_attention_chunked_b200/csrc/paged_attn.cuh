@@ -670,9 +670,11 @@ struct MmaEngine {
 // ---------------------------------------------------- engine: fp32 caches
 // Tensor cores in tf32, every factor in two terms: x = hi + lo, hi the nearest
 // tf32 value (11 bits) and lo the rest, of which the instruction keeps 11 bits;
-// x y ~ hi hi + hi lo + lo hi is off by about 2^-21 of |x y|, near fp32's own
-// rounding of a sum of d such products.  (Plain fp32 multiplications bound this
-// kernel at 3 TB/s for 4 query heads per KV head.)
+// x y ~ hi hi + hi lo + lo hi is off by about 2^-21 of |x y|, either way.  The instruction's additions cut where fp32's
+// round, so chains of them are kept short: a tile's values are summed from zero
+// and added to the rest by plain additions (one long chain was four times
+// further off at 65000 keys).  Plain fp32 multiplications bound this kernel at
+// 3 TB/s for 4 query heads per KV head.
 //
 // The same two products as MmaEngine, in steps of 8: S^T = K Q^T with A = K, O^T
 // = V^T P^T with A = V^T.  32-bit tiles have no ldmatrix, so rows and steps are
@@ -689,7 +691,7 @@ __device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, const uint
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // (the conversion instruction is slower)
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void shared4(uint32_t addr, float* f) {
@@ -740,7 +742,7 @@ struct Tf32Engine {
   __device__ __forceinline__ void tile(const TileAt& t) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int tok = ((g & 1) << 2) | (g >> 1);  // row g's token, of each eight
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float s[4] = {}, s2[4] = {}, small[4] = {};
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       float x[4], y[4];  // tokens tok and tok + 8
@@ -754,16 +756,16 @@ struct Tf32Engine {
         split_tf32(x[2 * u + 1], ah[2], al[2]);
         split_tf32(y[2 * u + 1], ah[3], al[3]);
         mma_tf32(u ? s2 : s, ah, &qh[i][2 * u]);
-        mma_tf32(u ? s2 : s, ah, &ql[i][2 * u]);
-        mma_tf32(u ? s2 : s, al, &qh[i][2 * u]);
+        mma_tf32(small, ah, &ql[i][2 * u]);
+        mma_tf32(small, al, &qh[i][2 * u]);
       }
     }
     const bool live0 = (t.mask >> tok) & 1u, live1 = (t.mask >> (tok + 8)) & 1u;
     bool moved = false;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      s[e] = live0 ? (s[e] + s2[e]) * sl2 : -INFINITY;
-      s[2 + e] = live1 ? (s[2 + e] + s2[2 + e]) * sl2 : -INFINITY;
+      s[e] = live0 ? (s[e] + s2[e] + small[e]) * sl2 : -INFINITY;
+      s[2 + e] = live1 ? (s[2 + e] + s2[2 + e] + small[2 + e]) * sl2 : -INFINITY;
       moved |= fmaxf(s[e], s[2 + e]) > m[e];
     }
     if (__any_sync(0xffffffffu, moved)) {
@@ -805,7 +807,8 @@ struct Tf32Engine {
       }
     }
 #pragma unroll
-    for (int j = 0; j < DV / 32; ++j)
+    for (int j = 0; j < DV / 32; ++j) {
+      float sum[2][4] = {};
 #pragma unroll
       for (int u = 0; u < 2; ++u) {  // eight tokens each
         float x[4], y[4];            // tokens 2 c and 2 c + 1, columns 32 j + 4 g ..
@@ -818,11 +821,16 @@ struct Tf32Engine {
           split_tf32(x[2 * z + 1], ah[1], al[1]);
           split_tf32(y[2 * z], ah[2], al[2]);
           split_tf32(y[2 * z + 1], ah[3], al[3]);
-          mma_tf32(o[j][z], ah, ph[u]);
-          mma_tf32(o[j][z], ah, pl[u]);
-          mma_tf32(o[j][z], al, ph[u]);
+          mma_tf32(sum[z], ah, pl[u]);
+          mma_tf32(sum[z], al, ph[u]);
+          mma_tf32(sum[z], ah, ph[u]);
         }
       }
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][z][e] += sum[z][e];
+    }
   }
 
   __device__ __forceinline__ void finish(const Sink<float>& out) {
