@@ -43,10 +43,11 @@ __global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const JoinArgs j) 
   float l = 0.0f, mx = -INFINITY;
   if (h < a.Hq) {
     const int g = h / a.G, hh = h - g * a.G, blk = hh / a.hb;
-    const int units = a.Hkv * a.nhb, u = g * a.nhb + blk;
+    const int u = g * a.nhb + blk;
     // the first piece is the second of its block, the others the first of theirs
     auto row = [&](int i) {
-      return (((size_t)(s.block + i) * 2 + (i == 0 ? 1 : 0)) * units + u) * a.hb + hh - blk * a.hb;
+      return (((size_t)(s.block + i) * 2 + (i == 0 ? 1 : 0)) * a.units + u) * a.hb + hh -
+             blk * a.hb;
     };
 #pragma unroll 4
     for (int i = grp; i < n; i += groups) {
@@ -55,15 +56,22 @@ __global__ void __launch_bounds__(kJoin) lt_paged_join_kernel(const JoinArgs j) 
                 *reinterpret_cast<const float4*>(a.block.part + p * a.dv + c4 * 4));
     }
   }
-  acc_s[threadIdx.x] = o;
-  l_s[threadIdx.x] = l;
-  m_s[threadIdx.x] = mx;
-  __syncthreads();
+  // the groups of a column, `lanes` threads apart, by halves
+  const int at0 = threadIdx.x;
+  for (int half = groups >> 1; half > 0; half >>= 1) {
+    if (grp >= half && grp < 2 * half) {
+      acc_s[at0] = o;
+      l_s[at0] = l;
+      m_s[at0] = mx;
+    }
+    __syncthreads();
+    if (grp < half) {
+      const int p = at0 + half * lanes;
+      add_piece(o, l, mx, make_float2(m_s[p], l_s[p]), acc_s[p]);
+    }
+    __syncthreads();
+  }
   if (grp != 0 || h >= a.Hq) return;
-  const int at0 = threadIdx.x;  // this column's groups are `lanes` apart
-  for (int q = 1; q < groups; ++q)
-    add_piece(o, l, mx, make_float2(m_s[at0 + q * lanes], l_s[at0 + q * lanes]),
-              acc_s[at0 + q * lanes]);
   const float f = inverse_sum(l);
   const float y[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
   const size_t orow = (size_t)s.b * a.Hq + h;
@@ -151,10 +159,13 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   if (!aligned_to(q, 16) || !aligned_to(out, 16) || !aligned_to(block_table, 4) ||
       !aligned_to(seq_lens, 4) || !aligned_to(lse, 4))
     return LT_ERR_INVALID_ARG;
-  // pools are addressed in 32 bits of 16 bytes, and a warp's tiles counted in 31
-  const int64_t most = (int64_t)max_pages * cache->page_size;
-  const int64_t tiles = ((most < 0x7fffffff ? most : 0x7fffffff) / 16 + 1) * H_q;
-  if (!pools_within(cache, (size_t)64 << 30) || tiles > ((int64_t)1 << 40) / B)
+  // pools are addressed in 32 bits of 16 bytes, columns and a block's tiles
+  // counted in 31 bits
+  const int64_t pages_hold = (int64_t)max_pages * cache->page_size;
+  const int most = (int)(pages_hold < 0x7fffff00 ? pages_hold : 0x7fffff00);
+  const int64_t columns = (int64_t)B * (most / 16 + 1);
+  if (!pools_within(cache, (size_t)64 << 30) || columns > 0x7fffffff ||
+      columns > ((int64_t)1 << 36) / H_q)
     return LT_ERR_INVALID_ARG;
   const size_t es = dtype_size(dtype);
   Span ins[8];
@@ -205,7 +216,11 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.Hkv = cache->H_kv;
   a.num_pages = cache->num_pages;
   a.page_size = cache->page_size;
-  a.max_pages = max_pages;
+  a.max_len = most;
+  a.units = a.Hkv * a.nhb;
+  a.k_shift = -1;
+  for (int s = 0, w = block_warps(cache->dtype); (1 << s) <= w; ++s)
+    if (a.units << s == w) a.k_shift = s;
   while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
   a.page_magic = (uint32_t)(((uint64_t)1 << (31 + a.page_shift)) / a.page_size + 1);
   a.window = window;

@@ -79,10 +79,12 @@ struct DecodeArgs {
   const int32_t* lens;
   int B, Hq, Hkv, G, nhb;  // nhb: blocks of query heads per KV head
   int hb;                  // query heads per block of them
-  int num_pages, page_size, max_pages, window;
+  int num_pages, page_size, window;
   uint32_t page_magic;  // floor(2^(31 + page_shift) / page_size) + 1
   int page_shift;       // ceil(log2(page_size))
+  int max_len;          // keys that a table row has pages for
   int tile;             // tokens per tile (the engine's kTile)
+  int units, k_shift;   // Hkv * nhb; log2 of the warps per unit (-1: they do not divide)
   int by_seq;           // shared[] goes by sequence (else by first block)
   float scale;
   void* out;
@@ -97,16 +99,13 @@ struct DecodeArgs {
 struct Seq {
   int first, len;  // keys [first, len) take part
   int tiles;
-  bool bad;
 };
-__device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b) {
+template <int TILE>
+__device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int len) {
   Seq s;
-  s.len = a.lens[b];
-  // (positions up to a tile past the end stay inside 32 bits)
-  s.bad = s.len < 0 || (int64_t)s.len > min((int64_t)a.max_pages * a.page_size, (int64_t)0x7fffff00);
-  if (s.bad) s.len = 0;
+  s.len = len < 0 || len > a.max_len ? 0 : len;
   s.first = a.window ? max(0, s.len - a.window) : 0;
-  s.tiles = (s.len - s.first + a.tile - 1) / a.tile;
+  s.tiles = (s.len - s.first + TILE - 1) / TILE;
   return s;
 }
 
@@ -891,11 +890,13 @@ struct Lookup {
 // A warp's pieces of units that it shares with others of its block: [0] of the
 // segment that its part began with, [1] of the one that it ended with.
 struct Left {
-  int64_t from;  // the sequence's first column
+  int from;  // the sequence's first column
   int b, u, tiles;
   bool any;
 };
 
+// The code before a warp's first load runs once and cold: it is kept short
+// (32-bit columns, one copy of the search: 10.6 -> 9.0 us for 1024 tokens).
 template <typename E>
 __global__ void __launch_bounds__(E::kWarps * 32, 1)
     lt_paged_decode_kernel(const DecodeArgs a) {
@@ -904,8 +905,8 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
   constexpr int W = E::kWarps, kThreads = W * 32, TILE = E::kTile, S = R::kStages;
   static_assert(W <= 16, "the pieces of a block's warps fit one warp's lanes");
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t before[kThreads];  // columns of the sequences before this thread's
-  __shared__ int64_t warp_sum[W];
+  __shared__ int before[kThreads];  // columns of the sequences before this thread's
+  __shared__ int warp_sum[W];
   __shared__ Left left[2 * W];
   __shared__ int order[2 * W], group0[2 * W + 1], groups;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -914,22 +915,23 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
 
   // each thread adds a run of sequences' tiles; a scan gives the runs' starts
   const int per = (a.B + kThreads - 1) / kThreads;
-  int64_t sum = 0;
+  int sum = 0;
+#pragma unroll 1
   for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-    const Seq s = seq_of(a, b);
-    if (s.bad && blockIdx.x == 0) report_error(a.err, kDevErrBadSeqlens);
-    sum += s.tiles;
+    const int len = a.lens[b];
+    if ((len < 0 || len > a.max_len) && blockIdx.x == 0) report_error(a.err, kDevErrBadSeqlens);
+    sum += seq_of<TILE>(a, len).tiles;
   }
-  int64_t scan = sum;
+  int scan = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, scan, off);
+    const int x = __shfl_up_sync(0xffffffffu, scan, off);
     if (lane >= off) scan += x;
   }
   if (lane == 31) warp_sum[warp] = scan;
   if (tid < 2 * W) left[tid].any = false;
   __syncthreads();
-  int64_t total = 0, mine = 0;
+  int total = 0, mine = 0;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
     if (w < warp) mine += warp_sum[w];
@@ -940,58 +942,62 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
 
   // the block's columns, and this warp's tiles of them in the order (unit,
   // column): whole parts of units where the units divide the warps
-  const int units = a.Hkv * a.nhb;
-  const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)1);
-  const int64_t c0 = blockIdx.x * run, c1 = min(c0 + run, total);
-  const int ncol = (int)max(c1 - c0, (int64_t)0);
-  int64_t start, count;
-  if (W % units == 0) {
-    const int k = W / units, p = (ncol + k - 1) / k, sub = warp % k;
-    start = (int64_t)(warp / k) * ncol + sub * p;
-    count = min(p, ncol - sub * p);
+  const int run = max((int)((unsigned)(total + gridDim.x - 1) / gridDim.x), 1);
+  const int c0 = blockIdx.x * run, c1 = min(c0 + run, total), ncol = max(c1 - c0, 0);
+  int col0, u0, count;
+  if (a.k_shift >= 0) {
+    const int p = (ncol + (1 << a.k_shift) - 1) >> a.k_shift;
+    u0 = warp >> a.k_shift;
+    col0 = (warp - (u0 << a.k_shift)) * p;
+    count = min(p, ncol - col0);
   } else {
-    const int64_t all = (int64_t)units * ncol, p = (all + W - 1) / W;
-    start = warp * p;
+    const int all = a.units * ncol, p = (all + W - 1) / W, start = warp * p;
+    u0 = start / max(ncol, 1);
+    col0 = start - u0 * ncol;
     count = min(p, all - start);
   }
 
-  auto locate = [&](int64_t col) {  // the sequence and tile of a column
-    int lo = 0, hi = kThreads;  // the last thread whose sequences begin at or before it
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (before[mid] <= col)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    Cursor c;
-    int64_t rem = col - before[lo];
-    c.b = lo * per;
-    c.s = seq_of(a, c.b);
-    while (c.b + 1 < a.B && rem >= c.s.tiles) {
-      rem -= c.s.tiles;
-      c.s = seq_of(a, ++c.b);
-    }
-    c.t = (int)rem;
-    c.col = (int)(col - c0);
-    return c;
-  };
-  auto next = [&](Cursor& c) {
-    ++c.t;
-    if (++c.col == ncol) {
-      const int u = c.u + 1;
-      c = locate(c0);
-      c.u = u;
-    } else if (c.t == c.s.tiles) {
-      c.t = 0;
-      do c.s = seq_of(a, ++c.b);
-      while (c.s.tiles == 0 && c.b + 1 < a.B);
-    }
-  };
-
   if (count > 0) {
-    Cursor cc = locate(c0 + start % ncol);
-    cc.u = (int)(start / ncol);
+    // the sequences and tiles of the warp's first column and, where its part
+    // may go on into another unit, of the block's
+    Cursor first = {}, cc = {};
+#pragma unroll 1
+    for (int pass = a.k_shift >= 0 ? 1 : 0; pass < 2; ++pass) {
+      const int col = pass ? col0 : 0;
+      int lo = 0, hi = kThreads;  // the last thread whose sequences begin at or before it
+#pragma unroll 1
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] <= c0 + col)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      int rem = c0 + col - before[lo];
+      cc.b = lo * per;
+      cc.s = seq_of<TILE>(a, a.lens[cc.b]);
+#pragma unroll 1
+      while (cc.b + 1 < a.B && rem >= cc.s.tiles) {
+        rem -= cc.s.tiles;
+        cc.s = seq_of<TILE>(a, a.lens[++cc.b]);
+      }
+      cc.t = rem;
+      cc.col = col;
+      if (pass == 0) first = cc;
+    }
+    cc.u = u0;
+    auto next = [&](Cursor& c) {
+      ++c.t;
+      if (++c.col == ncol) {
+        const int u = c.u + 1;
+        c = first;
+        c.u = u;
+      } else if (c.t == c.s.tiles) {
+        c.t = 0;
+        do c.s = seq_of<TILE>(a, a.lens[++c.b]);
+        while (c.s.tiles == 0 && c.b + 1 < a.B);
+      }
+    };
     Cursor pc = cc;
 
     uint8_t* ring = smem + warp * R::kWarpBytes;
@@ -1060,7 +1066,7 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
             mask;
     };
 
-    const int n = (int)count;
+    const int n = count;
     int issued = 0;
     Lookup pend = look(pc);
     auto feed = [&](int stage) {
@@ -1102,7 +1108,7 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
       if (++stage == S) stage = 0;
       const bool seq_done = cc.t + 1 == cc.s.tiles;
       if (seq_done || cc.col + 1 == ncol || i + 1 == n) {
-        const int64_t from = c0 + cc.col - cc.t, to = from + cc.s.tiles;
+        const int from = c0 + cc.col - cc.t, to = from + cc.s.tiles;
         const bool had_block = c0 + seg == max(from, c0) && c0 + cc.col + 1 == min(to, c1);
         const int g = cc.u / a.nhb, blk = cc.u - g * a.nhb;
         const size_t orow = (size_t)cc.b * a.Hq + g * a.G + blk * E::kHeads;
@@ -1113,7 +1119,7 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
         const int slot = first_seg ? 0 : 1;
         const Pieces to_where = had_block ? a.block : a.warp;
         const size_t piece =
-            (had_block ? ((size_t)blockIdx.x * 2 + (from < c0 ? 0 : 1)) * units + cc.u
+            (had_block ? ((size_t)blockIdx.x * 2 + (from < c0 ? 0 : 1)) * a.units + cc.u
                        : ((size_t)blockIdx.x * W + warp) * 2 + slot) * a.hb;
         out.part = to_where.part + piece * a.dv;
         out.ml = to_where.ml + piece * 2;
@@ -1121,6 +1127,11 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
         if (!had_block && lane == 0)
           left[2 * warp + slot] = Left{from, cc.b, cc.u, cc.s.tiles, true};
         first_seg = false;
+        // (the last column's sequence, of which every unit says the same)
+        if (!a.by_seq && cc.u == 0 && cc.col + 1 == ncol && lane == 0)
+          a.shared[blockIdx.x] =
+              Shared{cc.b, (int)blockIdx.x,
+                     from >= c0 && to > c1 ? (to - 1) / run - (int)blockIdx.x + 1 : 0, 0};
       }
       if (i + 1 < n) next(cc);
     }
@@ -1128,9 +1139,10 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
   }
 
   // sequences of no keys: zeros, from one block each
+#pragma unroll 1
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const Seq s = seq_of(a, b);
-    if (s.bad || s.tiles) continue;
+    const int len = a.lens[b];
+    if (len != 0) continue;
     for (int i = tid; i < a.Hq * a.dv; i += kThreads)
       from_float(static_cast<QT*>(a.out) + (size_t)b * a.Hq * a.dv + i, 0.0f);
     if (a.lse)
@@ -1138,30 +1150,14 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
   }
 
   // what the second launch has to do: by sequence (block b says it of sequence
-  // b), or by block, of the sequence that begins in its columns and goes on
-  if (tid == 0) {
-    Shared s = {0, 0, 0, 0};
-    int64_t from = 0, to = 0;
-    if (a.by_seq) {
-      s.b = blockIdx.x;
-      if (s.b < a.B) {
-        from = before[s.b];  // (one sequence per thread here)
-        to = from + seq_of(a, s.b).tiles;
-      }
-    } else if (ncol) {
-      const Cursor c = locate(c1 - 1);
-      s.b = c.b;
-      from = c1 - 1 - c.t;
-      to = from + c.s.tiles;
-      if (from < c0) to = from;
-    }
-    if (to > from) {
-      s.block = (int)(from / run);
-      s.blocks = (int)((to - 1) / run) - s.block + 1;
-      if (s.blocks == 1) s.blocks = 0;
-    }
-    if (!a.by_seq || blockIdx.x < a.B) a.shared[blockIdx.x] = s;
+  // b; one sequence per thread then), or by block, of the sequence that begins
+  // in its columns and goes on (said above, by the warp that came upon it)
+  if (tid == 0 && a.by_seq && blockIdx.x < a.B) {
+    const int b = blockIdx.x, from = before[b], tiles = seq_of<TILE>(a, a.lens[b]).tiles;
+    const int at = from / run, n = tiles ? (from + tiles - 1) / run - at + 1 : 0;
+    a.shared[b] = Shared{b, at, n > 1 ? n : 0, 0};
   }
+  if (tid == 0 && !a.by_seq && ncol == 0) a.shared[blockIdx.x] = Shared{0, 0, 0, 0};
 
   // ---- the pieces of this block's warps, joined
   __syncthreads();
@@ -1206,7 +1202,7 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
       if (a.lse && c4 == 0) a.lse[orow] = log_sum(mx, l);
     } else {
       const size_t p =
-          (((size_t)blockIdx.x * 2 + (f.from < c0 ? 0 : 1)) * units + f.u) * a.hb + h;
+          (((size_t)blockIdx.x * 2 + (f.from < c0 ? 0 : 1)) * a.units + f.u) * a.hb + h;
       *reinterpret_cast<float4*>(a.block.part + p * a.dv + c4 * 4) = o;
       if (c4 == 0) *reinterpret_cast<float2*>(a.block.ml + p * 2) = make_float2(mx, l);
     }

@@ -546,8 +546,8 @@ LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *b
  * q          [B][H_q][d] of element type dtype, dense, 16-byte aligned.
  * cache, block_table, table_stride, max_pages   as for lt_kv_cache_read; the
  *            cache's type is dtype's own or 8 bits, and each pool spans at
- *            most 64 GiB (LT_ERR_INVALID_ARG otherwise, and for B * H_q times
- *            the tiles of max_pages pages above 2^40).
+ *            most 64 GiB (LT_ERR_INVALID_ARG otherwise, and where B times the
+ *            16-token tiles of max_pages pages pass 2^31, or 2^36 / H_q).
  * seq_lens   [B] int32 device.  A negative length, or one over max_pages
  *            pages, is reported (LT_ERR_DEVICE_BAD_SEQLENS) and its rows of
  *            out and lse are left as they were.  A page outside the pool is
