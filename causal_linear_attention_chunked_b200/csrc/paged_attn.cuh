@@ -23,8 +23,17 @@
 // that one warp had whole is finished by it.  Where several warps of a block
 // share it, each leaves a piece, and the block joins them at its end; where
 // several blocks share it, each leaves one, and a second launch (which starts
-// early and waits for the first) joins those.  Pieces are always added in the
-// order of the tiles, so results do not depend on timing.
+// early and waits for the first) joins those.  The order of joining follows
+// from the lengths alone, so results do not depend on timing.
+//
+// Measured on one B200 (plain copy 6.55 TB/s, reads alone up to 7.1), 32 query
+// over 8 KV heads of 128: 64 ragged sequences (266k tokens) bf16 170 us, 6.5 TB/s;
+// e4m3 99 us, 5.7 TB/s, where the widening of the codes keeps the issue slots
+// busy; one sequence of 65536 tokens, bf16, 50 us, of which 12 are the two
+// launches' starts and ends.  Runs of (sequence, KV head) pairs instead of whole
+// columns read the e4m3 rows of one token at different times: 128 us.  Bulk
+// copies of single rows are slower than 16-byte copies below 256 bytes a row
+// (128-byte rows 4.5 against 7.0 TB/s).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -130,7 +139,9 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) 
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -261,7 +272,7 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 // relative to 2^mx) and the piece both go by the larger maximum
 __device__ __forceinline__ void add_piece(float4& o, float& l, float& mx, float2 ml, float4 x) {
   const float top = fmaxf(mx, ml.x), base = top == -INFINITY ? 0.0f : top;
-  const float f = exp2f(mx - base), g = exp2f(ml.x - base);
+  const float f = exp2_fast(mx - base), g = exp2_fast(ml.x - base);
   mx = top;
   l = fmaf(g, ml.y, f * l);
   o.x = fmaf(g, x.x, f * o.x);
@@ -669,11 +680,12 @@ struct MmaEngine {
 // ---------------------------------------------------- engine: fp32 caches
 // Tensor cores in tf32, every factor in two terms: x = hi + lo, hi the nearest
 // tf32 value (11 bits) and lo the rest, of which the instruction keeps 11 bits;
-// x y ~ hi hi + hi lo + lo hi is off by about 2^-21 of |x y|, either way.  The instruction's additions cut where fp32's
-// round, so chains of them are kept short: a tile's values are summed from zero
-// and added to the rest by plain additions (one long chain was four times
-// further off at 65000 keys).  Plain fp32 multiplications bound this kernel at
-// 3 TB/s for 4 query heads per KV head.
+// x y ~ hi hi + hi lo + lo hi is off by about 2^-21 of |x y|, either way.  The
+// instruction's additions cut where fp32's round, so chains of them are kept
+// short: a tile's values are summed from zero and added to the rest by plain
+// additions (one long chain was seven times further off at 65000 keys).  Plain
+// fp32 multiplications bound this kernel at 3 TB/s for 4 query heads per KV head;
+// so it reads 5.4 TB/s.  Values of 2^127 and more round to infinity.
 //
 // The same two products as MmaEngine, in steps of 8: S^T = K Q^T with A = K, O^T
 // = V^T P^T with A = V^T.  32-bit tiles have no ldmatrix, so rows and steps are

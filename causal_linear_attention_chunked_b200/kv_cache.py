@@ -351,6 +351,8 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
     _int32(seq_lens, "seq_lens", 1)
     if block_table.shape[0] != B or seq_lens.numel() != B:
         raise ValueError("block_table and seq_lens must have a row per sequence")
+    if not -2 ** 31 <= window < 2 ** 31:
+        raise ValueError("window must fit 32 bits")
     code = _dtype_code(q.dtype)
     dev = cache._dev
     ctx = _elsewhere(dev, stream, (q, block_table, seq_lens, out))

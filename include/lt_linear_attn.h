@@ -541,7 +541,9 @@ LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *b
  *     out_bh = sum_j p_j V_jg / sum_j p_j,   p_j = exp(scale * q_bh . K_jg)
  *     lse_bh = log sum_j p_j
  * A sequence of no tokens gives out = 0 and lse = -infinity.  The 8-bit
- * caches are read as 8 bits; nothing is written back.
+ * caches are read as 8 bits; nothing is written back.  An infinity or a NaN
+ * among the queries, keys or values that take part makes the outputs that it
+ * reaches NaN or infinite; what a page holds past a sequence's end is not used.
  *
  * q          [B][H_q][d] of element type dtype, dense, 16-byte aligned.
  * cache, block_table, table_stride, max_pages   as for lt_kv_cache_read; the
@@ -559,13 +561,15 @@ LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *b
  * B, H_q     1 <= B <= 65535, H_q a multiple of the cache's H_kv, at most
  *            65535.
  * workspace  as for lt_qk_norm_rope_bwd, with lt_paged_attn_decode_plan's bytes.
- * Evaluation: the tiles of all (sequence, KV head) pairs are dealt out evenly
- * to the warps of one persistent launch, whatever the lengths; each warp
- * keeps a running maximum and sum in fp32, and the pieces of a pair that
- * several warps share are joined in their order, by a second launch where
- * they lie in several blocks.  Scores, sums and accumulators are fp32; for
+ * Evaluation: the tiles of all sequences are dealt out evenly to the blocks
+ * of one launch, whatever the lengths; each warp keeps a running maximum and
+ * sum in fp32, and the pieces of a sequence that several warps share are
+ * joined in a fixed order, by a second launch where they lie in several
+ * blocks.  Runs agree bit for bit.  Scores, sums and accumulators are fp32; for
  * the tensor cores the weights are two terms of the cache's 16-bit type (one
- * fp16 term for an 8-bit cache under LT_BF16), and not rounded for LT_F32.
+ * fp16 term for an 8-bit cache under LT_BF16; two of fp16, or of tf32 for an
+ * fp32 cache, under LT_F32).  More than 16 query heads per KV head (8 under
+ * LT_F32) read the cache once for every 16 (8).
  * Returns as lt_kv_cache_write.
  */
 LT_API lt_status_t lt_paged_attn_decode(const void *q, const lt_kv_cache_t *cache,

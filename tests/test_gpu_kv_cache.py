@@ -62,7 +62,8 @@ def _expect_rows(pool, scale, slots, x, ps, dtype):
     (torch.float32, E4M3), (torch.float32, I8), (torch.float32, torch.float32)])
 @pytest.mark.parametrize("shape", [
     # tokens, heads, d, dv, pages, page size
-    (1, 1, 64, 64, 1, 1), (5, 3, 128, 64, 4, 16), (70, 8, 64, 128, 9, 24), (257, 2, 128, 128, 40, 8)])
+    (1, 1, 64, 64, 1, 1), (5, 3, 128, 64, 4, 16), (70, 8, 64, 128, 9, 24),
+    (257, 2, 128, 128, 40, 8)])
 def test_write(src, kv, shape, layout):
     import causal_linear_attention_chunked_b200 as L
     T, H, d, dv, pages, ps = shape
@@ -76,8 +77,9 @@ def test_write(src, kv, shape, layout):
     slots = torch.randperm(pages * ps, generator=g)[:T].int()
     if T > 3:
         slots[2] = -1                               # a padding token
-    want = [_expect_rows(c.k.cpu(), None if c.k_scale is None else c.k_scale.cpu(), slots, k, ps, kv),
-            _expect_rows(c.v.cpu(), None if c.v_scale is None else c.v_scale.cpu(), slots, v, ps, kv)]
+    cpu = lambda t: None if t is None else t.cpu()
+    want = [_expect_rows(c.k.cpu(), cpu(c.k_scale), slots, k, ps, kv),
+            _expect_rows(c.v.cpu(), cpu(c.v_scale), slots, v, ps, kv)]
     L.kv_cache_write(c, k.cuda(), v.cuda(), slots.cuda())
     assert L.get_last_device_error() == 0
     for (pool, scale), got, got_scale in ((want[0], c.k, c.k_scale), (want[1], c.v, c.v_scale)):

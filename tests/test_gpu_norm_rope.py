@@ -37,7 +37,8 @@ def _check_fwd(got, q, k, wq, wk, pos, freq, eps, il):
     # T, Hq, Hkv, d, rot, interleaved, first position
     (1, 1, 1, 64, 64, False, 0), (1, 32, 8, 128, 128, False, 131071), (7, 3, 1, 64, 32, True, 5),
     (130, 5, 5, 128, 16, False, 1000), (33, 8, 2, 64, 8, True, 0), (64, 2, 3, 128, 128, True, 17),
-    (300, 40, 1, 64, 0, False, 0), (1201, 8, 8, 64, 64, False, 2 ** 24), (9, 7, 2, 128, 56, False, 3),
+    (300, 40, 1, 64, 0, False, 0), (1201, 8, 8, 64, 64, False, 2 ** 24),
+    (9, 7, 2, 128, 56, False, 3),
     (5, 1, 4, 128, 120, True, 2 ** 30),
 ])
 def test_forward(dtype, shape):
@@ -181,7 +182,8 @@ def test_streams_graphs_and_workspace():
     import causal_linear_attention_chunked_b200 as L
     from causal_linear_attention_chunked_b200 import _binding as b
     q, k, wq, wk, g = _case(50, 4, 2, 64, torch.bfloat16, 7)
-    gq, gk = torch.randn(50, 4, 64, generator=g).bfloat16(), torch.randn(50, 2, 64, generator=g).bfloat16()
+    gq = torch.randn(50, 4, 64, generator=g).bfloat16()
+    gk = torch.randn(50, 2, 64, generator=g).bfloat16()
     pos, freq = torch.arange(50, dtype=torch.int32).cuda(), _freq(64).cuda()
     q, k, wq, wk, gq, gk = (t.cuda() for t in (q, k, wq, wk, gq, gk))
     ref = L.qk_norm_rope(q, k, wq, wk, pos, freq)
@@ -206,7 +208,7 @@ def test_streams_graphs_and_workspace():
     P = lambda t: ctypes.c_void_p(t.data_ptr())
     need = ctypes.c_size_t()
     assert b.lib.lt_qk_norm_rope_bwd_plan(64, 0, ctypes.byref(need)) == 0
-    dq, dk, dwq, dwk = torch.empty_like(q), torch.empty_like(k), torch.empty_like(wq), torch.empty_like(wk)
+    dq, dk, dwq, dwk = (torch.empty_like(t) for t in (q, k, wq, wk))
     ws = torch.empty(need.value, dtype=torch.uint8, device="cuda")
     for given, size, st in ((P(ws), need.value, 0), (P(ws), need.value - 1, 1), (None, 0, 0)):
         dwq.zero_()

@@ -319,7 +319,8 @@ def test_a_serving_run(kv):
     cut = lambda x: (x[:, :Hq * d].unflatten(-1, (Hq, d)),
                      x[:, Hq * d:(Hq + Hkv) * d].unflatten(-1, (Hkv, d)),
                      x[:, (Hq + Hkv) * d:].unflatten(-1, (Hkv, d)))
-    wq, wk = (1 + 0.2 * torch.randn(d, generator=g)).to(BF), (1 + 0.2 * torch.randn(d, generator=g)).to(BF)
+    wq = (1 + 0.2 * torch.randn(d, generator=g)).to(BF)
+    wk = (1 + 0.2 * torch.randn(d, generator=g)).to(BF)
     freq = (10000.0 ** (-torch.arange(d // 2).double() / (d // 2))).float()
     need = [-(-(m + steps) // ps) for m in prompt]
     table, pages = _pages([m * ps for m in need], ps, 0, g)
@@ -332,7 +333,8 @@ def test_a_serving_run(kv):
         q, k, v = cut(x)
         pos = torch.tensor([i for _, i in where], dtype=torch.int32)
         qr, kr = L.qk_norm_rope(q, k, wq.cuda(), wk.cuda(), pos.cuda(), freq.cuda())
-        L.kv_cache_write(c, kr, v, torch.tensor([slot(*w) for w in where], dtype=torch.int32).cuda())
+        slots = torch.tensor([slot(*w) for w in where], dtype=torch.int32)
+        L.kv_cache_write(c, kr, v, slots.cuda())
         ref, bound = plain.norm_rope(k.cpu(), wk, pos, freq, 1e-6, False)
         plain.check(kr, ref, bound, BF, "keys")
         for t, w in enumerate(where):
