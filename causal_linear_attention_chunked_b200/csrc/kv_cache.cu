@@ -9,7 +9,7 @@
 //
 // Bound by memory, quantising also close to instruction issue: the maximum of
 // a 16-bit row is taken two values at a time, and the quotients by a
-// multiplication and two corrections that round them exactly (see quotients).
+// multiplication with corrections (below) whose codes are the division's.
 // A row is spread over w/16 lanes (the maximum is a 2- or 3-step shuffle);
 // each lane moves two chunks of 8 elements, w/2 apart, so that both the 16-bit
 // and the 8-bit side are accessed in whole runs.  A block walks tiles of tokens;
@@ -17,7 +17,7 @@
 // memory, for all heads, while the rows of the tile before are under way.
 //
 // Measured on one B200 (plain copy 6.55 TB/s): 32768 bf16 tokens of 8 heads of
-// 128, keys and values, into e4m3 pages 43 us, 4.7 TB/s; 64 ragged sequences (266k
+// 128, keys and values, into e4m3 pages 41 us, 5.0 TB/s; 64 ragged sequences (266k
 // tokens of 8 heads of 64) back from e4m3 to bf16 134 us, 6.3 TB/s.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -62,9 +62,11 @@ struct CacheArgs {
   int* err;
 };
 
-// where a token's rows are: page and slot, or page -1
+// where a token's rows are in a pool and its scales: offsets of its first head,
+// or -1
 struct Place {
-  int page, slot;
+  int64_t row;    // elements
+  int64_t scale;  // a head's scales are page_size apart
 };
 
 // A block's (token, head) rows in order, advanced by a fixed step.
@@ -192,48 +194,37 @@ __device__ __forceinline__ uint32_t top_bits(const Chunk<__half>& c) {
 //
 // What is computed is minus the quotient, p = -(x v), p + (x + p b)(-v): so a
 // zero keeps its sign, which x - q b would lose.
-struct Divisor {
-  float b, v;
-  bool exact;  // by multiplication
-};
 template <int kCorrections>
-__device__ __forceinline__ F2 minus_quotient(F2 x, const Divisor& d) {
-  const F2 n = pack_f2(-d.v, -d.v), b = pack_f2(d.b, d.b);
-  F2 p = mul2(x, n);
+__device__ __forceinline__ F2 minus_quotient(F2 x, F2 b, F2 minus_v) {
+  F2 p = mul2(x, minus_v);
 #pragma unroll
-  for (int i = 0; i < kCorrections; ++i) p = fma2(fma2(p, b, x), n, p);
+  for (int i = 0; i < kCorrections; ++i) p = fma2(fma2(p, b, x), minus_v, p);
   return p;
 }
-// a row's scale from the bits of its largest magnitude
-template <typename KV>
-__device__ __forceinline__ Divisor scale_of(uint32_t top) {
+// y[0..7] -> -(y / scale), with the row's scale from the bits of its largest
+// magnitude (NaN where that is not finite)
+template <typename T, typename KV>
+__device__ __forceinline__ float minus_quotients(F2* y, uint32_t top) {
   constexpr float kMax = KvMax<KV>::value;
-  Divisor d;
-  d.exact = top - 0x21800000u <= 0x5d800000u - 0x21800000u;  // 2^-60 .. 2^60
   const float x = __uint_as_float(top);
-  if (d.exact) {
+  if (top - 0x21800000u <= 0x5d800000u - 0x21800000u) {  // 2^-60 .. 2^60
     constexpr float v = 1.0f / kMax;  // rounded by the compiler
     float q = x * v;
     q = fmaf(fmaf(q, -kMax, x), v, q);
-    d.b = fmaf(fmaf(q, -kMax, x), v, q);
-  } else {
-    d.b = fmaxf(__fdiv_rn(x, kMax), kTiny);
-  }
-  d.v = __frcp_rn(d.b);
-  return d;
-}
-template <typename T>
-__device__ __forceinline__ void minus_quotients(F2* y, const Divisor& d) {
-  if (d.exact) {
+    q = fmaf(fmaf(q, -kMax, x), v, q);
+    const float r = -__frcp_rn(q);
+    const F2 b = pack_f2(q, q), n = pack_f2(r, r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = minus_quotient<sizeof(T) == 2 ? 1 : 2>(y[e], d);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 x = unpack_f2(y[e]);
-      y[e] = pack_f2(__fdiv_rn(x.x, -d.b), __fdiv_rn(x.y, -d.b));
-    }
+    for (int e = 0; e < 8; ++e) y[e] = minus_quotient<sizeof(T) == 2 ? 1 : 2>(y[e], b, n);
+    return q;
   }
+  const float b = fmaxf(__fdiv_rn(x, kMax), kTiny);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float2 z = unpack_f2(y[e]);
+    y[e] = pack_f2(__fdiv_rn(z.x, -b), __fdiv_rn(z.y, -b));
+  }
+  return top < 0x7f800000u ? b : __uint_as_float(0x7fc00000u);
 }
 
 // the codes of -y[0..3]
@@ -282,14 +273,21 @@ __device__ __forceinline__ void decode(uint2 r, F2* y, Int8) {
 }
 
 // ---------------------------------------------------------- tokens' places
-__device__ __forceinline__ Place place_of_slot(const CacheArgs& a, int64_t t) {
+__device__ __forceinline__ Place place_at(const CacheArgs& a, const Pool& pool, int page,
+                                          int slot) {
+  return Place{(int64_t)page * pool.page + (int64_t)slot * pool.slot,
+               (int64_t)page * a.H * a.page_size + slot};
+}
+
+__device__ __forceinline__ Place place_of_slot(const CacheArgs& a, const Pool& pool, int64_t t) {
   const int s = a.slots[t];
-  if (s >= 0 && s / a.page_size < a.num_pages) return Place{s / a.page_size, s % a.page_size};
+  const int page = s / a.page_size;  // (meaningless below 0)
+  if (s >= 0 && page < a.num_pages) return place_at(a, pool, page, s - page * a.page_size);
   if (s != -1) report_error(a.err, kDevErrBadPage);
   return Place{-1, 0};
 }
 
-__device__ __forceinline__ Place place_of_row(const CacheArgs& a, int t) {
+__device__ __forceinline__ Place place_of_row(const CacheArgs& a, const Pool& pool, int t) {
   // the sequence that holds row t: the last s with cu[s] <= t; a row that no
   // sequence holds is left alone
   int lo = 0, hi = a.B;
@@ -305,7 +303,7 @@ __device__ __forceinline__ Place place_of_row(const CacheArgs& a, int t) {
       (int64_t)end - begin <= (int64_t)a.max_pages * a.page_size) {
     const int i = t - begin, n = i / a.page_size;
     const int page = __ldg(a.table + (int64_t)lo * a.table_stride + n);
-    if (page >= 0 && page < a.num_pages) return Place{page, i - n * a.page_size};
+    if (page >= 0 && page < a.num_pages) return place_at(a, pool, page, i - n * a.page_size);
     report_error(a.err, kDevErrBadPage);
   }
   return Place{-1, 0};
@@ -361,7 +359,7 @@ __device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool,
       const int tt = live ? at.tt : 0;
       hd[u] = live ? at.h : 0;
       pl[u] = place[tt];
-      if (!live) pl[u].page = -1;
+      if (!live) pl[u].row = -1;
       const T* p = in + tt * stride + hd[u] * WIDTH;
       x[u][0] = load_chunk(p);
       x[u][1] = load_chunk(p + HALF);
@@ -372,25 +370,18 @@ __device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool,
       uint32_t top = max(top_bits(x[u][0]), top_bits(x[u][1]));
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool finite = top < 0x7f800000u;
-      const Divisor d = scale_of<KV>(top);
-      uint2 code[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        F2 y[4];
-        widen8(x[u][c], y);
-        minus_quotients<T>(y, d);
-        code[c] = encode_minus(y, KV());
-      }
-      if (pl[u].page >= 0) {
-        uint8_t* out = static_cast<uint8_t*>(pool.p) + (int64_t)pl[u].page * pool.page +
-                       (int64_t)pl[u].slot * pool.slot + (int64_t)hd[u] * pool.head + j * 8;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<uint2*>(out + c * HALF) = finite ? code[c] : make_uint2(0, 0);
-        if (j == 0)
-          pool.scale[((int64_t)pl[u].page * a.H + hd[u]) * a.page_size + pl[u].slot] =
-              finite ? d.b : __uint_as_float(0x7fc00000u);
+      F2 y[2][4];
+      widen8(x[u][0], y[0]);
+      widen8(x[u][1], y[1]);
+      const float scale = minus_quotients<T, KV>(y[0], top);
+      uint2 code[2] = {encode_minus(y[0], KV()), encode_minus(y[1], KV())};
+      if (top >= 0x7f800000u) code[0] = code[1] = make_uint2(0, 0);
+      if (pl[u].row >= 0) {
+        uint8_t* out =
+            static_cast<uint8_t*>(pool.p) + pl[u].row + hd[u] * pool.head + j * 8;
+        *reinterpret_cast<uint2*>(out) = code[0];
+        *reinterpret_cast<uint2*>(out + HALF) = code[1];
+        if (j == 0) pool.scale[pl[u].scale + (int64_t)hd[u] * a.page_size] = scale;
       }
     }
   }
@@ -413,15 +404,13 @@ __device__ __forceinline__ void dequant_rows(const CacheArgs& a, const Pool& poo
       live[u] = false;
       if (r + u * RG < n) {
         const Place pl = place[at.tt];
-        live[u] = pl.page >= 0;
+        live[u] = pl.row >= 0;
         if (live[u]) {
-          const uint8_t* p = static_cast<const uint8_t*>(pool.p) + (int64_t)pl.page * pool.page +
-                             (int64_t)pl.slot * pool.slot + (int64_t)at.h * pool.head +
-                             j * 8;
+          const uint8_t* p =
+              static_cast<const uint8_t*>(pool.p) + pl.row + at.h * pool.head + j * 8;
           code[u][0] = __ldg(reinterpret_cast<const uint2*>(p));
           code[u][1] = __ldg(reinterpret_cast<const uint2*>(p + HALF));
-          scale[u] =
-              __ldg(&pool.scale[((int64_t)pl.page * a.H + at.h) * a.page_size + pl.slot]);
+          scale[u] = __ldg(&pool.scale[pl.scale + (int64_t)at.h * a.page_size]);
         }
       }
       at.next();
@@ -451,7 +440,7 @@ __device__ __forceinline__ void quant_walk(const CacheArgs& a, const Pool& pool,
   constexpr int L = WIDTH / 16;
   const RowAt at(threadIdx.x / L, kT / L, a.H);
   walk_tiles(
-      a.tokens, a.tok, [&](int64_t t) { return place_of_slot(a, t); },
+      a.tokens, a.tok, [&](int64_t t) { return place_of_slot(a, pool, t); },
       [&](int64_t t0, int nt, const Place* place) {
         quant_rows<T, KV, WIDTH>(a, pool, in + t0 * stride, stride, place, nt, at);
       });
@@ -471,7 +460,7 @@ __device__ __forceinline__ void dequant_walk(const CacheArgs& a, const Pool& poo
   constexpr int L = WIDTH / 16;
   const RowAt at(threadIdx.x / L, kT / L, a.H);
   walk_tiles(
-      a.N, a.tok, [&](int64_t t) { return place_of_row(a, (int)t); },
+      a.N, a.tok, [&](int64_t t) { return place_of_row(a, pool, (int)t); },
       [&](int64_t t0, int nt, const Place* place) {
         dequant_rows<T, KV, WIDTH>(a, pool, out + t0 * a.H * WIDTH, place, nt, at);
       });
@@ -500,7 +489,7 @@ __global__ void __launch_bounds__(kT) lt_kv_copy_kernel(const CacheArgs a) {
   const RowAt first(grp, RG, a.H);
   walk_tiles(
       kWrite ? a.tokens : (int64_t)a.N, a.tok,
-      [&](int64_t t) { return kWrite ? place_of_slot(a, t) : place_of_row(a, (int)t); },
+      [&](int64_t t) { return kWrite ? place_of_slot(a, pool, t) : place_of_row(a, pool, (int)t); },
       [&](int64_t t0, int nt, const Place* place) {
         const int n = nt * a.H;
         const uint8_t* in = static_cast<const uint8_t*>(a.in[which]) + t0 * stride + j * 16;
@@ -515,9 +504,9 @@ __global__ void __launch_bounds__(kT) lt_kv_copy_kernel(const CacheArgs a) {
             dst[u] = nullptr;
             if (r + u * RG < n) {
               const Place pl = place[at.tt];
-              if (pl.page >= 0) {
-                uint8_t* row = static_cast<uint8_t*>(pool.p) + (int64_t)pl.page * pool.page +
-                               (int64_t)pl.slot * pool.slot + (int64_t)at.h * pool.head + j * 16;
+              if (pl.row >= 0) {
+                uint8_t* row =
+                    static_cast<uint8_t*>(pool.p) + pl.row + at.h * pool.head + j * 16;
                 const uint8_t* src = kWrite ? in + at.tt * stride + at.h * pool.w : row;
                 dst[u] = kWrite ? row : out + (int64_t)(r + u * RG) * pool.w;
                 x[u] = __ldg(reinterpret_cast<const uint4*>(src));
