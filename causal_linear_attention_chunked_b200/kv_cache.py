@@ -321,9 +321,9 @@ def kv_cache_read(cache, block_table, cu_seqlens, N, dtype=None, k_out=None, v_o
         with ctx:
             return kv_cache_read(cache, block_table, cu_seqlens, N, dtype, k_out, v_out)
     k_shape, v_shape = (N, cache.H_kv, cache.d), (N, cache.H_kv, cache.dv)
-    k_out = cache.k.new_empty(k_shape, dtype=dtype) if k_out is None \
+    k_out = cache.k.new_empty(*k_shape, dtype=dtype) if k_out is None \
         else _given(k_out, k_shape, dtype, "k_out")
-    v_out = cache.k.new_empty(v_shape, dtype=dtype) if v_out is None \
+    v_out = cache.k.new_empty(*v_shape, dtype=dtype) if v_out is None \
         else _given(v_out, v_shape, dtype, "v_out")
     pages = block_table.shape[1]
     _check(lib.lt_kv_cache_read(cache._ref, block_table.data_ptr(),
@@ -360,9 +360,9 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
         with ctx:
             return paged_attn_decode(q, cache, block_table, seq_lens, scale, window, out,
                                      return_lse)
-    out = q.new_empty((B, Hq, cache.dv)) if out is None \
+    out = q.new_empty(B, Hq, cache.dv) if out is None \
         else _given(out, (B, Hq, cache.dv), q.dtype, "out")
-    lse = q.new_empty((B, Hq), dtype=torch.float32) if return_lse else None
+    lse = q.new_empty(B, Hq, dtype=torch.float32) if return_lse else None
     ws_bytes = cache._workspace(Hq, code)
     ws = q.new_empty(ws_bytes, dtype=torch.uint8)
     pages = block_table.shape[1]
