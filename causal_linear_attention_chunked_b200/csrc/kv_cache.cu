@@ -625,10 +625,10 @@ lt_status_t check_cache(const lt_kv_cache_t* c) {
   return LT_OK;
 }
 
-lt_status_t check_cache_pointers(const lt_kv_cache_t* c) {
-  if (!on_current_device(c->k) || !on_current_device(c->v) ||
-      (c->k_scale && !on_current_device(c->k_scale)) ||
-      (c->v_scale && !on_current_device(c->v_scale)))
+lt_status_t check_cache_pointers(int dev, const lt_kv_cache_t* c) {
+  if (!on_device(dev, c->k) || !on_device(dev, c->v) ||
+      (c->k_scale && !on_device(dev, c->k_scale)) ||
+      (c->v_scale && !on_device(dev, c->v_scale)))
     return LT_ERR_INVALID_ARG;
   return LT_OK;
 }
@@ -665,8 +665,9 @@ extern "C" lt_status_t lt_kv_cache_write(const lt_kv_cache_t* cache, const void*
   for (const Span& p : pools)
     for (const Span& i : ins)
       if (spans_overlap(p, i)) return LT_ERR_INVALID_ARG;
-  if (check_cache_pointers(cache) != LT_OK || !on_current_device(k) || !on_current_device(v) ||
-      !on_current_device(slots))
+  const int dev = current_device();
+  if (check_cache_pointers(dev, cache) != LT_OK || !on_device(dev, k) || !on_device(dev, v) ||
+      !on_device(dev, slots))
     return LT_ERR_INVALID_ARG;
   CacheArgs a = args_of(cache);
   a.in[0] = k;
@@ -692,8 +693,8 @@ extern "C" lt_status_t lt_kv_cache_read(const lt_kv_cache_t* cache, const int32_
   if (st != LT_OK) return st;
   if (!dtype_ok(dtype) || (!eight_bit(cache->dtype) && cache->dtype != kv_of(dtype)))
     return LT_ERR_UNSUPPORTED;
-  if (!block_table || !cu_seqlens || !k_out || !v_out || B < 1 || N < 1 || max_pages < 1 ||
-      table_stride < max_pages || table_stride > ((int64_t)1 << 40) ||
+  if (!block_table || !cu_seqlens || !k_out || !v_out || B < 1 || B > (1 << 30) || N < 1 ||
+      max_pages < 1 || table_stride < max_pages || table_stride > ((int64_t)1 << 40) ||
       !aligned_to(block_table, 4) || !aligned_to(cu_seqlens, 4) || !aligned_to(k_out, 16) ||
       !aligned_to(v_out, 16))
     return LT_ERR_INVALID_ARG;
@@ -707,8 +708,9 @@ extern "C" lt_status_t lt_kv_cache_read(const lt_kv_cache_t* cache, const int32_
   if (spans_overlap(ko, vo)) return LT_ERR_INVALID_ARG;
   for (const Span& i : ins)
     if (spans_overlap(ko, i) || spans_overlap(vo, i)) return LT_ERR_INVALID_ARG;
-  if (check_cache_pointers(cache) != LT_OK || !on_current_device(block_table) ||
-      !on_current_device(cu_seqlens) || !on_current_device(k_out) || !on_current_device(v_out))
+  const int dev = current_device();
+  if (check_cache_pointers(dev, cache) != LT_OK || !on_device(dev, block_table) ||
+      !on_device(dev, cu_seqlens) || !on_device(dev, k_out) || !on_device(dev, v_out))
     return LT_ERR_INVALID_ARG;
   CacheArgs a = args_of(cache);
   a.table = block_table;

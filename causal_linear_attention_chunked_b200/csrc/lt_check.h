@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "lt_fault.h"
 #include "lt_internal.h"
 
@@ -13,17 +15,40 @@ inline bool aligned_to(const void* p, unsigned a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
-// memory that a kernel on the current device may use: managed, or device
+// the current device, or -1
+inline int current_device() {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();  // clear the non-sticky error
+    return -1;
+  }
+  return dev;
+}
+
+// memory that a kernel on the current device (dev) may use: managed, or device
 // memory of that very device (a pointer of another device is refused here
 // rather than read over the bus)
-inline bool on_current_device(const void* p) {
+inline bool on_device(int dev, const void* p) {
   cudaPointerAttributes at;
-  int dev = 0;
-  if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();  // clear the non-sticky error
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+    cudaGetLastError();
     return false;
   }
   return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
+}
+
+// Lets `kern` use `bytes` of dynamic shared memory, once per device: `done` is
+// the kernel's own set of devices (a repeated call costs the host about as
+// much as a pointer check).
+inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done) {
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 struct Span {
@@ -58,7 +83,7 @@ inline bool stride_ok(int64_t tokens, int64_t stride, int64_t H, int64_t w, size
 
 // The checks of a cache that need no CUDA call, then (pointers) those that do.
 lt_status_t check_cache(const lt_kv_cache_t* c);
-lt_status_t check_cache_pointers(const lt_kv_cache_t* c);
+lt_status_t check_cache_pointers(int dev, const lt_kv_cache_t* c);
 // the four address ranges of a cache's pools and scales
 void cache_spans(const lt_kv_cache_t* c, Span out[4]);
 
@@ -67,10 +92,10 @@ struct Workspace {
   void* p = nullptr;
   bool own = false;
   cudaStream_t stream;
-  lt_status_t take(void* given, size_t given_bytes, size_t need, cudaStream_t s) {
+  lt_status_t take(int dev, void* given, size_t given_bytes, size_t need, cudaStream_t s) {
     stream = s;
     if (given) {
-      if (given_bytes < need || !aligned_to(given, 16) || !on_current_device(given))
+      if (given_bytes < need || !aligned_to(given, 16) || !on_device(dev, given))
         return LT_ERR_INVALID_ARG;
       p = given;
       return LT_OK;

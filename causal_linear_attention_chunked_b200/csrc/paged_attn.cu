@@ -166,7 +166,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   const int64_t pages_hold = (int64_t)max_pages * cache->page_size;
   const int most = (int)(pages_hold < 0x7fffff00 ? pages_hold : 0x7fffff00);
   const int64_t columns = (int64_t)B * (most / 16 + 1);
-  if (!pools_within(cache, (size_t)64 << 30) || columns > 0x7fffffff ||
+  if (!pools_within(cache, (size_t)64 << 30) || columns > 0x7fff0000 ||
       columns > ((int64_t)1 << 36) / H_q)
     return LT_ERR_INVALID_ARG;
   const size_t es = dtype_size(dtype);
@@ -182,9 +182,10 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
     if (spans_overlap(o, i) || spans_overlap(ls, i)) return LT_ERR_INVALID_ARG;
   for (int i = 0; i < 7; ++i)
     if (spans_overlap(ins[7], ins[i])) return LT_ERR_INVALID_ARG;
-  if (check_cache_pointers(cache) != LT_OK || !on_current_device(q) ||
-      !on_current_device(block_table) || !on_current_device(seq_lens) || !on_current_device(out) ||
-      (lse && !on_current_device(lse)))
+  const int dev = current_device();
+  if (check_cache_pointers(dev, cache) != LT_OK || !on_device(dev, q) ||
+      !on_device(dev, block_table) || !on_device(dev, seq_lens) || !on_device(dev, out) ||
+      (lse && !on_device(dev, lse)))
     return LT_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   int* err = device_error_word_current();
@@ -195,7 +196,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.nhb = (a.G + a.hb - 1) / a.hb;
   const Sizes z = sizes_of(dtype, cache->dtype, H_q, cache->H_kv, cache->dv, sms);
   Workspace w;
-  const lt_status_t sw = w.take(workspace, workspace_bytes, z.bytes, (cudaStream_t)stream);
+  const lt_status_t sw = w.take(dev, workspace, workspace_bytes, z.bytes, (cudaStream_t)stream);
   if (sw != LT_OK) return sw;
   a.q = q;
   a.k = static_cast<const uint8_t*>(cache->k);

@@ -1226,8 +1226,8 @@ cudaError_t launch_engine(const DecodeArgs& a, int sms, cudaStream_t stream) {
   if (a.tile != E::kTile) return cudaErrorInvalidValue;  // the workspace's sizes go by them
   auto kern = lt_paged_decode_kernel<E>;
   constexpr int smem = Ring<E>::kBytes;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(sms), E::kWarps * 32, smem, stream, a);
 }

@@ -471,8 +471,8 @@ template <typename T, int D, bool IL, bool kBack>
 cudaError_t launch_t(const NormArgs& a, int blocks, cudaStream_t stream) {
   constexpr int smem = Ring<T, D, kBack>::kBytes;
   auto kern = lt_norm_rope_kernel<T, D, IL, kBack>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
   kern<<<blocks, kT, smem, stream>>>(a);
   return cudaGetLastError();
@@ -582,10 +582,11 @@ extern "C" lt_status_t lt_qk_norm_rope(const void* q, const void* k, const void*
   const Span outs[] = {{q_out, (size_t)tokens * H_q * d * es},
                        {k_out, (size_t)tokens * H_kv * d * es}};
   if (!disjoint(outs, 2, ins, 6)) return LT_ERR_INVALID_ARG;
+  const int dev = current_device();
   for (const Span& s : ins)
-    if (s.p && !on_current_device(s.p)) return LT_ERR_INVALID_ARG;
+    if (s.p && !on_device(dev, s.p)) return LT_ERR_INVALID_ARG;
   for (const Span& s : outs)
-    if (!on_current_device(s.p)) return LT_ERR_INVALID_ARG;
+    if (!on_device(dev, s.p)) return LT_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return LT_ERR_CUDA;
   NormArgs a = {};
@@ -662,10 +663,11 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
   if (!disjoint(a1, 3, ins, 9) || !disjoint(a2, 3, ins, 9) ||
       !slices_disjoint(sq, dq_stride, nq * es, sk, dk_stride, nk * es, es))
     return LT_ERR_INVALID_ARG;
+  const int dev = current_device();
   for (const Span& s : ins)
-    if (s.p && s.p != workspace && !on_current_device(s.p)) return LT_ERR_INVALID_ARG;
-  if (!on_current_device(dq) || !on_current_device(dk) ||
-      (dq_weight && !on_current_device(dq_weight)) || (dk_weight && !on_current_device(dk_weight)))
+    if (s.p && s.p != workspace && !on_device(dev, s.p)) return LT_ERR_INVALID_ARG;
+  if (!on_device(dev, dq) || !on_device(dev, dk) ||
+      (dq_weight && !on_device(dev, dq_weight)) || (dk_weight && !on_device(dev, dk_weight)))
     return LT_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return LT_ERR_CUDA;
@@ -675,7 +677,7 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
   const int64_t blocks = block_count(tokens * parts, sms);
   Workspace w;
   if (gains) {
-    const lt_status_t sw = w.take(workspace, workspace_bytes,
+    const lt_status_t sw = w.take(dev, workspace, workspace_bytes,
                                   (size_t)kBlocks * sms * 2 * d * sizeof(float),
                                   (cudaStream_t)stream);
     if (sw != LT_OK) return sw;

@@ -249,10 +249,11 @@ class PagedKVCache:
         self.dtype, self.device, self._dev = k.dtype, k.device, k.get_device()
         self.num_pages, self.page_size, self.H_kv, self.d, self.dv = pages, page_size, H, d, \
             v.shape[3]
+        # (a dimension of one entry may have any stride: it is never taken)
+        kst, vst = ([s if n > 1 else 0 for s, n in zip(x.stride()[:3], x.shape)] for x in (k, v))
         self._c = KvCacheStruct(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if quant else None,
-            v_scale.data_ptr() if quant else None, k.stride(0), k.stride(1), k.stride(2),
-            v.stride(0), v.stride(1), v.stride(2), pages, page_size, H, d, v.shape[3],
+            v_scale.data_ptr() if quant else None, *kst, *vst, pages, page_size, H, d, v.shape[3],
             _KV_CODES[k.dtype])
         self._ref = ctypes.byref(self._c)
         self._workspace_bytes = {}

@@ -513,8 +513,8 @@ LT_API lt_status_t lt_kv_cache_write(const lt_kv_cache_t *cache, const void *k, 
  *
  * block_table [B][table_stride] int32 device, max_pages entries used per row;
  *            entries past a sequence's last page are not read.
- * cu_seqlens [B+1] int32 device, cu_seqlens[0] = 0, non-decreasing,
- *            cu_seqlens[B] <= N; rows of the outputs from cu_seqlens[B] on
+ * cu_seqlens [B+1] int32 device, 1 <= B <= 2^30, cu_seqlens[0] = 0,
+ *            non-decreasing, cu_seqlens[B] <= N; rows of the outputs from cu_seqlens[B] on
  *            are left as they were.  Inconsistent offsets, or a sequence
  *            longer than max_pages pages, are reported
  *            (LT_ERR_DEVICE_BAD_SEQLENS) and leave the rows that they describe
@@ -549,7 +549,8 @@ LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *b
  * cache, block_table, table_stride, max_pages   as for lt_kv_cache_read; the
  *            cache's type is dtype's own or 8 bits, and each pool spans at
  *            most 64 GiB (LT_ERR_INVALID_ARG otherwise, and where B times the
- *            16-token tiles of max_pages pages pass 2^31, or 2^36 / H_q).
+ *            16-token tiles of max_pages pages pass 2^31 - 2^16, or
+ *            2^36 / H_q).
  * seq_lens   [B] int32 device.  A negative length, or one over max_pages
  *            pages, is reported (LT_ERR_DEVICE_BAD_SEQLENS) and its rows of
  *            out and lse are left as they were.  A page outside the pool is

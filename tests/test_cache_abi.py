@@ -210,3 +210,17 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         lt.PagedKVCache(pool.double(), pool.double())
     with pytest.raises(ValueError):
         lt.PagedKVCache(pool, pool[:1])
+
+
+def test_limits_of_counts():
+    """Counts whose tiles or sequences would pass the kernels' 31-bit indices."""
+    lib = _b().lib
+    c = ctypes.byref(_cache())
+    assert lib.lt_kv_cache_read(c, FAKE, 4, 4, F2, (1 << 30) + 1, 64, F3, F4, None, 1) == 1
+
+    def decode(B, pages, Hq):
+        return lib.lt_paged_attn_decode(FAKE, c, F2, pages, pages, F3, B, Hq, 0.125, 0, F4, None,
+                                        None, 0, None, 1)
+    assert decode(65535, 32768, 2) == 1           # 2^31 - 2^15 tiles of 16 tokens and 65535 more
+    assert decode(65535, 17, 65534) == 1          # 2^20 tiles, 65534 heads: over 2^36
+    assert _b().lib.lt_status_string(7) != _b().lib.lt_status_string(5)

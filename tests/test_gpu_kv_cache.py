@@ -327,3 +327,30 @@ def test_refusals_on_the_device():
     shifted = L.PagedKVCache(odd[1:1 + 4096].view(2, 16, 2, 64), c.v)
     with pytest.raises(L.LtError):
         L.kv_cache_write(shifted, k, k, slots)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
+def test_strides_of_single_entries_do_not_matter(dtype):
+    """One head, one slot per page or one page: torch leaves such a dimension
+    any stride, and no address uses it."""
+    import causal_linear_attention_chunked_b200 as L
+    for pages, ps in ((5, 1), (1, 5)):
+        odd = (64 if pages > 1 else 3, 64 if ps > 1 else 7, 1, 1)
+        k = torch.zeros(5 * 64, device="cuda").to(dtype).as_strided((pages, ps, 1, 64), odd)
+        v = torch.zeros(5 * 64, device="cuda").to(dtype).as_strided((pages, ps, 1, 64), odd)
+        s = [torch.ones(pages, 1, ps, device="cuda") if dtype == E4M3 else None for _ in "kv"]
+        c = L.PagedKVCache(k, v, *s)
+        x = torch.full((5, 1, 64), 2.0, device="cuda").bfloat16()
+        x *= torch.arange(1, 6, device="cuda").view(5, 1, 1)
+        L.kv_cache_write(c, x, -x, torch.arange(5, dtype=torch.int32, device="cuda"))
+        table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+        cu = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+        kr, vr = L.kv_cache_read(c, table, cu, 5, dtype=torch.bfloat16)
+        # each row holds one value m: its scale is m / 448 and its codes 448 (or m
+        # itself), whose product rounds back to the bf16 value m
+        assert torch.equal(kr, x) and torch.equal(vr, -x)
+        out = L.paged_attn_decode(torch.zeros(1, 1, 64, device="cuda").bfloat16(), c, table,
+                                  torch.tensor([5], dtype=torch.int32, device="cuda"))
+        # equal weights: minus the mean of 2, 4, 6, 8, 10, within fp32 roundings
+        # of the five scales and the sum, far below half a step of bf16 at 6
+        assert torch.equal(out, torch.full_like(out, -6.0))
