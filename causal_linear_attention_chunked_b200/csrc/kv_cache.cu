@@ -12,13 +12,18 @@
 // multiplication with corrections (below) whose codes are the division's.
 // A row is spread over w/16 lanes (the maximum is a 2- or 3-step shuffle);
 // each lane moves two chunks of 8 elements, w/2 apart, so that both the 16-bit
-// and the 8-bit side are accessed in whole runs.  A block walks tiles of tokens;
-// it looks up a tile's slots (or the sequences they belong to) once, in shared
-// memory, for all heads, while the rows of the tile before are under way.
+// and the 8-bit side are accessed in whole runs.  Quantising, the warps of the
+// blocks that stay on the SMs step through the rows, a step's loads under way
+// while the step before is worked on, and look a row's slot up with its values
+// (a block per tile of tokens with the lookups in shared memory: 20% slower at
+// 16384 tokens of 8 heads of 64).  Copying and reading back, a block does one
+// tile of tokens, looks up its places once for all heads, and hides that
+// behind other blocks' rows.
 //
 // Measured on one B200 (plain copy 6.55 TB/s): 32768 bf16 tokens of 8 heads of
-// 128, keys and values, into e4m3 pages 41 us, 5.0 TB/s; 64 ragged sequences (266k
-// tokens of 8 heads of 64) back from e4m3 to bf16 134 us, 6.3 TB/s.
+// 128, keys and values, into e4m3 pages 38 us, 5.4 TB/s (16384 fp32 tokens 28 us,
+// 6.1 TB/s); 64 ragged sequences (266k tokens of 8 heads of 64) back from e4m3 to
+// bf16 134 us, 6.3 TB/s.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -34,6 +39,9 @@ namespace {
 
 constexpr int kT = 256;      // threads
 constexpr int kMaxTok = 64;  // tokens per tile, at most
+// quantising: blocks per SM for keys, and as many for values
+constexpr int kQuantBlocks = 2;
+
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 struct Pool {
@@ -59,6 +67,8 @@ struct CacheArgs {
   int max_pages;
   const int32_t* cu;
   int B, N;
+  uint32_t page_magic;  // quantising: floor(2^(31 + page_shift) / page_size) + 1
+  int page_shift;       // ceil(log2(page_size))
   int* err;
 };
 
@@ -190,10 +200,16 @@ __device__ __forceinline__ uint32_t top_bits(const Chunk<__half>& c) {
 // 16-bit inputs need one correction only: a code goes by two 8-bit (11-bit)
 // significands and the difference of their exponents, and over all of those
 // (22 differences; more give code 0) one correction gives the same codes (none
-// leaves 140 of 352320 bf16 cases different).
+// leaves 140 of 352320 bf16 cases different).  For them the reciprocal may be a
+// step off, which the correction's last factor does not notice.
 //
 // What is computed is minus the quotient, p = -(x v), p + (x + p b)(-v): so a
 // zero keeps its sign, which x - q b would lose.
+__device__ __forceinline__ float near_reciprocal(float b) {
+  float v;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(b));
+  return fmaf(v, fmaf(-b, v, 1.0f), v);  // a Newton step
+}
 template <int kCorrections>
 __device__ __forceinline__ F2 minus_quotient(F2 x, F2 b, F2 minus_v) {
   F2 p = mul2(x, minus_v);
@@ -202,7 +218,7 @@ __device__ __forceinline__ F2 minus_quotient(F2 x, F2 b, F2 minus_v) {
   return p;
 }
 // y[0..7] -> -(y / scale), with the row's scale from the bits of its largest
-// magnitude (NaN where that is not finite)
+// magnitude (where that is not finite: zeros, and NaN)
 template <typename T, typename KV>
 __device__ __forceinline__ float minus_quotients(F2* y, uint32_t top) {
   constexpr float kMax = KvMax<KV>::value;
@@ -212,11 +228,16 @@ __device__ __forceinline__ float minus_quotients(F2* y, uint32_t top) {
     float q = x * v;
     q = fmaf(fmaf(q, -kMax, x), v, q);
     q = fmaf(fmaf(q, -kMax, x), v, q);
-    const float r = -__frcp_rn(q);
+    const float r = -(sizeof(T) == 2 ? near_reciprocal(q) : __frcp_rn(q));
     const F2 b = pack_f2(q, q), n = pack_f2(r, r);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = minus_quotient<sizeof(T) == 2 ? 1 : 2>(y[e], b, n);
     return q;
+  }
+  if (top >= 0x7f800000u) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = pack_f2(-0.0f, -0.0f);
+    return __uint_as_float(0x7fc00000u);
   }
   const float b = fmaxf(__fdiv_rn(x, kMax), kTiny);
 #pragma unroll
@@ -224,7 +245,7 @@ __device__ __forceinline__ float minus_quotients(F2* y, uint32_t top) {
     const float2 z = unpack_f2(y[e]);
     y[e] = pack_f2(__fdiv_rn(z.x, -b), __fdiv_rn(z.y, -b));
   }
-  return top < 0x7f800000u ? b : __uint_as_float(0x7fc00000u);
+  return b;
 }
 
 // the codes of -y[0..3]
@@ -320,71 +341,16 @@ __device__ __forceinline__ void check_offsets(const CacheArgs& a) {
 }
 
 // ----------------------------------------------------------------- kernels
-// A block walks the tiles blockIdx.x, + gridDim.x, ... of `n` tokens: `look`
-// gives a token's place, `work` does a tile's rows (its first token, tokens and
-// places).
+// A block does one tile of tokens: `look` gives a token's place, `work` does the
+// tile's rows (its first token, tokens and places).
 template <typename Look, typename Work>
-__device__ __forceinline__ void walk_tiles(int64_t n, int tok, const Look& look,
-                                           const Work& work) {
-  __shared__ Place place[2][kMaxTok];
-  int64_t t0 = (int64_t)blockIdx.x * tok;
-  const int64_t step = (int64_t)gridDim.x * tok;
-  if (threadIdx.x < tok && t0 + threadIdx.x < n) place[0][threadIdx.x] = look(t0 + threadIdx.x);
+__device__ __forceinline__ void one_tile(int64_t n, int tok, const Look& look, const Work& work) {
+  __shared__ Place place[kMaxTok];
+  const int64_t t0 = (int64_t)blockIdx.x * tok;
+  const int nt = (int)min((int64_t)tok, n - t0);
+  if (threadIdx.x < nt) place[threadIdx.x] = look(t0 + threadIdx.x);
   __syncthreads();
-  for (int buf = 0; t0 < n; t0 += step, buf ^= 1) {
-    const int64_t t1 = t0 + step + threadIdx.x;
-    if (threadIdx.x < tok && t1 < n) place[buf ^ 1][threadIdx.x] = look(t1);
-    work(t0, (int)min((int64_t)tok, n - t0), place[buf]);
-    __syncthreads();
-  }
-}
-
-template <typename T, typename KV, int WIDTH>
-__device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool, const T* in,
-                                           int64_t stride, const Place* place, int nt, RowAt at) {
-  constexpr int kU = 2;  // rows in flight per thread
-  constexpr int L = WIDTH / 16, HALF = WIDTH / 2, RG = kT / L;  // lanes per row, rows at a time
-  const int j = threadIdx.x % L, n = nt * a.H;
-  in += j * 8;
-#pragma unroll 1
-  for (int r = threadIdx.x / L, rw = (threadIdx.x & ~31) / L; rw < n;
-       r += RG * kU, rw += RG * kU) {  // warps stay converged for the shuffles
-    Chunk<T> x[kU][2];
-    Place pl[kU];
-    int hd[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      // (past the last row: the tile's first again, and nothing stored)
-      const bool live = r + u * RG < n;
-      const int tt = live ? at.tt : 0;
-      hd[u] = live ? at.h : 0;
-      pl[u] = place[tt];
-      if (!live) pl[u].row = -1;
-      const T* p = in + tt * stride + hd[u] * WIDTH;
-      x[u][0] = load_chunk(p);
-      x[u][1] = load_chunk(p + HALF);
-      at.next();
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      uint32_t top = max(top_bits(x[u][0]), top_bits(x[u][1]));
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      F2 y[2][4];
-      widen8(x[u][0], y[0]);
-      widen8(x[u][1], y[1]);
-      const float scale = minus_quotients<T, KV>(y[0], top);
-      uint2 code[2] = {encode_minus(y[0], KV()), encode_minus(y[1], KV())};
-      if (top >= 0x7f800000u) code[0] = code[1] = make_uint2(0, 0);
-      if (pl[u].row >= 0) {
-        uint8_t* out =
-            static_cast<uint8_t*>(pool.p) + pl[u].row + hd[u] * pool.head + j * 8;
-        *reinterpret_cast<uint2*>(out) = code[0];
-        *reinterpret_cast<uint2*>(out + HALF) = code[1];
-        if (j == 0) pool.scale[pl[u].scale + (int64_t)hd[u] * a.page_size] = scale;
-      }
-    }
-  }
+  work(t0, nt, place);
 }
 
 template <typename T, typename KV, int WIDTH>
@@ -432,34 +398,83 @@ __device__ __forceinline__ void dequant_rows(const CacheArgs& a, const Pool& poo
   }
 }
 
-// blockIdx.y: 0 keys, 1 values
+// Quantising: a warp takes 32 / L rows at a time, every so many apart.  A step's
+// loads go out as soon as the step before has widened its own, and land while
+// its codes are worked out (two steps ahead: no faster, and fp32 rows then do
+// not fit the registers that four blocks per SM leave).
 template <typename T, typename KV, int WIDTH>
-__device__ __forceinline__ void quant_walk(const CacheArgs& a, const Pool& pool, int which) {
-  const T* in = static_cast<const T*>(a.in[which]);
+__device__ __forceinline__ void quant_rows(const CacheArgs& a, const Pool& pool, int which) {
+  constexpr int L = WIDTH / 16, HALF = WIDTH / 2, RW = 32 / L;  // lanes per row, rows per step
+  const int lane = threadIdx.x & 31, j = lane % L;
+  const int64_t warp = (int64_t)blockIdx.x * (kT / 32) + (threadIdx.x >> 5);
+  const int64_t rows = a.tokens * a.H, step = (int64_t)gridDim.x * (kT / 32) * RW;
+  if (warp * RW >= rows) return;
+  const int n = (int)((rows - warp * RW + step - 1) / step);  // the warp's steps
+  // token and head of this lane's next row to load
+  const int64_t r0 = warp * RW + lane / L;
+  uint32_t t = (uint32_t)(r0 / a.H), h = (uint32_t)(r0 - (int64_t)t * a.H);
+  const uint32_t dt = (uint32_t)(step / a.H), dh = (uint32_t)(step - (int64_t)dt * a.H);
+  const T* const in = static_cast<const T*>(a.in[which]) + j * 8;
   const int64_t stride = a.stride[which];
-  constexpr int L = WIDTH / 16;
-  const RowAt at(threadIdx.x / L, kT / L, a.H);
-  walk_tiles(
-      a.tokens, a.tok, [&](int64_t t) { return place_of_slot(a, pool, t); },
-      [&](int64_t t0, int nt, const Place* place) {
-        quant_rows<T, KV, WIDTH>(a, pool, in + t0 * stride, stride, place, nt, at);
-      });
+  Chunk<T> x[2];
+  int slot, head;
+  auto load = [&]() {
+    const bool live = t < (uint32_t)a.tokens;
+    const uint32_t tt = live ? t : 0;  // (past the last row: the first token's, not stored)
+    const T* p = in + tt * stride + h * WIDTH;
+    slot = live ? __ldg(a.slots + tt) : -1;
+    head = h;
+    x[0] = load_chunk(p);
+    x[1] = load_chunk(p + HALF);
+    t += dt;
+    h += dh;
+    if (h >= (uint32_t)a.H) {
+      h -= a.H;
+      ++t;
+    }
+  };
+  load();
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    uint32_t top = max(top_bits(x[0]), top_bits(x[1]));
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    F2 y[2][4];
+    widen8(x[0], y[0]);
+    widen8(x[1], y[1]);
+    const int s = slot, hd = head;
+    if (i + 1 < n) load();
+    const float scale = minus_quotients<T, KV>(y[0], top);
+    // s / page_size, exact for 0 <= s < 2^31
+    const int page = (int)(((uint64_t)(uint32_t)s * a.page_magic) >> (31 + a.page_shift));
+    if (s >= 0 && page < a.num_pages) {
+      const int at = s - page * a.page_size;
+      uint8_t* out = static_cast<uint8_t*>(pool.p) + page * pool.page + at * pool.slot +
+                     hd * pool.head + j * 8;
+      *reinterpret_cast<uint2*>(out) = encode_minus(y[0], KV());
+      *reinterpret_cast<uint2*>(out + HALF) = encode_minus(y[1], KV());
+      if (j == 0) pool.scale[((int64_t)page * a.H + hd) * a.page_size + at] = scale;
+    } else if (s != -1) {
+      report_error(a.err, kDevErrBadPage);
+    }
+  }
 }
+// blockIdx.y: 0 keys, 1 values
 template <typename T, typename KV>
 __global__ void __launch_bounds__(kT) lt_kv_quant_kernel(const CacheArgs a) {
   const Pool pool = a.pool[blockIdx.y];
   if (pool.w == 64)
-    quant_walk<T, KV, 64>(a, pool, blockIdx.y);
+    quant_rows<T, KV, 64>(a, pool, blockIdx.y);
   else
-    quant_walk<T, KV, 128>(a, pool, blockIdx.y);
+    quant_rows<T, KV, 128>(a, pool, blockIdx.y);
 }
 
 template <typename T, typename KV, int WIDTH>
-__device__ __forceinline__ void dequant_walk(const CacheArgs& a, const Pool& pool, int which) {
+__device__ __forceinline__ void dequant_tile(const CacheArgs& a, const Pool& pool, int which) {
   T* out = static_cast<T*>(a.out[which]);
   constexpr int L = WIDTH / 16;
   const RowAt at(threadIdx.x / L, kT / L, a.H);
-  walk_tiles(
+  one_tile(
       a.N, a.tok, [&](int64_t t) { return place_of_row(a, pool, (int)t); },
       [&](int64_t t0, int nt, const Place* place) {
         dequant_rows<T, KV, WIDTH>(a, pool, out + t0 * a.H * WIDTH, place, nt, at);
@@ -470,9 +485,9 @@ __global__ void __launch_bounds__(kT) lt_kv_dequant_kernel(const CacheArgs a) {
   const Pool pool = a.pool[blockIdx.y];
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(a);
   if (pool.w == 64)
-    dequant_walk<T, KV, 64>(a, pool, blockIdx.y);
+    dequant_tile<T, KV, 64>(a, pool, blockIdx.y);
   else
-    dequant_walk<T, KV, 128>(a, pool, blockIdx.y);
+    dequant_tile<T, KV, 128>(a, pool, blockIdx.y);
 }
 
 // Rows as they are, in 16-byte pieces: into the cache, or out of it.  Strides
@@ -487,7 +502,7 @@ __global__ void __launch_bounds__(kT) lt_kv_copy_kernel(const CacheArgs a) {
   const int grp = threadIdx.x / L, j = threadIdx.x % L;
   const int64_t stride = a.stride[which];
   const RowAt first(grp, RG, a.H);
-  walk_tiles(
+  one_tile(
       kWrite ? a.tokens : (int64_t)a.N, a.tok,
       [&](int64_t t) { return kWrite ? place_of_slot(a, pool, t) : place_of_row(a, pool, (int)t); },
       [&](int64_t t0, int nt, const Place* place) {
@@ -535,25 +550,25 @@ cudaError_t launch_quant(const CacheArgs& a, bool e4m3, bool write, dim3 grid, c
 // Tokens per tile: enough rows for every group of a block's threads and to
 // share the lookup of their places, few enough that a decode step's tokens
 // spread over the device.
-int tile_tokens(int64_t tokens, int heads, int lanes, int most, int sms) {
+int tile_tokens(int64_t tokens, int heads, int lanes, int sms) {
   const int least = (kT / lanes + heads - 1) / heads;
   const int64_t n = tokens / (4 * sms);
-  return n < least ? (least < most ? least : most) : n > most ? most : (int)n;
+  return n < least ? (least < kMaxTok ? least : kMaxTok) : n > kMaxTok ? kMaxTok : (int)n;
 }
 
 cudaError_t launch(CacheArgs a, lt_dtype_t t, lt_kv_dtype_t kv, bool write, int sms,
                    cudaStream_t s) {
   const int64_t n = write ? a.tokens : a.N;
   const int row = (a.pool[0].w > a.pool[1].w ? a.pool[0].w : a.pool[1].w) * (int)kv_size(kv);
-  // Quantising, a block's set-up costs as much as two of its tiles: four blocks
-  // stay on each SM (two for keys, two for values) and walk (32768 tokens of 8
-  // heads of 128: 47 us; a block per tile 55 of 55 tokens, 80 of 13).  The
-  // others hide a tile's lookup behind other blocks' rows instead (64 ragged
-  // sequences read back: 134 us; walking 176).
-  const bool walk = eight_bit(kv) && write;
-  a.tok = tile_tokens(n, a.H, row / 16, walk ? 32 : kMaxTok, sms);
-  const int64_t tiles = (n + a.tok - 1) / a.tok;
-  const dim3 grid((unsigned)(walk && tiles > 2 * sms ? 2 * sms : tiles), 2);
+  a.tok = tile_tokens(n, a.H, row / 16, sms);
+  dim3 grid((unsigned)((n + a.tok - 1) / a.tok), 2);
+  if (eight_bit(kv) && write) {
+    while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
+    a.page_magic = (uint32_t)(((uint64_t)1 << (31 + a.page_shift)) / a.page_size + 1);
+    // as many blocks as stay on the SMs, fewer where they would have no row
+    const int64_t rows = n * a.H, per = kT / (row / 16), most = kQuantBlocks * sms;
+    grid.x = (unsigned)(rows > per * most ? most : (rows + per - 1) / per);
+  }
   if (eight_bit(kv)) {
     const bool e4m3 = kv == LT_KV_E4M3;
     return t == LT_BF16  ? launch_quant<__nv_bfloat16>(a, e4m3, write, grid, s)

@@ -96,7 +96,8 @@ def _given(t, shape, dtype, name):
 def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
     n, Hq, d, q_step = _tokens(q, "q")
     nk, Hkv, dk, k_step = _tokens(k, "k")
-    if nk != n or dk != d or q.shape[:-2] != k.shape[:-2]:
+    dims = q.dim()
+    if nk != n or dk != d or k.dim() != dims or (dims == 4 and q.shape[0] != k.shape[0]):
         raise ValueError("q and k must have the same tokens and width")
     dtype = q.dtype
     if k.dtype != dtype:
@@ -107,7 +108,7 @@ def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
         if w is not None:
             if w_dtype is None:
                 w_dtype = w.dtype
-            if w.shape != (d,) or not w.is_contiguous() or w.dtype != w_dtype or \
+            if w.dim() != 1 or w.numel() != d or not w.is_contiguous() or w.dtype != w_dtype or \
                     w_dtype not in (dtype, torch.float32):
                 raise ValueError("weights must be contiguous [d] tensors, both float32 or both "
                                  "of q's dtype")
@@ -121,7 +122,7 @@ def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise TypeError("inv_freq must be a contiguous float32 vector")
         n_pos, rot = positions.numel(), 2 * inv_freq.numel()
-        if rot and n_pos != n and (q.dim() != 4 or n_pos != q.shape[1]):
+        if rot and n_pos != n and (dims != 4 or n_pos != q.shape[1]):
             raise ValueError("positions must be one per token, or [N] for a [B, N] batch")
     return n, Hq, Hkv, d, q_step, k_step, code, w_code, n_pos, rot
 
