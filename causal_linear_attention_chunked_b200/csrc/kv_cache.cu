@@ -547,20 +547,25 @@ cudaError_t launch_quant(const CacheArgs& a, bool e4m3, bool write, dim3 grid, c
   return cudaGetLastError();
 }
 
-// Tokens per tile: enough rows for every group of a block's threads and to
-// share the lookup of their places, few enough that a decode step's tokens
-// spread over the device.
-int tile_tokens(int64_t tokens, int heads, int lanes, int sms) {
-  const int least = (kT / lanes + heads - 1) / heads;
+// Tokens per tile, at most kMaxTok: enough rows for every group of a block's
+// threads (at most 64: a row has four lanes or more), few enough that a batch
+// spreads over the device, and kTileBytes of the dense side at most (token: its
+// bytes there).  32 KB: 49k bf16 tokens of 8 heads of 128 read back in 64.7 us, 266k
+// of 64 from e4m3 in 143; 16 KB 67.4 and 162, 64 KB 66.0 and 146.
+constexpr int kTileBytes = 32768;
+int tile_tokens(int64_t tokens, int heads, int lanes, int64_t token, int sms) {
+  const int64_t least = (kT / lanes + heads - 1) / heads, fit = kTileBytes / token;
+  const int64_t most = fit < least ? least : fit > kMaxTok ? kMaxTok : fit;
   const int64_t n = tokens / (4 * sms);
-  return n < least ? (least < kMaxTok ? least : kMaxTok) : n > kMaxTok ? kMaxTok : (int)n;
+  return (int)(n < least ? least : n > most ? most : n);
 }
 
 cudaError_t launch(CacheArgs a, lt_dtype_t t, lt_kv_dtype_t kv, bool write, int sms,
                    cudaStream_t s) {
   const int64_t n = write ? a.tokens : a.N;
   const int row = (a.pool[0].w > a.pool[1].w ? a.pool[0].w : a.pool[1].w) * (int)kv_size(kv);
-  a.tok = tile_tokens(n, a.H, row / 16, sms);
+  const int64_t token = (int64_t)a.H * (row / (int)kv_size(kv)) * (int64_t)dtype_size(t);
+  a.tok = tile_tokens(n, a.H, row / 16, token, sms);
   dim3 grid((unsigned)((n + a.tok - 1) / a.tok), 2);
   if (eight_bit(kv) && write) {
     while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
