@@ -354,3 +354,61 @@ def test_strides_of_single_entries_do_not_matter(dtype):
         # equal weights: minus the mean of 2, 4, 6, 8, 10, within fp32 roundings
         # of the five scales and the sum, far below half a step of bf16 at 6
         assert torch.equal(out, torch.full_like(out, -6.0))
+
+
+@pytest.mark.parametrize("src,kv,T,H,d,dv", [
+    (torch.bfloat16, E4M3, 9001, 3, 128, 64), (torch.float16, I8, 9001, 5, 64, 128),
+    (torch.float32, E4M3, 7001, 7, 128, 128), (torch.bfloat16, I8, 331, 64, 64, 64)])
+def test_write_of_more_rows_than_the_device_takes_at_once(src, kv, T, H, d, dv):
+    """Every warp steps through several rows, whose heads and tokens wrap; some
+    tokens are skipped."""
+    import causal_linear_attention_chunked_b200 as L
+    g = torch.Generator().manual_seed(T + H)
+    ps = 24
+    pages = -(-T // ps) + 1
+    c = _cache(pages, ps, H, d, dv, kv)
+    k, v = (torch.randn(T, H, w, generator=g).to(src) for w in (d, dv))
+    slots = torch.randperm(pages * ps, generator=g)[:T].int()
+    slots[::7] = -1
+    want = [torch.zeros(0)] * 4
+    for i, (pool, scale, x) in enumerate(((c.k, c.k_scale, k), (c.v, c.v_scale, v))):
+        rows, sc = _raw(pool.cpu()).flatten(0, 1).clone(), scale.cpu().transpose(1, 2).flatten(0, 1)
+        codes, s = plain.quantise(x, kv)
+        live = slots >= 0
+        rows[slots[live].long()] = _raw(codes)[live]
+        sc = sc.clone()
+        sc[slots[live].long()] = s[live]
+        want[2 * i], want[2 * i + 1] = rows, sc
+    L.kv_cache_write(c, k.cuda(), v.cuda(), slots.cuda())
+    assert L.get_last_device_error() == 0
+    for i, (pool, scale) in enumerate(((c.k, c.k_scale), (c.v, c.v_scale))):
+        assert torch.equal(_raw(pool.cpu()).flatten(0, 1), want[2 * i])
+        assert torch.equal(scale.cpu().transpose(1, 2).flatten(0, 1), want[2 * i + 1])
+
+
+def test_8_bit_offsets_past_32_bits():
+    """8-bit pools of more than 2^32 bytes: rows written to, read from and
+    attended at their end, as in a small cache."""
+    import causal_linear_attention_chunked_b200 as L
+    ps, H, d, T = 256, 8, 128, 300
+    pages = 2 ** 32 // (ps * H * d) + 4
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn(T, H, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(1, 16, d, generator=g, device="cuda").bfloat16()
+    cu = torch.tensor([0, T], dtype=torch.int32).cuda()
+    got = []
+    for n in (pages, 2):
+        c = L.PagedKVCache.empty(n, ps, H, d, dtype=I8)
+        table = torch.tensor([[n - 1, n - 2]], dtype=torch.int32).cuda()
+        at = torch.arange(T, device="cuda")
+        L.kv_cache_write(c, k, v, ((n - 1 - at // ps) * ps + at % ps).int())
+        got.append(L.kv_cache_read(c, table, cu, T) +
+                   (L.paged_attn_decode(q, c, table, cu[1:]),))
+        del c
+    assert L.get_last_device_error() == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    # int8: half a step of 1/127 of the row's maximum, bf16's rounding of the
+    # product, and the fp32 roundings of scale, quotient and product
+    tol = k.float().abs().amax(-1, keepdim=True) * (0.5 / 127 + 2.0 ** -8 + 2.0 ** -21)
+    assert bool(((got[0][0].float() - k.float()).abs() <= tol).all())
