@@ -248,3 +248,28 @@ def test_refusals_on_the_device():
         L.qk_norm_rope(q, q, q_out=torch.zeros(4, 2, 63, device="cuda"))
     with pytest.raises(L.LtError):
         L.qk_norm_rope(q, q, eps=0.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [
+    (5003, 3, 2, 64, 64, False), (7200, 1, 1, 128, 96, True), (4801, 9, 1, 128, 128, False)])
+def test_more_tokens_than_the_device_has_warps(dtype, shape):
+    """Warps that go on to further tokens: their rings wrap, and their angles
+    change with the token."""
+    import causal_linear_attention_chunked_b200 as L
+    T, Hq, Hkv, d, rot, il = shape
+    q, k, wq, wk, g = _case(T, Hq, Hkv, d, dtype, 9)
+    gq = torch.randn(T, Hq, d, generator=g).to(dtype)
+    gk = torch.randn(T, Hkv, d, generator=g).to(dtype)
+    pos = torch.randint(0, 100000, (T,), generator=g).int()
+    freq = _freq(rot)
+    dev = [t.cuda() for t in (gq, gk, q, k, wq, wk, pos, freq)]
+    _check_fwd([y.cpu() for y in L.qk_norm_rope(*dev[2:], eps=1e-5, interleaved=il)], q, k, wq, wk,
+               pos, freq, 1e-5, il)
+    got = L.qk_norm_rope_bwd(*dev, eps=1e-5, interleaved=il)
+    again = L.qk_norm_rope_bwd(*dev, eps=1e-5, interleaved=il)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    for i, (x, w, gr) in enumerate(((q, wq, gq), (k, wk, gk))):
+        (dx, dxb), (dw, dwb) = plain.norm_rope_bwd(gr, x, w, pos, freq, 1e-5, il)
+        plain.check(got[i], dx, dxb, dtype, "dx %d" % i)
+        plain.check(got[2 + i], dw, dwb, dtype, "dw %d" % i)
