@@ -21,8 +21,9 @@
 // run two at a time (f32x2).
 //
 // Measured on one B200 (plain copy 6.55 TB/s), 32 + 8 bf16 heads of 128: 32768
-// tokens forward 115 us, 5.8 TB/s; 16384 tokens backward 94 us, 5.4 TB/s, with
-// the issue slots 64% busy.
+// tokens forward 107 us, 6.3 TB/s; 16384 tokens backward 88 us, 5.7 TB/s (replayed
+// from a graph; 118 and 98 in seconds of back-to-back calls, whose power lowers the
+// clock: the issue slots are 64% busy).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -113,14 +114,14 @@ __device__ __forceinline__ void sincos_turn(float t, float* s, float* c) {
 // the token's angles: the rows of a warp's step compute a share each and
 // exchange them
 template <typename T, int D, bool IL>
-__device__ __forceinline__ void angles_of(const NormArgs& a, const Lane<D>& ln, int64_t t,
+__device__ __forceinline__ void angles_of(const NormArgs& a, const Lane<D>& ln, uint32_t t,
                                           Angles<IL>& out) {
   constexpr int L = Lane<D>::L, RW = Lane<D>::RW, SH = 4 / RW;  // a lane's share
   constexpr double kInvTwoPi = 0.15915494309189533577;
   float c[4], s[4];
   float mc[SH], ms[SH];
   if (ln.rotated) {
-    const int pos = __ldg(a.positions + (a.n_pos == a.tokens ? t : t % a.n_pos));
+    const int pos = __ldg(a.positions + (a.n_pos == a.tokens ? t : t % (uint32_t)a.n_pos));
 #pragma unroll
     for (int e = 0; e < SH; ++e) {
       const int i = ln.grp * SH + e;  // which of the lane's four
@@ -218,14 +219,13 @@ constexpr uint64_t kWaitNs = 1000000000ull;  // a wait gives up after 1 s
 // A warp's batches in order: units (token, part) unit, + step, ..., and of each
 // the token's batches part, + parts, ... (the queries' first, then the keys').
 struct Walk {
-  int64_t unit, t;
-  int part, b;
+  uint32_t unit, t;
+  int b;
   __device__ __forceinline__ void place(const NormArgs& a) {
-    t = a.parts == 1 ? unit : unit / a.parts;
-    part = (int)(unit - t * a.parts);
-    b = part;
+    t = a.parts == 1 ? unit : unit / (uint32_t)a.parts;
+    b = (int)(unit - t * (uint32_t)a.parts);
   }
-  __device__ __forceinline__ void next(const NormArgs& a, int nb, int64_t step) {
+  __device__ __forceinline__ void next(const NormArgs& a, int nb, uint32_t step) {
     b += a.parts;
     if (b >= nb) {
       unit += step;
@@ -272,9 +272,9 @@ __global__ void __launch_bounds__(kT, kBlocks) lt_norm_rope_kernel(const NormArg
 
   const LN ln(a.rot);
   const int nbq = (a.H[0] + STEP - 1) / STEP, nb = nbq + (a.H[1] + STEP - 1) / STEP;
-  const int64_t units = a.tokens * a.parts, step = (int64_t)gridDim.x * kW;
+  const uint32_t units = (uint32_t)a.tokens * a.parts, step = gridDim.x * kW;
   Walk use, load;
-  use.unit = (int64_t)warp * gridDim.x + blockIdx.x;
+  use.unit = warp * gridDim.x + blockIdx.x;
   use.place(a);
   load = use;
 
@@ -289,12 +289,12 @@ __global__ void __launch_bounds__(kT, kBlocks) lt_norm_rope_kernel(const NormArg
       mbar_arrive_expect_tx(&full[lstage], kBack ? 2 * bytes : bytes);
       bulk_load(dst,
                 static_cast<const T*>(bt.ph ? a.x[1] : a.x[0]) +
-                    load.t * (bt.ph ? a.stride[1] : a.stride[0]) + bt.h0 * D,
+                    (int64_t)load.t * (bt.ph ? a.stride[1] : a.stride[0]) + bt.h0 * D,
                 bytes, &full[lstage]);
       if (kBack)
         bulk_load(dst + R::kBatch,
                   static_cast<const T*>(bt.ph ? a.g[1] : a.g[0]) +
-                      (load.t * (bt.ph ? a.H[1] : a.H[0]) + bt.h0) * D,
+                      ((int64_t)load.t * (bt.ph ? a.H[1] : a.H[0]) + bt.h0) * D,
                   bytes, &full[lstage]);
     }
     ++issued;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kT, kBlocks) lt_norm_rope_kernel(const NormArg
   for (int e = 0; e < 4; ++e) dw[0][e] = dw[1][e] = F2{0};
 
   Angles<IL> ang;
-  int64_t have = -1;  // the token whose angles `ang` holds
+  uint32_t have = ~0u;  // the token whose angles `ang` holds
   int done = 0, stage = 0, parity = 0;
 #pragma unroll 1
   for (; use.unit < units; ++done) {
@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(kT, kBlocks) lt_norm_rope_kernel(const NormArg
     if (lane == 0) {
       const int64_t os = kBack ? (bt.ph ? a.ostride[1] : a.ostride[0])
                                : (int64_t)(bt.ph ? a.H[1] : a.H[0]) * D;
-      bulk_store(static_cast<T*>(bt.ph ? a.out[1] : a.out[0]) + use.t * os + bt.h0 * D, batch,
-                 (uint32_t)(bt.n * D * sizeof(T)));
+      bulk_store(static_cast<T*>(bt.ph ? a.out[1] : a.out[0]) + (int64_t)use.t * os + bt.h0 * D,
+                 batch, (uint32_t)(bt.n * D * sizeof(T)));
       bulk_commit_group();
       bulk_wait_read_but_last();  // the batch before this one has left its stage
     }
@@ -540,7 +540,7 @@ lt_status_t check(const void* q, const void* k, const void* qw, const void* kw,
   if (rot > 0 && (!positions || !inv_freq || n_pos < 1 || tokens % n_pos != 0))
     return LT_ERR_INVALID_ARG;
   const size_t es = dtype_size(dtype);
-  if (tokens > ((int64_t)1 << 40) || !stride_ok(tokens, q_stride, H_q, d, es) ||
+  if (tokens > 0x7fffffff || !stride_ok(tokens, q_stride, H_q, d, es) ||
       !stride_ok(tokens, k_stride, H_kv, d, es))
     return LT_ERR_INVALID_ARG;
   if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(qw, 16) || !aligned_to(kw, 16) ||

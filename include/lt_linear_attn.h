@@ -404,8 +404,8 @@ LT_API lt_status_t lt_linear_attn_decode_step(const void *q, const void *k, cons
  * interleaved  0 or 1, the pairing.
  * q_out, k_out  [tokens][H][d] dense, dtype, 16-byte aligned; written whole;
  *            must not overlap any input or each other.
- * tokens     >= 1, H_q, H_kv >= 1 (any two counts), d 64 or 128; a tensor's
- *            extent below 2^62 bytes.
+ * tokens     1 <= tokens < 2^31, H_q, H_kv >= 1 (any two counts), d 64 or 128;
+ *            a tensor's extent below 2^62 bytes.
  * eps        finite and > 0.
  * dtype      LT_BF16, LT_F16 or LT_F32; arithmetic in fp32, one rounding at
  *            the end.  The sum of squares is held in fp32: |x| above about
