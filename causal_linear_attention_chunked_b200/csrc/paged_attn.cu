@@ -99,7 +99,9 @@ int heads_per_unit(lt_dtype_t t, int G) {
   const int most = t == LT_F32 ? 8 : 16;
   return G < most ? G : most;
 }
-int block_warps(lt_kv_dtype_t kv) { return kv == LT_KV_F32 ? 4 : 8; }
+int block_warps(lt_dtype_t t, lt_kv_dtype_t kv, int d, int dv) {
+  return kv == LT_KV_F32 ? 4 : (d + dv) * (int)kv_size(kv) <= 128 && t != LT_F32 ? 16 : 8;
+}
 int tile_tokens(lt_kv_dtype_t kv, int d, int dv) {
   return (d + dv) * (int)kv_size(kv) <= 256 ? 32 : 16;
 }
@@ -111,10 +113,10 @@ struct Sizes {
   size_t floats;       // of a piece
   size_t bytes;
 };
-Sizes sizes_of(lt_dtype_t t, lt_kv_dtype_t kv, int H_q, int H_kv, int dv, int sms) {
+Sizes sizes_of(lt_dtype_t t, lt_kv_dtype_t kv, int H_q, int H_kv, int d, int dv, int sms) {
   const int G = H_q / H_kv, hb = heads_per_unit(t, G), nhb = (G + hb - 1) / hb;
   Sizes z;
-  z.warp = (size_t)sms * block_warps(kv) * 2;
+  z.warp = (size_t)sms * block_warps(t, kv, d, dv) * 2;
   z.block = (size_t)sms * 2 * H_kv * nhb;
   z.floats = (size_t)hb * (dv + 2);
   z.bytes = (z.warp + z.block) * z.floats * sizeof(float) + (size_t)sms * sizeof(Shared);
@@ -138,7 +140,7 @@ extern "C" lt_status_t lt_paged_attn_decode_plan(int H_q, int H_kv, int d, int d
     return LT_ERR_INVALID_ARG;
   if (num_sms <= 0) num_sms = device_sm_count();
   if (num_sms <= 0) return LT_ERR_CUDA;
-  *workspace_bytes = sizes_of(dtype, kv_dtype, H_q, H_kv, dv, num_sms).bytes;
+  *workspace_bytes = sizes_of(dtype, kv_dtype, H_q, H_kv, d, dv, num_sms).bytes;
   return LT_OK;
 }
 
@@ -194,7 +196,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.G = H_q / cache->H_kv;
   a.hb = heads_per_unit(dtype, a.G);
   a.nhb = (a.G + a.hb - 1) / a.hb;
-  const Sizes z = sizes_of(dtype, cache->dtype, H_q, cache->H_kv, cache->dv, sms);
+  const Sizes z = sizes_of(dtype, cache->dtype, H_q, cache->H_kv, cache->d, cache->dv, sms);
   Workspace w;
   const lt_status_t sw = w.take(dev, workspace, workspace_bytes, z.bytes, (cudaStream_t)stream);
   if (sw != LT_OK) return sw;
@@ -222,7 +224,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.max_len = most;
   a.units = a.Hkv * a.nhb;
   a.k_shift = -1;
-  for (int s = 0, w = block_warps(cache->dtype); (1 << s) <= w; ++s)
+  for (int s = 0, w = block_warps(dtype, cache->dtype, cache->d, cache->dv); (1 << s) <= w; ++s)
     if (a.units << s == w) a.k_shift = s;
   while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
   a.page_magic = (uint32_t)(((uint64_t)1 << (31 + a.page_shift)) / a.page_size + 1);

@@ -376,7 +376,11 @@ struct MmaEngine {
   static_assert(!kWide || kQuant, "fp32 caches have an engine of their own");
   // 8 KB per tile: short rows share a tile's bookkeeping (e4m3 rows of 128 in
   // tiles of 16, with 16 warps, issued a third more instructions per token)
-  static constexpr int kD = D, kHeads = 8 * kNB, kWarps = 8;
+  static constexpr int kD = D, kHeads = 8 * kNB;
+  // 8-bit rows of 64: tiles are 4 KB, and a warp's chain of steps per tile is no
+  // shorter, so twice the warps (64 sequences, 175k tokens of 8 heads, e4m3: 83 -> 68
+  // us; fp32 queries, whose products need the registers, 5% slower so)
+  static constexpr int kWarps = (D + DV) * Kv::kBytes <= 128 && !kWide ? 16 : 8;
   static constexpr int kTile = (D + DV) * Kv::kBytes <= 256 ? 32 : 16;
   static constexpr int kHalves = kTile / 16;
   static constexpr int kKRow = D * Kv::kBytes, kVRow = DV * Kv::kBytes;  // bytes

@@ -224,3 +224,12 @@ def test_limits_of_counts():
     assert decode(65535, 32768, 2) == 1           # 2^31 - 2^15 tiles of 16 tokens and 65535 more
     assert decode(65535, 17, 65534) == 1          # 2^20 tiles, 65534 heads: over 2^36
     assert _b().lib.lt_status_string(7) != _b().lib.lt_status_string(5)
+
+
+def test_plan_of_narrow_8_bit_rows():
+    """Rows of 64 + 64 bytes: sixteen warps per block, eight under fp32 queries."""
+    lib, n = _b().lib, ctypes.c_size_t()
+    assert lib.lt_paged_attn_decode_plan(8, 8, 64, 64, 1, 3, 148, ctypes.byref(n)) == 0
+    assert n.value == 148 * ((16 + 8) * 2 * 1 * (64 + 2) * 4 + 16)
+    assert lib.lt_paged_attn_decode_plan(8, 8, 64, 64, 0, 3, 148, ctypes.byref(n)) == 0
+    assert n.value == 148 * ((8 + 8) * 2 * 1 * (64 + 2) * 4 + 16)

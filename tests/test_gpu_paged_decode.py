@@ -359,3 +359,17 @@ def test_a_serving_run(kv):
         else:
             codes, sc = plain.quantise(K, kv)
             assert torch.equal(got, codes.double() * sc.double()[..., None])
+
+
+@pytest.mark.parametrize("qt,kv", [(BF, E4M3), (HF, I8), (F32, E4M3)])
+@pytest.mark.parametrize("lens,ps,Hq,Hkv", [
+    ([20000, 3, 0, 4097], 64, 4, 1), ([9, 40, 0, 17] * 100, 16, 8, 4), ([5000, 33, 700], 24, 9, 3),
+    ([3000] * 5, 64, 17, 17)])
+def test_long_and_ragged_8_bit_rows_of_64(qt, kv, lens, ps, Hq, Hkv):
+    """The narrow 8-bit rows, which more warps per block share."""
+    import causal_linear_attention_chunked_b200 as L
+    c, q, table, n = _setup(lens, ps, Hq, Hkv, 64, 64, qt, kv, 8)
+    got, lse = L.paged_attn_decode(q.cuda(), c, table.cuda(), n.cuda(), return_lse=True)
+    assert L.get_last_device_error() == 0
+    _check(got, lse, _ref(c, q, table, n), qt)
+    assert torch.equal(L.paged_attn_decode(q.cuda(), c, table.cuda(), n.cuda()), got)
