@@ -527,32 +527,45 @@ struct MmaEngine {
       for (int e = 0; e < 4; ++e) s[b][e] = (s[b][e] + s2[b][e]) * sl2[b][e & 1];
   }
 
-  // O^T += V^T P^T of 16 tokens, their weights' tiles hi (and lo)
-  __device__ __forceinline__ void values(uint32_t at, const uint32_t (*hi)[2],
-                                         const uint32_t (*lo)[2]) {
+  // O^T += V^T P^T of the tile, w its weights' tiles.  The sum of a tile starts
+  // from zero, its small terms first, and is added to the rest by plain
+  // additions: the instruction's own cut what they lose, all to one side
+  // (means of 16384 keys in one chain of products: off by 1e-4).
+  using Weights = uint32_t[kHalves][kSplit ? 2 : 1][kNB][2];
+  __device__ __forceinline__ void values(uint32_t at, const Weights& w) {
 #pragma unroll
     for (int j = 0; j < DV / 16; j += 2) {
-      uint32_t a0[4], a1[4];
-      if constexpr (!kQuant) {
-        ldsm4t(a0, chunk_on(at, 2 * j));
-        ldsm4t(a1, chunk_on(at, 2 * j + 2));
-      } else {
-        uint32_t w[4];
-        ldsm4t(w, chunk_on(at, j));
-        widen4<true>(w[0], a0[0], a0[1], KT());
-        widen4<true>(w[1], a0[2], a0[3], KT());
-        widen4<true>(w[2], a1[0], a1[1], KT());
-        widen4<true>(w[3], a1[2], a1[3], KT());
+      float sum[2][kNB][4] = {};
+#pragma unroll
+      for (int y = 0; y < kHalves; ++y) {
+        const uint32_t row = at + y * 16 * kVRow;
+        uint32_t a0[4], a1[4];
+        if constexpr (!kQuant) {
+          ldsm4t(a0, chunk_on(row, 2 * j));
+          ldsm4t(a1, chunk_on(row, 2 * j + 2));
+        } else {
+          uint32_t x[4];
+          ldsm4t(x, chunk_on(row, j));
+          widen4<true>(x[0], a0[0], a0[1], KT());
+          widen4<true>(x[1], a0[2], a0[3], KT());
+          widen4<true>(x[2], a1[0], a1[1], KT());
+          widen4<true>(x[3], a1[2], a1[3], KT());
+        }
+#pragma unroll
+        for (int n = kSplit ? 1 : 0; n >= 0; --n)
+#pragma unroll
+          for (int b = 0; b < kNB; ++b) {
+            mma<MT>(sum[0][b], a0, w[y][n][b][0], w[y][n][b][1]);
+            mma<MT>(sum[1][b], a1, w[y][n][b][0], w[y][n][b][1]);
+          }
       }
 #pragma unroll
-      for (int b = 0; b < kNB; ++b) {
-        mma<MT>(o[b][j], a0, hi[b][0], hi[b][1]);
-        mma<MT>(o[b][j + 1], a1, hi[b][0], hi[b][1]);
-        if constexpr (kSplit) {
-          mma<MT>(o[b][j], a0, lo[b][0], lo[b][1]);
-          mma<MT>(o[b][j + 1], a1, lo[b][0], lo[b][1]);
+      for (int b = 0; b < kNB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[b][j][e] += sum[0][b][e];
+          o[b][j + 1][e] += sum[1][b][e];
         }
-      }
     }
   }
 
@@ -612,7 +625,7 @@ struct MmaEngine {
       }
     if (__any_sync(0xffffffffu, moved)) rescale(s, top);
     const float inv_a = __uint_as_float(0x7f000000u - vtop);
-    uint32_t hi[kHalves][kNB][2], lo[kHalves][kNB][2];
+    Weights w;
 #pragma unroll
     for (int b = 0; b < kNB; ++b) {
       const float base[2] = {(m[b][0] == -INFINITY ? 0.0f : m[b][0]) - kShift,
@@ -630,16 +643,15 @@ struct MmaEngine {
             p0 *= f;
             p1 *= f;
           }
-          const uint32_t w = pack2<MT>(p0, p1);
-          hi[y][b][u] = transpose8(w);
+          const uint32_t hi = pack2<MT>(p0, p1);
+          w[y][0][b][u] = transpose8(hi);
           if constexpr (kSplit) {
-            const float2 x = unpack2<MT>(w);
-            lo[y][b][u] = transpose8(pack2<MT>(p0 - x.x, p1 - x.y));
+            const float2 x = unpack2<MT>(hi);
+            w[y][1][b][u] = transpose8(pack2<MT>(p0 - x.x, p1 - x.y));
           }
         }
     }
-#pragma unroll
-    for (int y = 0; y < kHalves; ++y) values(v_at + y * 16 * kVRow, hi[y], lo[y]);
+    values(v_at, w);
   }
 
   __device__ __forceinline__ void finish(const Sink<QT>& out) {

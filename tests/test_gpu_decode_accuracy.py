@@ -1,0 +1,103 @@
+"""Attention of one new token over the paged cache: what its arithmetic must
+hold in 32 bits, seen through inputs whose results are known exactly."""
+import pytest
+import torch
+
+from cache_plain import half_step, smallest
+from test_gpu_paged_decode import E4M3, F32, I8, TYPES
+
+pytestmark = pytest.mark.gpu
+
+
+def _decode(q, K, V, ks, vs, lens, ps, kv, table=None, **kw):
+    """(out, lse) of sequences that lie one after another in a cache of pages of
+    ps tokens, each from a page of its own on (or by `table`).  K, V [tokens, H,
+    w]: values of the cache's type (codes for 8 bits), ks, vs [tokens, H]."""
+    import causal_linear_attention_chunked_b200 as L
+    if table is None:
+        need = [max(1, -(-n // ps)) for n in lens]
+        table = torch.zeros(len(lens), max(need), dtype=torch.int32)
+        at = 0
+        for b, n in enumerate(need):
+            table[b, :n] = torch.arange(at, at + n)
+            at += n
+    pools = [x.to(kv).view(-1, ps, *x.shape[1:]) for x in (K, V)]
+    scales = [None, None]
+    if kv in (E4M3, I8):
+        scales = [s.float().view(-1, ps, s.shape[1]).transpose(1, 2).contiguous() for s in (ks, vs)]
+    c = L.PagedKVCache(*pools, *scales)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = L.paged_attn_decode(q, c, table.cuda(), n, return_lse=True, **kw)
+    assert L.get_last_device_error() == 0
+    return got
+
+
+LONG = [
+    # lengths, page size, query heads, KV heads, d, dv
+    ([20000, 3, 1, 4097], 64, 4, 1, 128, 128), ([19999], 24, 8, 8, 64, 64),
+    ([9, 40, 1, 17] * 100, 16, 8, 4, 64, 64), ([5000, 33, 700], 48, 24, 2, 64, 128),
+    ([3000] * 5, 128, 17, 17, 128, 64), ([2500, 31], 16, 40, 1, 64, 64)]
+
+
+@pytest.mark.parametrize("qt,kv", TYPES)
+@pytest.mark.parametrize("lens,ps,Hq,H,d,dv", LONG)
+def test_every_key_counts_once(qt, kv, lens, ps, Hq, H, d, dv):
+    """Queries of zeros weigh every key alike: the log sum is log n (a lost or
+    repeated key moves it by 1 / n, 5e-5 at most here), and columns of V that mark
+    every so-manieth token, or single ones at the edges of tiles, pages and the
+    sequence, come back as their share.  Weights and marks are powers of two and
+    their sums whole numbers, so what rounds is the quotient (2 steps) and the
+    logarithm (4 of its size in base 2)."""
+    need = [max(1, -(-n // ps)) for n in lens]
+    V = torch.zeros(sum(need) * ps, H, dv, device="cuda")
+    want = torch.zeros(len(lens), dv, dtype=torch.float64, device="cuda")
+    cols = torch.arange(dv, device="cuda")
+    at = 0
+    for b, n in enumerate(lens):
+        j = torch.arange(n, device="cuda")
+        mark = (j[:, None] % dv == cols) & (cols % 2 == 0)
+        edges = [0, n - 1, n - 2, n // 2, 1, 15, 16, 31, 32, 33, ps - 1, ps, 2 * ps, n - ps, 47, 48,
+                 n // 3, n // 5, n // 7, n // 148, n // 149 + 1, 1023, 1024, 4095, 4096]
+        edges = [x for x in edges if 0 <= x < n][:dv // 2]
+        mark[torch.tensor(edges, device="cuda"),
+             torch.arange(len(edges), device="cuda") * 2 + 1] = True
+        V[at:at + n] = mark[:, None].float()
+        want[b] = mark.sum(0).double() / n
+        at += need[b] * ps
+    ones = torch.ones(V.shape[:2], device="cuda")
+    K = torch.ones(V.shape[0], H, d, device="cuda")
+    q = torch.zeros(len(lens), Hq, d, device="cuda", dtype=qt)
+    out, lse = _decode(q, K, V, ones, ones, lens, ps, kv)
+    n = torch.tensor(lens, dtype=torch.float64, device="cuda")[:, None]
+    assert bool(((lse.double() - n.log()).abs() <= 2.0 ** -22 * (1 + n.log2())).all())
+    ref = want[:, None].expand(out.shape)
+    tol = half_step(qt) * ref + 2.0 ** -22 * ref + smallest(qt)
+    assert bool(((out.double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("kv", [F32, E4M3, I8])
+def test_long_sums_are_rounded_not_cut(kv):
+    """Means of 16384 positive values: a tile's sum (a few products, each cut at
+    2^-23) is added to the rest by rounded additions, so the errors of T tiles do
+    not pile up on one side: their mean stays under 2^-21, their size under
+    2^-21 + sqrt(T) 2^-24 (T = 1024)."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n, H, d, ps, B = 16384, 8, 64, 64, 148
+    V = torch.rand(n, H, d, generator=g, device="cuda") * 0.5 + 0.5
+    vs = torch.rand(n, H, generator=g, device="cuda") + 0.5
+    if kv == I8:
+        V = torch.round(V * 127)
+    elif kv == E4M3:
+        V = V.to(kv).float()
+    lens = [n - b for b in range(B)]
+    table = torch.arange(n // ps, dtype=torch.int32)[None].repeat(B, 1)
+    q = torch.zeros(B, H, d, device="cuda")
+    out, lse = _decode(q, torch.ones_like(V), V, torch.ones_like(vs), vs, lens, ps, kv, table)
+    x = V.double() * (vs.double()[..., None] if kv != F32 else 1)
+    sums = x.cumsum(0)
+    ref = torch.stack([sums[m - 1] / m for m in lens])
+    err = (out.double() - ref) / ref
+    assert float(err.mean().abs()) <= 2.0 ** -21
+    assert float(err.square().mean().sqrt()) <= 2.0 ** -21 + 32 * 2.0 ** -24
+    m = torch.tensor(lens, dtype=torch.float64, device="cuda")[:, None]
+    assert bool(((lse.double() - m.log()).abs() <= 2.0 ** -22 * (1 + m.log2())).all())
