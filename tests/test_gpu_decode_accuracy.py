@@ -32,6 +32,41 @@ def _decode(q, K, V, ks, vs, lens, ps, kv, table=None, **kw):
     return got
 
 
+@pytest.mark.parametrize("qt,kv", TYPES)
+@pytest.mark.parametrize("G,d", [(1, 64), (10, 128)])
+def test_weights_are_held_in_32_bits(qt, kv, G, d):
+    """Three keys of scores 0, -t and -t - e with values 0, 1 and -1: two weights
+    that all but cancel, so that their rounding shows under the output's own.
+    Each of the two (below 0.9) is off by 2^-22 of itself in the exponential, 2^-22
+    in its score's three roundings, 2^-23 in its terms, the sum by 2^-23; over a
+    sum of weights of 2.8 that is less than 2^-21."""
+    H, B = 8, 250
+    t = torch.linspace(0.1, 1.0, H * B, device="cuda").view(B, H)
+    t = t if kv in (E4M3, I8) else t.to(kv).float()
+    e = 2.0 ** -14
+    K = torch.zeros(B, 3, H, d, device="cuda")
+    V = torch.zeros(B, 3, H, d, device="cuda")
+    V[:, 1], V[:, 2] = 1, -1
+    ks = torch.ones(B, 3, H, device="cuda")
+    q = torch.zeros(B, G * H, d, device="cuda", dtype=qt)
+    q[..., 0] = 1
+    if kv in (E4M3, I8):
+        K[:, 1:, :, 0] = -1
+        ks[:, 1], ks[:, 2] = t, t + e
+        lo, hi = ks[:, 1].double(), ks[:, 2].double()
+    else:
+        q[..., 1] = 1
+        K[:, 1:, :, 0] = -t[:, None]
+        K[:, 2, :, 1] = -e
+        lo, hi = t.double(), t.double() + e
+    out, _ = _decode(q, K.flatten(0, 1), V.flatten(0, 1), ks.flatten(0, 1),
+                     torch.ones_like(ks).flatten(0, 1), [3] * B, 3, kv, scale=1.0)
+    ref = (torch.exp(-lo) - torch.exp(-hi)) / (1 + torch.exp(-lo) + torch.exp(-hi))
+    ref = ref.repeat_interleave(G, 1)[..., None].expand(out.shape)
+    tol = half_step(qt) * ref + 2.0 ** -21 + smallest(qt)
+    assert bool(((out.double() - ref).abs() <= tol).all())
+
+
 LONG = [
     # lengths, page size, query heads, KV heads, d, dv
     ([20000, 3, 1, 4097], 64, 4, 1, 128, 128), ([19999], 24, 8, 8, 64, 64),
