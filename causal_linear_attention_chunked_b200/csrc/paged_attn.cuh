@@ -357,9 +357,9 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi, I
 // scaled by a power of two per head into [1, 2), so that no bf16 query leaves
 // fp16's range.
 //
-// fp32 queries (8-bit caches only) are two fp16 terms as well, each head's
-// largest entry at 2^12, so that both terms of all but tiny entries are full
-// precision: 22 bits, two products per step.
+// fp32 queries (8-bit caches only) are three fp16 terms, which hold all 24 bits,
+// each head's largest entry at 2^12, so that what falls below fp16's smallest
+// numbers is under 2^-37 of it.
 //
 // kShift: fp16 weights are held times 2^12 (it cancels in the division), so
 // that weights down to 2^-26 of the largest keep fp16's full precision; 2^12 *
@@ -375,7 +375,7 @@ struct MmaEngine {
   static constexpr bool kQuant = Kv::kQuant;
   static constexpr bool kHalf = !__is_same(MT, __nv_bfloat16);
   static constexpr bool kWide = __is_same(QT, float);  // fp32 queries
-  static constexpr int kTerms = kWide ? 2 : 1;
+  static constexpr int kTerms = kWide ? 3 : 1;
   static constexpr int kWeightTerms = !kHalf || kWide ? 3 : 2;
   static_assert(!kWide || kQuant, "fp32 caches have an engine of their own");
   // 8 KB per tile: short rows share a tile's bookkeeping (e4m3 rows of 128 in
@@ -498,11 +498,13 @@ struct MmaEngine {
 
   // S^T of 16 tokens, times the heads' factors; `at`: see tile()
   __device__ __forceinline__ void scores(float (*s)[4], uint32_t at) {
-    float s2[kNB][4];  // even and odd steps: two chains of products
+    // even and odd steps: two chains of products; the queries' further terms,
+    // small beside the first, in a chain of their own
+    float s2[kNB][4], small[kNB][4];
 #pragma unroll
     for (int b = 0; b < kNB; ++b)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[b][e] = s2[b][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) s[b][e] = s2[b][e] = small[b][e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < D / 16; i += 2) {
       uint32_t a0[4], a1[4];
@@ -521,14 +523,18 @@ struct MmaEngine {
       for (int n = 0; n < kTerms; ++n)
 #pragma unroll
         for (int b = 0; b < kNB; ++b) {
-          mma<MT>(s[b], a0, qf[n][b][i][0], qf[n][b][i][1]);
-          mma<MT>(s2[b], a1, qf[n][b][i + 1][0], qf[n][b][i + 1][1]);
+          mma<MT>(n ? small[b] : s[b], a0, qf[n][b][i][0], qf[n][b][i][1]);
+          mma<MT>(n ? small[b] : s2[b], a1, qf[n][b][i + 1][0], qf[n][b][i + 1][1]);
         }
     }
 #pragma unroll
     for (int b = 0; b < kNB; ++b)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[b][e] = (s[b][e] + s2[b][e]) * sl2[b][e & 1];
+      for (int e = 0; e < 4; ++e) {
+        s[b][e] += s2[b][e];
+        if constexpr (kTerms > 1) s[b][e] += small[b][e];
+        s[b][e] *= sl2[b][e & 1];
+      }
   }
 
   // O^T += V^T P^T of the tile, w its weights' tiles.  The sum of a tile starts

@@ -136,3 +136,25 @@ def test_long_sums_are_rounded_not_cut(kv):
     assert float(err.square().mean().sqrt()) <= 2.0 ** -21 + 32 * 2.0 ** -24
     m = torch.tensor(lens, dtype=torch.float64, device="cuda")[:, None]
     assert bool(((lse.double() - m.log()).abs() <= 2.0 ** -22 * (1 + m.log2())).all())
+
+
+@pytest.mark.parametrize("kv,swap", [(E4M3, False), (I8, False)])
+def test_scores_of_fp32_factors_that_cancel(kv, swap):
+    """q = (a, -b) over a key (1, 1), or q = (1, -1) over a key (a, b): the score
+    is a - b, the last few bits of 24-bit numbers, so every bit of them takes
+    part.  The scale, its product and the log sum round: 2^-21 of the value."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    B, d = 500, 64
+    a = torch.randint(2 ** 23, 2 ** 24 - 200, (B,), generator=g, device="cuda")
+    m = torch.randint(1, 100, (B,), generator=g, device="cuda")
+    x, y = a.double() * 2.0 ** -23, (a + m).double() * 2.0 ** -23
+    q = torch.zeros(B, 1, d, device="cuda")
+    K = torch.zeros(B, 1, d, device="cuda")
+    if swap:
+        q[:, 0, 0], q[:, 0, 1], K[:, 0, 0], K[:, 0, 1] = 1, -1, x.float(), y.float()
+    else:
+        q[:, 0, 0], q[:, 0, 1], K[:, 0, 0], K[:, 0, 1] = x.float(), -y.float(), 1, 1
+    one = torch.ones(B, 1, device="cuda")
+    _, lse = _decode(q, K, torch.ones_like(K), one, one, [1] * B, 1, kv, scale=2.0 ** 20)
+    ref = -m.double()[:, None] / 8
+    assert bool(((lse.double() - ref).abs() <= 2.0 ** -21 * ref.abs()).all())
