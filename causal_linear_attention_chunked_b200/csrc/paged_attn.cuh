@@ -706,32 +706,45 @@ struct MmaEngine {
 };
 
 // ---------------------------------------------------- engine: fp32 caches
-// Tensor cores in tf32, every factor in two terms: x = hi + lo, hi the nearest
-// tf32 value (11 bits) and lo the rest, of which the instruction keeps 11 bits;
-// x y ~ hi hi + hi lo + lo hi is off by about 2^-21 of |x y|, either way.  The
-// instruction's additions cut where fp32's round, so chains of them are kept
-// short: a tile's values are summed from zero and added to the rest by plain
-// additions (one long chain was seven times further off at 65000 keys).  Plain
-// fp32 multiplications bound this kernel at 3 TB/s for 4 query heads per KV head;
-// so it reads 5.4 TB/s.  Values of 2^127 and more round to infinity.
+// Tensor cores in bf16, every factor in three terms, which hold all 24 bits of
+// one: x = hi + mid + lo, hi the first 8 bits (cut), mid the rest rounded to 8, lo
+// what is left.  Of the nine products of terms the six largest are taken; the others
+// are at most 2^-22 of |x y|, 2^-25 in the mean and either way, which is what fp32
+// arithmetic itself rounds off.  (Two terms of tf32, three products, took as many
+// instructions but were 2^-21 off: a single key did not come back as its value.)
+// Sums as in MmaEngine.  Plain fp32 multiplications bound this kernel at 3 TB/s for 4
+// query heads per KV head; so it reads 5.0 TB/s (32 sequences, 147k tokens of 8
+// heads of 128: 249 us), and waits on the splitting of keys and values, not on memory.
+// Subtracting after widening the packed terms: 256 us; the five small products
+// in one chain: 255.
 //
-// The same two products as MmaEngine, in steps of 8: S^T = K Q^T with A = K, O^T
-// = V^T P^T with A = V^T.  32-bit tiles have no ldmatrix, so rows and steps are
-// numbered to make a lane's share four neighbouring values, read at once and
-// without bank conflicts: of S^T, row g is token 4 (g & 1) + g / 2 of its eight,
-// and a lane's four d are the two halves of two steps; of V^T, a step's token c
-// is 2 c and c + 4 is 2 c + 1, and rows g and g + 8 of two tiles are a lane's
-// four columns.
-__device__ __forceinline__ void mma_tf32(float* c, const uint32_t* a, const uint32_t* b) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+// The same two products as MmaEngine: S^T = K Q^T with A = K, O^T = V^T P^T with A
+// = V^T.  32-bit tiles have no ldmatrix, so rows and columns are numbered to make a
+// lane's share four neighbouring values, read at once and without bank
+// conflicts: of S^T, row g is token 4 (g & 1) + g / 2 of its eight, and a lane's
+// four d of a step are 16 s + 4 c ..; of V^T, rows g and g + 8 of two products are
+// a lane's four columns.
+struct Bf16Terms {
+  uint32_t t[3];  // of two values, packed
+};
+// h - x, h a bf16 (mixed operands: no widening of the packed terms)
+__device__ __forceinline__ float less(uint32_t h, float x) {
+  float r;
+  asm("sub.f32.bf16 %0, %1, %2;" : "=f"(r) : "h"((uint16_t)h), "f"(x));
+  return r;
 }
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // (the conversion instruction is slower)
-  lo = __float_as_uint(x - __uint_as_float(hi));
+__device__ __forceinline__ Bf16Terms split_terms(float x, float y) {
+  Bf16Terms r;
+  r.t[0] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+  // minus the rest, of 16 bits; its first 8, rounded; and the 8 that are left
+  x = less(r.t[0], x);
+  y = less(r.t[0] >> 16, y);
+  const uint32_t c = pack2<__nv_bfloat16>(x, y);
+  r.t[1] = c ^ 0x80008000u;
+  x = less(c, x);
+  y = less(c >> 16, y);
+  r.t[2] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+  return r;
 }
 __device__ __forceinline__ void shared4(uint32_t addr, float* f) {
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
@@ -741,13 +754,13 @@ __device__ __forceinline__ void shared4(uint32_t addr, float* f) {
 }
 
 template <int D, int DV>
-struct Tf32Engine {
+struct Fp32Engine {
   using QT = float;
   static constexpr int kD = D, kHeads = 8, kTile = 16, kWarps = 4;
   static constexpr int kKRow = D * 4, kVRow = DV * 4;  // bytes
   static constexpr bool kQuant = false;
   static constexpr int kExtra = 0;
-  uint32_t qh[D / 16][4], ql[D / 16][4];  // of head g = lane / 4, d 16 s + 4 c ..
+  uint32_t qf[D / 16][2][3];  // of head g = lane / 4, d 16 s + 4 c ..
   float o[DV / 32][2][4];
   float m[2], l[2];  // heads 2 c, 2 c + 1
   float sl2;
@@ -772,39 +785,52 @@ struct Tf32Engine {
     for (int s = 0; s < D / 16; ++s) {
       const float4 x = g < nheads ? __ldg(reinterpret_cast<const float4*>(q + g * D + 16 * s) + c)
                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const float f[4] = {x.x, x.y, x.z, x.w};
+      const Bf16Terms a = split_terms(x.x, x.y), b = split_terms(x.z, x.w);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) split_tf32(f[e], qh[s][e], ql[s][e]);
+      for (int n = 0; n < 3; ++n) {
+        qf[s][0][n] = a.t[n];
+        qf[s][1][n] = b.t[n];
+      }
     }
+  }
+
+  // the five smaller products of terms, in two sums: of the middle terms with the
+  // first, and the rest
+  __device__ __forceinline__ static void mma_small(float* small, float* tiny,
+                                                   const uint32_t (*a)[4], const uint32_t* b0,
+                                                   const uint32_t* b1) {
+    mma<__nv_bfloat16>(tiny, a[2], b0[0], b1[0]);
+    mma<__nv_bfloat16>(small, a[1], b0[0], b1[0]);
+    mma<__nv_bfloat16>(tiny, a[0], b0[2], b1[2]);
+    mma<__nv_bfloat16>(small, a[0], b0[1], b1[1]);
+    mma<__nv_bfloat16>(tiny, a[1], b0[1], b1[1]);
   }
 
   __device__ __forceinline__ void tile(const TileAt& t) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int tok = ((g & 1) << 2) | (g >> 1);  // row g's token, of each eight
-    float s[4] = {}, s2[4] = {}, small[4] = {};
+    float s[4] = {}, s2[4] = {}, small[4] = {}, tiny[4] = {};
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       float x[4], y[4];  // tokens tok and tok + 8
       shared4(t.k + chunk_at<kKRow>(tok, 4 * i + c), x);
       shared4(t.k + chunk_at<kKRow>(tok + 8, 4 * i + c), y);
+      uint32_t a[3][4];
+      const Bf16Terms p[4] = {split_terms(x[0], x[1]), split_terms(y[0], y[1]),
+                              split_terms(x[2], x[3]), split_terms(y[2], y[3])};
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {  // two steps of 8
-        uint32_t ah[4], al[4];
-        split_tf32(x[2 * u], ah[0], al[0]);
-        split_tf32(y[2 * u], ah[1], al[1]);
-        split_tf32(x[2 * u + 1], ah[2], al[2]);
-        split_tf32(y[2 * u + 1], ah[3], al[3]);
-        mma_tf32(u ? s2 : s, ah, &qh[i][2 * u]);
-        mma_tf32(small, ah, &ql[i][2 * u]);
-        mma_tf32(small, al, &qh[i][2 * u]);
-      }
+      for (int n = 0; n < 3; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[n][e] = p[e].t[n];
+      mma_small(small, tiny, a, qf[i][0], qf[i][1]);
+      mma<__nv_bfloat16>(i & 1 ? s2 : s, a[0], qf[i][0][0], qf[i][1][0]);
     }
     const bool live0 = (t.mask >> tok) & 1u, live1 = (t.mask >> (tok + 8)) & 1u;
     bool moved = false;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      s[e] = live0 ? (s[e] + s2[e] + small[e]) * sl2 : -INFINITY;
-      s[2 + e] = live1 ? (s[2 + e] + s2[2 + e] + small[2 + e]) * sl2 : -INFINITY;
+      s[e] = live0 ? (s[e] + s2[e] + (small[e] + tiny[e])) * sl2 : -INFINITY;
+      s[2 + e] = live1 ? (s[2 + e] + s2[2 + e] + (small[2 + e] + tiny[2 + e])) * sl2 : -INFINITY;
       moved |= fmaxf(s[e], s[2 + e]) > m[e];
     }
     if (__any_sync(0xffffffffu, moved)) {
@@ -834,7 +860,8 @@ struct Tf32Engine {
     }
     // the weights of head g and tokens 2 c, 2 c + 1 of each eight, from the
     // lanes of those tokens' rows (token t is row 2 (t & 3) + t / 4)
-    uint32_t ph[2][2], pl[2][2];
+    Bf16Terms w[2];
+    float pv[2][2];
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
       const int from = 2 * c + z, src = 4 * (2 * (from & 3) + (from >> 2)) + (g >> 1);
@@ -842,33 +869,35 @@ struct Tf32Engine {
       for (int u = 0; u < 2; ++u) {
         const float a = __shfl_sync(0xffffffffu, p[2 * u], src);
         const float b = __shfl_sync(0xffffffffu, p[2 * u + 1], src);
-        split_tf32(g & 1 ? b : a, ph[u][z], pl[u][z]);
+        pv[u][z] = g & 1 ? b : a;
       }
     }
 #pragma unroll
+    for (int u = 0; u < 2; ++u) w[u] = split_terms(pv[u][0], pv[u][1]);
+#pragma unroll
     for (int j = 0; j < DV / 32; ++j) {
-      float sum[2][4] = {};
+      float x[4][4];  // tokens 2 c, 2 c + 1 of each eight, columns 32 j + 4 g ..
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {  // eight tokens each
-        float x[4], y[4];            // tokens 2 c and 2 c + 1, columns 32 j + 4 g ..
-        shared4(t.v + chunk_at<kVRow>(8 * u + 2 * c, 8 * j + g), x);
-        shared4(t.v + chunk_at<kVRow>(8 * u + 2 * c + 1, 8 * j + g), y);
+      for (int e = 0; e < 4; ++e)
+        shared4(t.v + chunk_at<kVRow>(8 * (e >> 1) + 2 * c + (e & 1), 8 * j + g), x[e]);
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          uint32_t ah[4], al[4];
-          split_tf32(x[2 * z], ah[0], al[0]);
-          split_tf32(x[2 * z + 1], ah[1], al[1]);
-          split_tf32(y[2 * z], ah[2], al[2]);
-          split_tf32(y[2 * z + 1], ah[3], al[3]);
-          mma_tf32(sum[z], ah, pl[u]);
-          mma_tf32(sum[z], al, ph[u]);
-          mma_tf32(sum[z], ah, ph[u]);
-        }
+      for (int z = 0; z < 2; ++z) {
+        uint32_t a[3][4];
+        const Bf16Terms p4[4] = {
+            split_terms(x[0][2 * z], x[1][2 * z]), split_terms(x[0][2 * z + 1], x[1][2 * z + 1]),
+            split_terms(x[2][2 * z], x[3][2 * z]), split_terms(x[2][2 * z + 1], x[3][2 * z + 1])};
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[n][e] = p4[e].t[n];
+        float sum[4] = {}, tiny[4] = {};
+        mma_small(sum, tiny, a, w[0].t, w[1].t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += tiny[e];
+        mma<__nv_bfloat16>(sum, a[0], w[0].t[0], w[1].t[0]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][z][e] += sum[e];
       }
-#pragma unroll
-      for (int z = 0; z < 2; ++z)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][z][e] += sum[z][e];
     }
   }
 

@@ -567,10 +567,11 @@ LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *b
  * sum in fp32, and the pieces of a sequence that several warps share are
  * joined in a fixed order, by a second launch where they lie in several
  * blocks.  Runs agree bit for bit.  Scores, sums and accumulators are fp32; for
- * the tensor cores the weights are split into terms that keep them to 2^-23:
- * three of bf16 for a bf16 cache, two of fp16 (three under LT_F32) otherwise;
- * for an fp32 cache two terms of tf32 (2^-21).  More than 16 query heads per
- * KV head (8 under LT_F32) read the cache once for every 16 (8).
+ * the tensor cores the weights are split into terms that keep them to 2^-23
+ * (three of bf16 for a bf16 cache, two of fp16 for an fp16 or 8-bit one), and
+ * so are fp32 queries, keys and values (three terms, all 24 bits).  More than
+ * 16 query heads per KV head (8 under LT_F32) read the cache once for every 16
+ * (8).
  * Returns as lt_kv_cache_write.
  */
 LT_API lt_status_t lt_paged_attn_decode(const void *q, const lt_kv_cache_t *cache,

@@ -32,6 +32,33 @@ def _decode(q, K, V, ks, vs, lens, ps, kv, table=None, **kw):
     return got
 
 
+def _codes(shape, kv, g):
+    """Random values of the cache's type and, as [..] without the width, scales."""
+    x = torch.randn(*shape, generator=g, device="cuda")
+    x = torch.clamp(torch.round(40 * x), -127, 127) if kv == I8 else x.to(kv).float()
+    return x, torch.rand(shape[:-1], generator=g, device="cuda") + 0.5
+
+
+@pytest.mark.parametrize("qt,kv", TYPES)
+@pytest.mark.parametrize("G,d,dv", [(1, 64, 64), (4, 128, 128), (12, 64, 128)])
+def test_one_key_is_its_value_row(qt, kv, G, d, dv):
+    """One key: its weight is 1 whatever its score, so a row comes back as it is
+    held, and one of 8 bits as code x scale, rounded to fp32 (each half of the
+    tensor cores' cut sum at most a step of 2^-23) and then to the output."""
+    g = torch.Generator(device="cuda").manual_seed(G)
+    B, H = 300, 2
+    K, ks = _codes((3 * B, H, d), kv, g)
+    V, vs = _codes((3 * B, H, dv), kv, g)
+    q = torch.randn(B, G * H, d, generator=g, device="cuda").to(qt)
+    if kv == F32:
+        V[:3, 0, :4] = torch.tensor([torch.finfo(F32).max, -1.5e38, 2.0 ** -126, 1e-30])
+    out, lse = _decode(q, K, V, ks, vs, [3] * B, 3, kv, window=1)
+    ref = V[2::3].double() * (vs[2::3].double()[..., None] if kv in (E4M3, I8) else 1)
+    ref = ref.repeat_interleave(G, 1)
+    tol = half_step(qt) * ref.abs() + 2.0 ** -22 * ref.abs() if kv in (E4M3, I8) else 0
+    assert bool(((out.double() - ref).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("qt,kv", TYPES)
 @pytest.mark.parametrize("G,d", [(1, 64), (10, 128)])
 def test_weights_are_held_in_32_bits(qt, kv, G, d):
@@ -138,7 +165,7 @@ def test_long_sums_are_rounded_not_cut(kv):
     assert bool(((lse.double() - m.log()).abs() <= 2.0 ** -22 * (1 + m.log2())).all())
 
 
-@pytest.mark.parametrize("kv,swap", [(E4M3, False), (I8, False)])
+@pytest.mark.parametrize("kv,swap", [(F32, False), (F32, True), (E4M3, False), (I8, False)])
 def test_scores_of_fp32_factors_that_cancel(kv, swap):
     """q = (a, -b) over a key (1, 1), or q = (1, -1) over a key (a, b): the score
     is a - b, the last few bits of 24-bit numbers, so every bit of them takes
