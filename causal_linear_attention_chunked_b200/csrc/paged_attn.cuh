@@ -269,10 +269,11 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 }
 
 // one more piece: values x, maximum and sum ml; what is joined so far (o, l,
-// relative to 2^mx) and the piece both go by the larger maximum
+// relative to 2^mx) and the piece both go by the larger maximum (exp2f: a factor
+// below fp32's normal numbers counts too, beside values as large)
 __device__ __forceinline__ void add_piece(float4& o, float& l, float& mx, float2 ml, float4 x) {
   const float top = fmaxf(mx, ml.x), base = top == -INFINITY ? 0.0f : top;
-  const float f = exp2_fast(mx - base), g = exp2_fast(ml.x - base);
+  const float f = exp2f(mx - base), g = exp2f(ml.x - base);
   mx = top;
   l = fmaf(g, ml.y, f * l);
   o.x = fmaf(g, x.x, f * o.x);

@@ -185,3 +185,20 @@ def test_scores_of_fp32_factors_that_cancel(kv, swap):
     _, lse = _decode(q, K, torch.ones_like(K), one, one, [1] * B, 1, kv, scale=2.0 ** 20)
     ref = -m.double()[:, None] / 8
     assert bool(((lse.double() - ref).abs() <= 2.0 ** -21 * ref.abs()).all())
+
+
+def test_pieces_of_tiny_weight_and_huge_values_join():
+    """Keys whose weight is 2^-127 of the largest, with values of 2^118: 2^-9 of the
+    result, whichever block or warp had them.  The score's roundings move that
+    share by 127 x 3 x 2^-24, and a piece that mixes both kinds (one of a
+    few tiles) holds its weights to 2^-7."""
+    n, d = 5000, 64
+    K = torch.zeros(n, 1, d, device="cuda")
+    V = torch.ones(n, 1, d, device="cuda")
+    K[n // 2:, :, 0] = -127
+    V[n // 2:] = 2.0 ** 118
+    q = torch.zeros(1, 2, d, device="cuda")
+    q[..., 0] = 1
+    one = torch.ones(n, 1, device="cuda")
+    out, _ = _decode(q, K, V, one, one, [n], 8, F32, scale=0.6931471805599453)
+    assert bool(((out.double() - 1 - 2.0 ** -9).abs() <= 2.0 ** -20).all())
