@@ -362,9 +362,10 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi, I
 // each head's largest entry at 2^12, so that what falls below fp16's smallest
 // numbers is under 2^-37 of it.
 //
-// kShift: fp16 weights are held times 2^12 (it cancels in the division), so
-// that weights down to 2^-26 of the largest keep fp16's full precision; 2^12 *
-// 65504 * 2^31 keys stay inside fp32.  bf16 has fp32's range and needs none.
+// kShift: fp16 weights are held times 2^12, so that weights down to 2^-26 of the
+// largest keep fp16's full precision; 2^12 * 65504 * 2^31 keys stay inside fp32.
+// bf16 has fp32's range and needs none.  finish() takes it out of sums and values
+// again, and A last, so that neither takes a result out of fp32's range.
 //
 // The maximum moves only when some score passes it: one vote per tile instead
 // of a reduction.
@@ -390,7 +391,7 @@ struct MmaEngine {
   static constexpr int kHalves = kTile / 16;
   static constexpr int kKRow = D * Kv::kBytes, kVRow = DV * Kv::kBytes;  // bytes
   static constexpr int kExtra = 0;  // shared bytes per warp beside the ring
-  static constexpr float kShift = kHalf ? 12.0f : 0.0f;
+  static constexpr float kShift = kHalf ? 12.0f : 0.0f, kUnshift = kHalf ? 1.0f / 4096 : 1.0f;
   uint32_t qf[kTerms][kNB][D / 16][2];
   float o[kNB][DV / 16][4];
   // per head 2c, 2c + 1 of each block (c the lane's index among four)
@@ -678,24 +679,25 @@ struct MmaEngine {
         for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         const int h = 8 * b + 2 * c + e;
         if (h >= heads) continue;
-        const float mm = m[b][e] - kShift;
-        const float f = kQuant ? __uint_as_float(vtop) : 1.0f;
+        sum *= kUnshift;
         if (out.partial) {
-          if (lane < 4) *reinterpret_cast<float2*>(out.ml + 2 * h) = make_float2(mm, sum);
-          put(out.part + (size_t)h * DV, b, e, f);
+          if (lane < 4) *reinterpret_cast<float2*>(out.ml + 2 * h) = make_float2(m[b][e], sum);
+          put(out.part + (size_t)h * DV, b, e, kUnshift);
         } else {
-          if (lane < 4 && out.lse) out.lse[h] = log_sum(mm, sum);
-          put(out.out + (size_t)h * DV, b, e, f * inverse_sum(sum));
+          if (lane < 4 && out.lse) out.lse[h] = log_sum(m[b][e], sum);
+          put(out.out + (size_t)h * DV, b, e, kUnshift * inverse_sum(sum));
         }
       }
   }
 
+  // head e's row: its values times f, and A
   template <typename P>
   __device__ __forceinline__ void put(P* row, int b, int e, float f) {
     const int r = (threadIdx.x & 31) >> 2;
+    const float top = kQuant ? __uint_as_float(vtop) : 1.0f;
 #pragma unroll
     for (int j = 0; j < DV / 16; ++j) {
-      const float x = o[b][j][e] * f, y = o[b][j][2 + e] * f;
+      const float x = o[b][j][e] * f * top, y = o[b][j][2 + e] * f * top;
       if constexpr (kQuant) {
         store_pair(row + 16 * j + 2 * r, x, y);
       } else {

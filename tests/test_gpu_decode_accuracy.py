@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from cache_plain import half_step, smallest
-from test_gpu_paged_decode import E4M3, F32, I8, TYPES
+from test_gpu_paged_decode import BF, E4M3, F32, I8, TYPES
 
 pytestmark = pytest.mark.gpu
 
@@ -202,3 +202,25 @@ def test_pieces_of_tiny_weight_and_huge_values_join():
     one = torch.ones(n, 1, device="cuda")
     out, _ = _decode(q, K, V, one, one, [n], 8, F32, scale=0.6931471805599453)
     assert bool(((out.double() - 1 - 2.0 ** -9).abs() <= 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("qt,kv", [(BF, E4M3), (BF, I8), (F32, E4M3), (F32, I8)])
+@pytest.mark.parametrize("exponent", [-126, -110, 100, 106])
+def test_value_scales_at_the_ends_of_fp32(qt, kv, exponent):
+    """Rows whose scales are the smallest, and large ones whose sum stays inside
+    fp32 (6000 x 127 x 2 x 2^106 < 2^127), as the weighted sum of the formula does,
+    however many warps and blocks share the sequence.  The sum's
+    tiles and pieces and the quotient round: 2^-20; values below fp32's normal
+    numbers to half their step, 2^-150."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    lens, H, d = [6000, 1, 40], 2, 64
+    V, vs = _codes((6048, H, d), kv, g)
+    V = V.abs()
+    vs = (vs + 0.5) * 2.0 ** exponent
+    q = torch.zeros(3, 2 * H, d, device="cuda", dtype=qt)
+    out, _ = _decode(q, torch.ones_like(V), V, torch.ones_like(vs), vs, lens, 8, kv)
+    x = V.double() * vs.double()[..., None]
+    ref = torch.stack([x[:6000].mean(0), x[6000], x[6008:].mean(0)]).repeat_interleave(2, 1)
+    tol = (half_step(qt) + 2.0 ** -20) * ref + 2.0 ** -150 + (smallest(qt) if qt == BF else 0)
+    assert bool(torch.isfinite(out).all())
+    assert bool(((out.double() - ref).abs() <= tol).all())
