@@ -102,13 +102,20 @@ struct Angles {
 
 // sine and cosine of a fraction of a turn, |t| <= 1/2.  16-bit outputs: the
 // hardware functions, within 2^-21 on [-pi, pi], far below half a step of the
-// type (2^-11 at least); fp32: the accurate ones.
+// type (2^-11 at least).  fp32: the accurate ones, of the fraction rounded to fp32,
+// turned on by what that left out (up to 9e-8 of angle, more than they are off).
 template <typename T>
-__device__ __forceinline__ void sincos_turn(float t, float* s, float* c) {
-  if constexpr (sizeof(T) == 2)
-    __sincosf(6.2831853071795865f * t, s, c);
-  else
-    sincospif(2.0f * t, s, c);
+__device__ __forceinline__ void sincos_turn(double t, float* s, float* c) {
+  const float f = (float)t;
+  if constexpr (sizeof(T) == 2) {
+    __sincosf(6.2831853071795865f * f, s, c);
+  } else {
+    float sf, cf;
+    sincospif(2.0f * f, &sf, &cf);
+    const float rest = 6.2831853071795865f * (float)(t - (double)f);
+    *s = fmaf(cf, rest, sf);
+    *c = fmaf(-sf, rest, cf);
+  }
 }
 
 // the token's angles: the rows of a warp's step compute a share each and
@@ -129,7 +136,7 @@ __device__ __forceinline__ void angles_of(const NormArgs& a, const Lane<D>& ln, 
                           : 4 * ln.j + i;
       double turns = (double)pos * (double)__ldg(a.inv_freq + pair) * kInvTwoPi;
       turns -= rint(turns);
-      sincos_turn<T>((float)turns, &ms[e], &mc[e]);
+      sincos_turn<T>(turns, &ms[e], &mc[e]);
     }
   } else {
 #pragma unroll
