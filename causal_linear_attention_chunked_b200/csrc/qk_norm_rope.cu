@@ -678,7 +678,9 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
                       {k_weight, d * ws},
                       {rot ? positions : nullptr, (size_t)n_pos * 4},
                       {rot ? inv_freq : nullptr, (size_t)rot * 2},
-                      {gains ? workspace : nullptr, workspace_bytes}};
+                      {gains ? workspace : nullptr, workspace_bytes}};  // (used for the gains alone)
+  for (int i = 0; i < 8; ++i)
+    if (spans_overlap(ins[8], ins[i])) return LT_ERR_INVALID_ARG;
   const Span sq = {dq, strided_bytes(tokens, dq_stride, H_q, d, es)};
   const Span sk = {dk, strided_bytes(tokens, dk_stride, H_kv, d, es)};
   const Span wq = {dq_weight, d * ws}, wk = {dk_weight, d * ws};
@@ -687,8 +689,8 @@ extern "C" lt_status_t lt_qk_norm_rope_bwd(
       !slices_disjoint(sq, dq_stride, nq * es, sk, dk_stride, nk * es, es))
     return LT_ERR_INVALID_ARG;
   const int dev = current_device();
-  for (const Span& s : ins)
-    if (s.p && s.p != workspace && !on_device(dev, s.p)) return LT_ERR_INVALID_ARG;
+  for (int i = 0; i < 8; ++i)
+    if (ins[i].p && !on_device(dev, ins[i].p)) return LT_ERR_INVALID_ARG;
   if (!on_device(dev, dq) || !on_device(dev, dk) ||
       (dq_weight && !on_device(dev, dq_weight)) || (dk_weight && !on_device(dev, dk_weight)))
     return LT_ERR_INVALID_ARG;

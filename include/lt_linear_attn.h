@@ -438,7 +438,8 @@ LT_API lt_status_t lt_qk_norm_rope(const void *q, const void *k, const void *q_w
  * workspace  NULL (the library allocates it stream-ordered and releases it
  *            before returning), or 16-byte aligned device memory of at least
  *            lt_qk_norm_rope_bwd_plan's bytes that no other call uses until
- *            this one's work is done.
+ *            this one's work is done; it must not overlap any input or
+ *            output.  Not used where no gain's gradient is asked for.
  * Evaluation: the gains' gradients are summed in fp32 per thread, block and
  * launch in a fixed order, so runs agree bit for bit.
  * Returns as lt_qk_norm_rope.
