@@ -214,17 +214,13 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positio
     return dq, dk, dqw, dkw
 
 
-class PagedKVCache:
-    """A paged key-value cache over the caller's pools.
+class _Pools:
+    """A cache's pools as the library takes them: checked, and their places noted."""
 
-    k [pages, page_size, H_kv, d], v [pages, page_size, H_kv, dv]: bfloat16,
-    float16, float32, float8_e4m3fn or int8; any strides that keep rows
-    contiguous and 16-byte aligned.  8-bit caches have k_scale, v_scale
-    [pages, H_kv, page_size] float32 (contiguous), one scale per row.  The
-    pools are not copied, and stay alive with this object.
-    """
+    __slots__ = ("at", "struct", "ref", "dev", "dtype", "num_pages", "page_size", "H_kv", "d", "dv",
+                 "workspace_bytes")
 
-    def __init__(self, k, v, k_scale=None, v_scale=None):
+    def __init__(self, k, v, k_scale, v_scale):
         if k.dim() != 4 or v.dim() != 4 or k.shape[:3] != v.shape[:3]:
             raise ValueError("k and v must be [pages, page_size, H_kv, width] pools of one shape "
                              "but for the width")
@@ -246,28 +242,78 @@ class PagedKVCache:
         for t in (v, k_scale, v_scale):
             if t is not None and t.device != k.device:
                 raise ValueError("all tensors must be on one device")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.dtype, self.device, self._dev = k.dtype, k.device, k.get_device()
+        self.at = _places(k, v, k_scale, v_scale)
+        self.dtype, self.dev = k.dtype, k.get_device()
         self.num_pages, self.page_size, self.H_kv, self.d, self.dv = pages, page_size, H, d, \
             v.shape[3]
         # (a dimension of one entry may have any stride: it is never taken)
         kst, vst = ([s if n > 1 else 0 for s, n in zip(x.stride()[:3], x.shape)] for x in (k, v))
-        self._c = KvCacheStruct(
-            k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if quant else None,
-            v_scale.data_ptr() if quant else None, *kst, *vst, pages, page_size, H, d, v.shape[3],
-            _KV_CODES[k.dtype])
-        self._ref = ctypes.byref(self._c)
-        self._workspace_bytes = {}
+        self.struct = KvCacheStruct(*self.at, *kst, *vst, pages, page_size, H, d, v.shape[3],
+                                    _KV_CODES[k.dtype])
+        self.ref = ctypes.byref(self.struct)
+        self.workspace_bytes = {}
 
-    def _workspace(self, Hq, code):
+    def workspace(self, Hq, code):
         """Workspace bytes of paged_attn_decode for Hq query heads of dtype `code`."""
-        n = self._workspace_bytes.get((Hq, code))
+        n = self.workspace_bytes.get((Hq, code))
         if n is None:
             need = ctypes.c_size_t()
             _check(lib.lt_paged_attn_decode_plan(Hq, self.H_kv, self.d, self.dv, code,
                                                  _KV_CODES[self.dtype], 0, need))
-            n = self._workspace_bytes[(Hq, code)] = need.value
+            n = self.workspace_bytes[(Hq, code)] = need.value
         return n
+
+
+def _places(k, v, k_scale, v_scale):
+    return k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale)
+
+
+def _pool(name):
+    def get(self):
+        return self._tensors[name]
+
+    def replace(self, tensor):
+        self._tensors[name] = tensor
+        self._pools = None
+    return property(get, replace)
+
+
+class PagedKVCache:
+    """A paged key-value cache over the caller's pools.
+
+    k [pages, page_size, H_kv, d], v [pages, page_size, H_kv, dv]: bfloat16,
+    float16, float32, float8_e4m3fn or int8; any strides that keep rows
+    contiguous and 16-byte aligned.  8-bit caches have k_scale, v_scale
+    [pages, H_kv, page_size] float32 (contiguous), one scale per row.  The
+    pools are not copied, and stay alive with this object.
+
+    k, v, k_scale and v_scale may be set to other pools (larger ones, say): the
+    next call takes the pools as they then are, and checks them together.  So it
+    does when the memory of one has moved (resize_, set_).  A pool whose shape
+    or strides are changed in place, over the same memory, must be set again.
+    """
+
+    k, v, k_scale, v_scale = _pool(0), _pool(1), _pool(2), _pool(3)
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        self._tensors = [k, v, k_scale, v_scale]
+        self._pools = _Pools(k, v, k_scale, v_scale)
+
+    def _now(self):
+        """The pools, noted anew where one was replaced or has moved."""
+        p, t = self._pools, self._tensors
+        if p is None or p.at != _places(*t):
+            p = self._pools = _Pools(*t)
+        return p
+
+    _ref = property(lambda self: self._now().ref)
+    dtype = property(lambda self: self.k.dtype)
+    device = property(lambda self: self.k.device)
+    num_pages = property(lambda self: self.k.shape[0])
+    page_size = property(lambda self: self.k.shape[1])
+    H_kv = property(lambda self: self.k.shape[2])
+    d = property(lambda self: self.k.shape[3])
+    dv = property(lambda self: self.v.shape[3])
 
     @classmethod
     def empty(cls, num_pages, page_size, H_kv, d, dv=None, dtype=torch.bfloat16, device="cuda"):
@@ -289,18 +335,19 @@ def kv_cache_write(cache, k, v, slots, stream=None):
     or -1 to skip the token; they must differ.  See lt_kv_cache_write."""
     n, H, d, k_step = _tokens(k, "k")
     nv, Hv, dv, v_step = _tokens(v, "v")
-    if nv != n or H != cache.H_kv or Hv != H or d != cache.d or dv != cache.dv:
+    pools = cache._now()
+    if nv != n or H != pools.H_kv or Hv != H or d != pools.d or dv != pools.dv:
         raise ValueError("k and v must be [tokens, H_kv, d] and [tokens, H_kv, dv] of the cache")
     if k.dtype != v.dtype:
         raise TypeError("k and v must have one dtype")
     if slots.dtype != torch.int32 or not slots.is_contiguous() or slots.numel() != n:
         raise TypeError("slots must be a contiguous int32 tensor, one per token")
-    ctx = _elsewhere(cache._dev, stream, (k, v, slots))
+    ctx = _elsewhere(pools.dev, stream, (k, v, slots))
     if ctx is not None:
         with ctx:
             return kv_cache_write(cache, k, v, slots)
-    _check(lib.lt_kv_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), slots.data_ptr(), n,
-                                 k_step, v_step, _raw_stream(cache._dev), _dtype_code(k.dtype)))
+    _check(lib.lt_kv_cache_write(pools.ref, k.data_ptr(), v.data_ptr(), slots.data_ptr(), n,
+                                 k_step, v_step, _raw_stream(pools.dev), _dtype_code(k.dtype)))
 
 
 def kv_cache_read(cache, block_table, cu_seqlens, N, dtype=None, k_out=None, v_out=None,
@@ -316,22 +363,23 @@ def kv_cache_read(cache, block_table, cu_seqlens, N, dtype=None, k_out=None, v_o
     B = cu_seqlens.numel() - 1
     if block_table.shape[0] != B:
         raise ValueError("block_table must have a row per sequence")
+    pools = cache._now()
     if dtype is None:
-        dtype = cache.dtype if cache.dtype in _CODES else torch.bfloat16
-    ctx = _elsewhere(cache._dev, stream, (block_table, cu_seqlens, k_out, v_out))
+        dtype = pools.dtype if pools.dtype in _CODES else torch.bfloat16
+    ctx = _elsewhere(pools.dev, stream, (block_table, cu_seqlens, k_out, v_out))
     if ctx is not None:
         with ctx:
             return kv_cache_read(cache, block_table, cu_seqlens, N, dtype, k_out, v_out)
-    k_shape, v_shape = (N, cache.H_kv, cache.d), (N, cache.H_kv, cache.dv)
+    k_shape, v_shape = (N, pools.H_kv, pools.d), (N, pools.H_kv, pools.dv)
     k_out = cache.k.new_empty(*k_shape, dtype=dtype) if k_out is None \
         else _given(k_out, k_shape, dtype, "k_out")
     v_out = cache.k.new_empty(*v_shape, dtype=dtype) if v_out is None \
         else _given(v_out, v_shape, dtype, "v_out")
     pages = block_table.shape[1]
-    _check(lib.lt_kv_cache_read(cache._ref, block_table.data_ptr(),
+    _check(lib.lt_kv_cache_read(pools.ref, block_table.data_ptr(),
                                 block_table.stride(0) if B > 1 else pages, pages,
                                 cu_seqlens.data_ptr(), B, N, k_out.data_ptr(), v_out.data_ptr(),
-                                _raw_stream(cache._dev), _dtype_code(dtype)))
+                                _raw_stream(pools.dev), _dtype_code(dtype)))
     return k_out, v_out
 
 
@@ -347,7 +395,8 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
     if q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous [B, H_q, d] tensor")
     B, Hq, d = q.shape
-    if d != cache.d:
+    pools = cache._now()
+    if d != pools.d:
         raise ValueError("q and the cache must have the same width")
     _int32(block_table, "block_table", 2)
     _int32(seq_lens, "seq_lens", 1)
@@ -356,20 +405,20 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
     if not -2 ** 31 <= window < 2 ** 31:
         raise ValueError("window must fit 32 bits")
     code = _dtype_code(q.dtype)
-    dev = cache._dev
+    dev = pools.dev
     ctx = _elsewhere(dev, stream, (q, block_table, seq_lens, out))
     if ctx is not None:
         with ctx:
             return paged_attn_decode(q, cache, block_table, seq_lens, scale, window, out,
                                      return_lse)
-    out = q.new_empty(B, Hq, cache.dv) if out is None \
-        else _given(out, (B, Hq, cache.dv), q.dtype, "out")
+    out = q.new_empty(B, Hq, pools.dv) if out is None \
+        else _given(out, (B, Hq, pools.dv), q.dtype, "out")
     lse = q.new_empty(B, Hq, dtype=torch.float32) if return_lse else None
-    ws_bytes = cache._workspace(Hq, code)
+    ws_bytes = pools.workspace(Hq, code)
     ws = q.new_empty(ws_bytes, dtype=torch.uint8)
     pages = block_table.shape[1]
     _check(lib.lt_paged_attn_decode(
-        q.data_ptr(), cache._ref, block_table.data_ptr(),
+        q.data_ptr(), pools.ref, block_table.data_ptr(),
         block_table.stride(0) if B > 1 else pages, pages, seq_lens.data_ptr(), B, Hq,
         1.0 / math.sqrt(d) if scale is None else scale, window, out.data_ptr(), _ptr(lse),
         ws.data_ptr(), ws_bytes, _raw_stream(dev), code))
