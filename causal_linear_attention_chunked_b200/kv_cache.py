@@ -10,9 +10,10 @@ One serving step of a softmax layer:
     kv_cache_write(cache, k, v, slots)
     out = paged_attn_decode(q, cache, block_table, seq_lens)
 
-Calls run on the tensors' device and, unless ``stream`` is given, on its
-current stream.  Tensors that a call allocates (outputs, workspace) belong to
-the stream that it runs on.
+Calls of no tokens or no sequences do nothing: their outputs are empty (the
+gains' gradients zeros).  Calls run on the tensors' device and, unless
+``stream`` is given, on its current stream.  Tensors that a call allocates
+(outputs, workspace) belong to the stream that it runs on.
 """
 import ctypes
 import math
@@ -149,6 +150,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
                                 q_out, k_out)
     q_out = _dense_like(q) if q_out is None else _given(q_out, q.shape, q.dtype, "q_out")
     k_out = _dense_like(k) if k_out is None else _given(k_out, k.shape, q.dtype, "k_out")
+    if n == 0:
+        return q_out, k_out
     _check(lib.lt_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions), n_pos,
         _ptr(inv_freq), rot, 1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), n, Hq,
@@ -202,6 +205,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positio
         dk_step = _tokens(dk, "dk")[3]
     dqw = torch.empty_like(q_weight) if q_weight is not None else None
     dkw = torch.empty_like(k_weight) if k_weight is not None else None
+    if n == 0:
+        return dq, dk, *(w if w is None else w.zero_() for w in (dqw, dkw))
     ws, ws_bytes = None, 0
     if dqw is not None or dkw is not None:
         ws_bytes = _bwd_workspace(dev, d)
@@ -346,6 +351,8 @@ def kv_cache_write(cache, k, v, slots, stream=None):
     if ctx is not None:
         with ctx:
             return kv_cache_write(cache, k, v, slots)
+    if n == 0:
+        return
     _check(lib.lt_kv_cache_write(pools.ref, k.data_ptr(), v.data_ptr(), slots.data_ptr(), n,
                                  k_step, v_step, _raw_stream(pools.dev), _dtype_code(k.dtype)))
 
@@ -375,6 +382,8 @@ def kv_cache_read(cache, block_table, cu_seqlens, N, dtype=None, k_out=None, v_o
         else _given(k_out, k_shape, dtype, "k_out")
     v_out = cache.k.new_empty(*v_shape, dtype=dtype) if v_out is None \
         else _given(v_out, v_shape, dtype, "v_out")
+    if B == 0 or N == 0:
+        return k_out, v_out
     pages = block_table.shape[1]
     _check(lib.lt_kv_cache_read(pools.ref, block_table.data_ptr(),
                                 block_table.stride(0) if B > 1 else pages, pages,
@@ -414,6 +423,8 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
     out = q.new_empty(B, Hq, pools.dv) if out is None \
         else _given(out, (B, Hq, pools.dv), q.dtype, "out")
     lse = q.new_empty(B, Hq, dtype=torch.float32) if return_lse else None
+    if B == 0:
+        return (out, lse) if return_lse else out
     ws_bytes = pools.workspace(Hq, code)
     ws = q.new_empty(ws_bytes, dtype=torch.uint8)
     pages = block_table.shape[1]
