@@ -82,6 +82,16 @@ def _tokens(t, name):
     return n, H, w, step if n > 1 else H * w
 
 
+def _wants_gradient(tensors, outs):
+    """Whether autograd is to see the call; then it takes no outputs of the caller's."""
+    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in tensors):
+        return False
+    if any(t is not None for t in outs):
+        raise ValueError("an output that the caller gives takes no gradient, and an input requires "
+                         "one: leave it out, or call under torch.no_grad()")
+    return True
+
+
 def _dense_like(t):
     return torch.empty_like(t, memory_format=torch.contiguous_format)
 
@@ -139,7 +149,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
     int32, one per token, or [N] shared by a [B, N] batch; inv_freq: float32
     [rot / 2] angles per position (rot values of each head are rotated, a
     multiple of 8); both None: the norm alone.  interleaved: pairs (2i, 2i + 1)
-    instead of (i, i + rot / 2).  See lt_qk_norm_rope."""
+    instead of (i, i + rot / 2).  Where q, k or a gain requires a gradient, the
+    result has one (by qk_norm_rope_bwd; once).  See lt_qk_norm_rope."""
     n, Hq, Hkv, d, q_step, k_step, code, w_code, n_pos, rot = _norm_args(q, k, q_weight, k_weight,
                                                                          positions, inv_freq)
     dev = q.get_device()
@@ -148,6 +159,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
         with ctx:
             return qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved,
                                 q_out, k_out)
+    if _wants_gradient((q, k, q_weight, k_weight, inv_freq), (q_out, k_out)):
+        return _QkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
     q_out = _dense_like(q) if q_out is None else _given(q_out, q.shape, q.dtype, "q_out")
     k_out = _dense_like(k) if k_out is None else _given(k_out, k.shape, q.dtype, "k_out")
     if n == 0:
@@ -157,6 +170,23 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
         _ptr(inv_freq), rot, 1 if interleaved else 0, q_out.data_ptr(), k_out.data_ptr(), n, Hq,
         Hkv, d, q_step, k_step, eps, _raw_stream(dev), code, w_code))
     return q_out, k_out
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.how = eps, interleaved
+        return qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        if ctx.needs_input_grad[5]:
+            raise RuntimeError("qk_norm_rope has no gradient for inv_freq")
+        got = qk_norm_rope_bwd(dq_out.contiguous(), dk_out.contiguous(), *ctx.saved_tensors,
+                               *ctx.how)
+        return *(g if need else None for g, need in zip(got, ctx.needs_input_grad)), *[None] * 4
 
 
 _bwd_bytes = {}
@@ -336,8 +366,9 @@ class PagedKVCache:
 def kv_cache_write(cache, k, v, slots, stream=None):
     """New keys and values into the cache, quantised to 8 bits where it holds 8
     bits.  k [.., H_kv, d], v [.., H_kv, dv] (slices of a fused projection are
-    taken as they are); slots: int32, one per token, page * page_size + offset,
-    or -1 to skip the token; they must differ.  See lt_kv_cache_write."""
+    taken as they are, values without their gradients); slots: int32, one per
+    token, page * page_size + offset, or -1 to skip the token; they must differ.
+    See lt_kv_cache_write."""
     n, H, d, k_step = _tokens(k, "k")
     nv, Hv, dv, v_step = _tokens(v, "v")
     pools = cache._now()
@@ -400,7 +431,8 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
     q [B, H_q, d]; block_table int32 [B, max_pages]; seq_lens int32 [B], the
     tokens of each sequence in the cache (0 gives zeros, and lse -inf); scale:
     of the scores (default 1 / sqrt(d)); window: the last `window` tokens only
-    (0: all).  See lt_paged_attn_decode."""
+    (0: all).  There is no backward pass: where q requires a gradient, asking
+    for it raises.  See lt_paged_attn_decode."""
     if q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous [B, H_q, d] tensor")
     B, Hq, d = q.shape
@@ -420,6 +452,8 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
         with ctx:
             return paged_attn_decode(q, cache, block_table, seq_lens, scale, window, out,
                                      return_lse)
+    if _wants_gradient((q,), (out,)):
+        return _PagedAttnDecode.apply(q, cache, block_table, seq_lens, scale, window, return_lse)
     out = q.new_empty(B, Hq, pools.dv) if out is None \
         else _given(out, (B, Hq, pools.dv), q.dtype, "out")
     lse = q.new_empty(B, Hq, dtype=torch.float32) if return_lse else None
@@ -434,3 +468,13 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
         1.0 / math.sqrt(d) if scale is None else scale, window, out.data_ptr(), _ptr(lse),
         ws.data_ptr(), ws_bytes, _raw_stream(dev), code))
     return (out, lse) if return_lse else out
+
+
+class _PagedAttnDecode(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, cache, block_table, seq_lens, scale, window, return_lse):
+        return paged_attn_decode(q, cache, block_table, seq_lens, scale, window, None, return_lse)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("paged_attn_decode has no backward pass")
