@@ -93,17 +93,9 @@ bool pools_within(const lt_kv_cache_t* c, size_t bytes) {
   return s[0].n <= bytes && s[1].n <= bytes;
 }
 
-// query heads per unit, warps per block and tokens per tile: the engines'
-// kHeads, kWarps and kTile
-int heads_per_unit(lt_dtype_t t, int G) {
-  const int most = t == LT_F32 ? 8 : 16;
+int unit_heads(lt_dtype_t t, int G) {
+  const int most = heads_at_once(t == LT_F32, G);
   return G < most ? G : most;
-}
-int block_warps(lt_dtype_t t, lt_kv_dtype_t kv, int d, int dv) {
-  return kv == LT_KV_F32 ? 4 : (d + dv) * (int)kv_size(kv) <= 128 && t != LT_F32 ? 16 : 8;
-}
-int tile_tokens(lt_kv_dtype_t kv, int d, int dv) {
-  return (d + dv) * (int)kv_size(kv) <= 256 ? 32 : 16;
 }
 
 // the workspace, one block of the first launch per SM: pieces of its warps
@@ -114,9 +106,9 @@ struct Sizes {
   size_t bytes;
 };
 Sizes sizes_of(lt_dtype_t t, lt_kv_dtype_t kv, int H_q, int H_kv, int d, int dv, int sms) {
-  const int G = H_q / H_kv, hb = heads_per_unit(t, G), nhb = (G + hb - 1) / hb;
+  const int G = H_q / H_kv, hb = unit_heads(t, G), nhb = (G + hb - 1) / hb;
   Sizes z;
-  z.warp = (size_t)sms * block_warps(t, kv, d, dv) * 2;
+  z.warp = (size_t)sms * block_warps(t == LT_F32, (int)kv_size(kv), d, dv) * 2;
   z.block = (size_t)sms * 2 * H_kv * nhb;
   z.floats = (size_t)hb * (dv + 2);
   z.bytes = (z.warp + z.block) * z.floats * sizeof(float) + (size_t)sms * sizeof(Shared);
@@ -194,7 +186,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   if (sms <= 0 || !err) return LT_ERR_CUDA;
   DecodeArgs a = {};
   a.G = H_q / cache->H_kv;
-  a.hb = heads_per_unit(dtype, a.G);
+  a.hb = unit_heads(dtype, a.G);
   a.nhb = (a.G + a.hb - 1) / a.hb;
   const Sizes z = sizes_of(dtype, cache->dtype, H_q, cache->H_kv, cache->d, cache->dv, sms);
   Workspace w;
@@ -224,12 +216,12 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.max_len = most;
   a.units = a.Hkv * a.nhb;
   a.k_shift = -1;
-  for (int s = 0, w = block_warps(dtype, cache->dtype, cache->d, cache->dv); (1 << s) <= w; ++s)
-    if (a.units << s == w) a.k_shift = s;
+  const int warps = block_warps(dtype == LT_F32, (int)ks, cache->d, cache->dv);
+  for (int s = 0; (1 << s) <= warps; ++s)
+    if (a.units << s == warps) a.k_shift = s;
   while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
   a.page_magic = (uint32_t)(((uint64_t)1 << (31 + a.page_shift)) / a.page_size + 1);
   a.window = window;
-  a.tile = tile_tokens(cache->dtype, cache->d, cache->dv);
   a.scale = scale;
   a.out = out;
   a.lse = lse;

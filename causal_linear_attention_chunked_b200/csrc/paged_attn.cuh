@@ -63,6 +63,22 @@ struct Int8 {
   int8_t b;
 };
 
+// What the engines and the workspace's sizes go by.  Query heads that a warp has at
+// once (a unit: up to so many of one KV head's G): one or two blocks of 8.
+constexpr int heads_at_once(bool f32, int G) { return f32 || G <= 8 ? 8 : 16; }
+// Tokens per tile: 8 KB per tile, so that short rows share a tile's bookkeeping
+// (e4m3 rows of 128 in tiles of 16, with 16 warps, issued a third more
+// instructions per token).  kv_bytes: of a value in the cache.
+constexpr int tile_tokens(int kv_bytes, int d, int dv) {
+  return (d + dv) * kv_bytes <= 256 ? 32 : 16;
+}
+// Warps per block.  8-bit rows of 64: tiles are 4 KB, and a warp's chain of steps per
+// tile is no shorter, so twice the warps (64 sequences, 175k tokens of 8 heads, e4m3:
+// 83 -> 68 us; fp32 queries, whose products need the registers, 5% slower so).
+constexpr int block_warps(bool f32, int kv_bytes, int d, int dv) {
+  return kv_bytes == 4 ? 4 : (d + dv) * kv_bytes <= 128 && !f32 ? 16 : 8;
+}
+
 // A piece of a pair: unnormalised sums of values [heads][dv], and the maximum
 // and sum of weights [heads][2].
 struct Pieces {
@@ -92,7 +108,6 @@ struct DecodeArgs {
   uint32_t page_magic;  // floor(2^(31 + page_shift) / page_size) + 1
   int page_shift;       // ceil(log2(page_size))
   int max_len;          // keys that a table row has pages for
-  int tile;             // tokens per tile (the engine's kTile)
   int units, k_shift;   // Hkv * nhb; log2 of the warps per unit (-1: they do not divide)
   int by_seq;           // shared[] goes by sequence (else by first block)
   float scale;
@@ -380,14 +395,9 @@ struct MmaEngine {
   static constexpr int kTerms = kWide ? 3 : 1;
   static constexpr int kWeightTerms = !kHalf || kWide ? 3 : 2;
   static_assert(!kWide || kQuant, "fp32 caches have an engine of their own");
-  // 8 KB per tile: short rows share a tile's bookkeeping (e4m3 rows of 128 in
-  // tiles of 16, with 16 warps, issued a third more instructions per token)
   static constexpr int kD = D, kHeads = 8 * kNB;
-  // 8-bit rows of 64: tiles are 4 KB, and a warp's chain of steps per tile is no
-  // shorter, so twice the warps (64 sequences, 175k tokens of 8 heads, e4m3: 83 -> 68
-  // us; fp32 queries, whose products need the registers, 5% slower so)
-  static constexpr int kWarps = (D + DV) * Kv::kBytes <= 128 && !kWide ? 16 : 8;
-  static constexpr int kTile = (D + DV) * Kv::kBytes <= 256 ? 32 : 16;
+  static constexpr int kWarps = block_warps(kWide, Kv::kBytes, D, DV);
+  static constexpr int kTile = tile_tokens(Kv::kBytes, D, DV);
   static constexpr int kHalves = kTile / 16;
   static constexpr int kKRow = D * Kv::kBytes, kVRow = DV * Kv::kBytes;  // bytes
   static constexpr int kExtra = 0;  // shared bytes per warp beside the ring
@@ -759,7 +769,9 @@ __device__ __forceinline__ void shared4(uint32_t addr, float* f) {
 template <int D, int DV>
 struct Fp32Engine {
   using QT = float;
-  static constexpr int kD = D, kHeads = 8, kTile = 16, kWarps = 4;
+  static constexpr int kD = D, kHeads = heads_at_once(true, 1);
+  static constexpr int kWarps = block_warps(true, 4, D, DV), kTile = tile_tokens(4, D, DV);
+  static_assert(kTile == 16, "a tile is one step of the products");
   static constexpr int kKRow = D * 4, kVRow = DV * 4;  // bytes
   static constexpr bool kQuant = false;
   static constexpr int kExtra = 0;
@@ -1283,7 +1295,6 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
 
 template <typename E>
 cudaError_t launch_engine(const DecodeArgs& a, int sms, cudaStream_t stream) {
-  if (a.tile != E::kTile) return cudaErrorInvalidValue;  // the workspace's sizes go by them
   auto kern = lt_paged_decode_kernel<E>;
   constexpr int smem = Ring<E>::kBytes;
   static std::atomic<uint64_t> done{0};
@@ -1301,10 +1312,10 @@ cudaError_t launch_mma_nb(const DecodeArgs& a, int d, int sms, cudaStream_t s) {
                     : launch_engine<MmaEngine<QT, KT, 128, 128, NB>>(a, sms, s);
 }
 
-// 16-bit queries: one engine for up to 8 query heads per KV head, one for more
 template <typename QT, typename KT>
 cudaError_t launch_mma(const DecodeArgs& a, int d, int sms, cudaStream_t s) {
-  return a.G <= 8 ? launch_mma_nb<QT, KT, 1>(a, d, sms, s) : launch_mma_nb<QT, KT, 2>(a, d, sms, s);
+  return heads_at_once(false, a.G) == 8 ? launch_mma_nb<QT, KT, 1>(a, d, sms, s)
+                                        : launch_mma_nb<QT, KT, 2>(a, d, sms, s);
 }
 
 // the first launch, one translation unit per query type
