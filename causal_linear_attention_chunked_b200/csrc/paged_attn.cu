@@ -97,6 +97,10 @@ int unit_heads(lt_dtype_t t, int G) {
   const int most = heads_at_once(t == LT_F32, G);
   return G < most ? G : most;
 }
+int warps_of(lt_dtype_t t, lt_kv_dtype_t kv, int d, int dv, int G) {
+  const bool f32 = t == LT_F32;
+  return block_warps(f32, (int)kv_size(kv), d, dv, heads_at_once(f32, G));
+}
 
 // the workspace, one block of the first launch per SM: pieces of its warps
 // (two each), of its units (two each), and an entry for the second launch
@@ -108,7 +112,7 @@ struct Sizes {
 Sizes sizes_of(lt_dtype_t t, lt_kv_dtype_t kv, int H_q, int H_kv, int d, int dv, int sms) {
   const int G = H_q / H_kv, hb = unit_heads(t, G), nhb = (G + hb - 1) / hb;
   Sizes z;
-  z.warp = (size_t)sms * block_warps(t == LT_F32, (int)kv_size(kv), d, dv) * 2;
+  z.warp = (size_t)sms * warps_of(t, kv, d, dv, G) * 2;
   z.block = (size_t)sms * 2 * H_kv * nhb;
   z.floats = (size_t)hb * (dv + 2);
   z.bytes = (z.warp + z.block) * z.floats * sizeof(float) + (size_t)sms * sizeof(Shared);
@@ -216,7 +220,7 @@ extern "C" lt_status_t lt_paged_attn_decode(const void* q, const lt_kv_cache_t* 
   a.max_len = most;
   a.units = a.Hkv * a.nhb;
   a.k_shift = -1;
-  const int warps = block_warps(dtype == LT_F32, (int)ks, cache->d, cache->dv);
+  const int warps = warps_of(dtype, cache->dtype, cache->d, cache->dv, a.G);
   for (int s = 0; (1 << s) <= warps; ++s)
     if (a.units << s == warps) a.k_shift = s;
   while ((1 << a.page_shift) < a.page_size) ++a.page_shift;

@@ -72,11 +72,14 @@ constexpr int heads_at_once(bool f32, int G) { return f32 || G <= 8 ? 8 : 16; }
 constexpr int tile_tokens(int kv_bytes, int d, int dv) {
   return (d + dv) * kv_bytes <= 256 ? 32 : 16;
 }
-// Warps per block.  8-bit rows of 64: tiles are 4 KB, and a warp's chain of steps per
-// tile is no shorter, so twice the warps (64 sequences, 175k tokens of 8 heads, e4m3:
-// 83 -> 68 us; fp32 queries, whose products need the registers, 5% slower so).
-constexpr int block_warps(bool f32, int kv_bytes, int d, int dv) {
-  return kv_bytes == 4 ? 4 : (d + dv) * kv_bytes <= 128 && !f32 ? 16 : 8;
+// Warps per block, for units of up to `heads` query heads.  8-bit rows of 64: tiles
+// are 4 KB, and a warp's chain of steps per tile is no shorter, so twice the warps
+// where their registers do (64 sequences, 266k tokens of 8 heads, e4m3: 75.0 us
+// with 8, 62.5 with 16).  Not for 9 heads or more, which spill in the 128 registers
+// of 16 warps (the same sequences, 16 heads over 1: 23.6 us with 8, 26.8 with 16; 80
+// over 8: 500 and 530; 256 over 4, of 16 units, 202 and 190), nor fp32 queries.
+constexpr int block_warps(bool f32, int kv_bytes, int d, int dv, int heads) {
+  return kv_bytes == 4 ? 4 : (d + dv) * kv_bytes <= 128 && !f32 && heads == 8 ? 16 : 8;
 }
 
 // A piece of a pair: unnormalised sums of values [heads][dv], and the maximum
@@ -396,7 +399,7 @@ struct MmaEngine {
   static constexpr int kWeightTerms = !kHalf || kWide ? 3 : 2;
   static_assert(!kWide || kQuant, "fp32 caches have an engine of their own");
   static constexpr int kD = D, kHeads = 8 * kNB;
-  static constexpr int kWarps = block_warps(kWide, Kv::kBytes, D, DV);
+  static constexpr int kWarps = block_warps(kWide, Kv::kBytes, D, DV, kHeads);
   static constexpr int kTile = tile_tokens(Kv::kBytes, D, DV);
   static constexpr int kHalves = kTile / 16;
   static constexpr int kKRow = D * Kv::kBytes, kVRow = DV * Kv::kBytes;  // bytes
@@ -770,7 +773,7 @@ template <int D, int DV>
 struct Fp32Engine {
   using QT = float;
   static constexpr int kD = D, kHeads = heads_at_once(true, 1);
-  static constexpr int kWarps = block_warps(true, 4, D, DV), kTile = tile_tokens(4, D, DV);
+  static constexpr int kWarps = block_warps(true, 4, D, DV, 8), kTile = tile_tokens(4, D, DV);
   static_assert(kTile == 16, "a tile is one step of the products");
   static constexpr int kKRow = D * 4, kVRow = DV * 4;  // bytes
   static constexpr bool kQuant = false;
