@@ -99,8 +99,6 @@ struct RowAt {
 };
 
 // ------------------------------------------------- chunks of eight elements
-struct E4M3 {};
-struct Int8 {};
 template <typename KV>
 struct KvMax;
 template <>

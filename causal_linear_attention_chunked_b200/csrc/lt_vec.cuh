@@ -17,6 +17,10 @@ __device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) {
 }
 __device__ __forceinline__ void from_float(__half* p, float x) { *p = __float2half_rn(x); }
 
+// the types that an 8-bit cache holds (each user of them decodes into its own)
+struct E4M3 {};
+struct Int8 {};
+
 // raw storage of four elements of T (8 or 16 bytes)
 template <typename T>
 struct Quad {

@@ -56,13 +56,6 @@ namespace paged {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-struct E4M3 {
-  uint8_t b;
-};
-struct Int8 {
-  int8_t b;
-};
-
 // What the engines and the workspace's sizes go by.  Query heads that a warp has at
 // once (a unit: up to so many of one KV head's G): one or two blocks of 8.
 constexpr int heads_at_once(bool f32, int G) { return f32 || G <= 8 ? 8 : 16; }
@@ -403,7 +396,6 @@ struct MmaEngine {
   static constexpr int kTile = tile_tokens(Kv::kBytes, D, DV);
   static constexpr int kHalves = kTile / 16;
   static constexpr int kKRow = D * Kv::kBytes, kVRow = DV * Kv::kBytes;  // bytes
-  static constexpr int kExtra = 0;  // shared bytes per warp beside the ring
   static constexpr float kShift = kHalf ? 12.0f : 0.0f, kUnshift = kHalf ? 1.0f / 4096 : 1.0f;
   uint32_t qf[kTerms][kNB][D / 16][2];
   float o[kNB][DV / 16][4];
@@ -411,8 +403,6 @@ struct MmaEngine {
   float m[kNB][2], l[kNB][2], sl2[kNB][2];
   uint32_t vtop;  // A's bits
   int heads;
-
-  __device__ __forceinline__ void init(uint8_t*) {}
 
   __device__ __forceinline__ void begin(const QT* q, int nheads, float scale) {
     const int lane = threadIdx.x & 31, c = lane & 3;
@@ -777,14 +767,11 @@ struct Fp32Engine {
   static_assert(kTile == 16, "a tile is one step of the products");
   static constexpr int kKRow = D * 4, kVRow = DV * 4;  // bytes
   static constexpr bool kQuant = false;
-  static constexpr int kExtra = 0;
   uint32_t qf[D / 16][2][3];  // of head g = lane / 4, d 16 s + 4 c ..
   float o[DV / 32][2][4];
   float m[2], l[2];  // heads 2 c, 2 c + 1
   float sl2;
   int heads;
-
-  __device__ __forceinline__ void init(uint8_t*) {}
 
   __device__ __forceinline__ void begin(const float* q, int nheads, float scale) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -956,7 +943,7 @@ struct Ring {
   // warps, the bytes in flight that cover the memory latency of an SM's share
   static constexpr int kWant = 8 * 24576 / E::kWarps / kStage;
   static constexpr int kStages = kWant < 3 ? 3 : kWant > 8 ? 8 : kWant;
-  static constexpr int kWarpBytes = kStage * kStages + (E::kExtra + 127) / 128 * 128;
+  static constexpr int kWarpBytes = kStage * kStages;
   static constexpr int kBytes = kWarpBytes * E::kWarps;
   static_assert(kBytes <= 220 * 1024, "shared memory");
 };
@@ -1090,7 +1077,6 @@ __global__ void __launch_bounds__(E::kWarps * 32, 1)
     uint8_t* ring = smem + warp * R::kWarpBytes;
     const uint32_t ring_u = smem_u32(ring);
     E eng;
-    eng.init(ring + R::kStage * S);
 
     const int row = lane & (TILE - 1);
     constexpr uint32_t kFull = TILE == 32 ? 0xffffffffu : (1u << (TILE & 31)) - 1u;
