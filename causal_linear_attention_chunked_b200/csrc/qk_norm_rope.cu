@@ -518,12 +518,15 @@ cudaError_t launch(const NormArgs& a, int blocks, int d, int il, lt_dtype_t dtyp
                            : launch_d<float, kBack>(a, blocks, d, il, s);
 }
 
-// Warps that share a token's heads: one where the tokens alone fill the
-// device's warps, more where they are few (a decode step), up to one per batch.
+// Warps that share a token's heads: one where the tokens alone fill the warps that
+// a launch has on the device, more where they are few (a decode step), up to one
+// per batch.  Counting half of those warps: 600 tokens of 32 + 8 bf16 heads of 128
+// forward 7.1 us against 5.0, backward 12.9 against 9.5; 256 tokens 4.4 against 3.7 and
+// 8.4 against 7.1.  Rounding up instead of down: 2300 tokens 11.7 us against 9.6.
 int token_parts(int64_t tokens, int H_q, int H_kv, int d, lt_dtype_t dtype, int sms) {
   const int step = kBatchBytes / (d * (int)dtype_size(dtype));  // Ring::kStep
   const int batches = (H_q + step - 1) / step + (H_kv + step - 1) / step;
-  const int64_t want = (int64_t)sms * kW / tokens;
+  const int64_t want = (int64_t)sms * kBlocks * kW / tokens;
   return want < 1 ? 1 : want > batches ? batches : (int)want;
 }
 

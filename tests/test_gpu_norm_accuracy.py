@@ -1,4 +1,4 @@
-"""Norm and rotation: the angle's accuracy in fp32."""
+"""Norm and rotation: the angle's accuracy in fp32, and few tokens."""
 import pytest
 import torch
 
@@ -34,3 +34,25 @@ def test_fp32_angles_are_held_in_fp32(interleaved):
             err = (got - ref).abs()
             assert float(err.max()) <= 2.0 ** -23 + 2.0 ** -25
             assert float(err.square().mean().sqrt()) <= 1.6 * 1.5e-8
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [200, 600, 790, 1184, 1185])
+def test_tokens_whose_heads_several_warps_share(T, dtype):
+    """Token counts around the steps of how many warps share a token, both
+    directions (32 + 8 heads of 128: several batches each)."""
+    import cache_plain as plain
+    import causal_linear_attention_chunked_b200 as L
+    g = torch.Generator().manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g).to(dtype)
+    q, k, gq, gk = r(T, 32, 128), r(T, 8, 128), r(T, 32, 128), r(T, 8, 128)
+    wq, wk = r(128), r(128)
+    pos = torch.randint(0, 100000, (T,), generator=g).int()
+    freq = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).float()
+    dev = [t.cuda() for t in (gq, gk, q, k, wq, wk, pos, freq)]
+    out, got = L.qk_norm_rope(*dev[2:]), L.qk_norm_rope_bwd(*dev)
+    for i, (x, w, up) in enumerate(((q, wq, gq), (k, wk, gk))):
+        plain.check(out[i], *plain.norm_rope(x, w, pos, freq, 1e-6, False), dtype, "out %d" % i)
+        (dx, dxb), (dw, dwb) = plain.norm_rope_bwd(up, x, w, pos, freq, 1e-6, False)
+        plain.check(got[i], dx, dxb, dtype, "dx %d" % i)
+        plain.check(got[2 + i], dw, dwb, dtype, "dw %d" % i)
