@@ -719,10 +719,10 @@ struct MmaEngine {
 // arithmetic itself rounds off.  (Two terms of tf32, three products, took as many
 // instructions but were 2^-21 off: a single key did not come back as its value.)
 // Sums as in MmaEngine.  Plain fp32 multiplications bound this kernel at 3 TB/s for 4
-// query heads per KV head; so it reads 5.0 TB/s (32 sequences, 147k tokens of 8
-// heads of 128: 249 us), and waits on the splitting of keys and values, not on memory.
-// Subtracting after widening the packed terms: 256 us; the five small products
-// in one chain: 255.
+// query heads per KV head; so it reads 5.6 TB/s (32 sequences, 147k tokens of 8
+// heads of 128: 225 us), held by the splitting of keys and values beside memory.
+// Subtracting after widening the packed terms, and the five small products in
+// one chain, were 3% slower each.
 //
 // The same two products as MmaEngine: S^T = K Q^T with A = K, O^T = V^T P^T with A
 // = V^T.  32-bit tiles have no ldmatrix, so rows and columns are numbered to make a
@@ -772,10 +772,12 @@ struct Fp32Engine {
   float m[2], l[2];  // heads 2 c, 2 c + 1
   float sl2;
   int heads;
+  const float* query;
 
   __device__ __forceinline__ void begin(const float* q, int nheads, float scale) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     heads = nheads;
+    query = q;
     sl2 = scale * kLog2e;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -811,6 +813,21 @@ struct Fp32Engine {
     mma<__nv_bfloat16>(tiny, a[1], b0[1], b1[1]);
   }
 
+  // q . K of one head and row of the tile at k, by plain multiplications: for the scores
+  // whose terms hold a NaN, which an infinity leaves among its own, where the
+  // products may be infinities of one sign (a key of weight 0, say).
+  __device__ __noinline__ static float plain_score(const float* q, uint32_t k, int row) {
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < D / 4; ++i) {
+      float x[4];
+      shared4(k + chunk_at<kKRow>(row, i), x);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) sum = fmaf(__ldg(q + 4 * i + n), x[n], sum);
+    }
+    return sum;
+  }
+
   __device__ __forceinline__ void tile(const TileAt& t) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int tok = ((g & 1) << 2) | (g >> 1);  // row g's token, of each eight
@@ -831,11 +848,23 @@ struct Fp32Engine {
       mma<__nv_bfloat16>(i & 1 ? s2 : s, a[0], qf[i][0][0], qf[i][1][0]);
     }
     const bool live0 = (t.mask >> tok) & 1u, live1 = (t.mask >> (tok + 8)) & 1u;
-    bool moved = false;
+    bool moved = false, nan = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[e] += s2[e] + (small[e] + tiny[e]);
+      nan |= isnan(s[e]);
+    }
+    if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (isnan(s[e]) && 2 * c + (e & 1) < heads)
+          s[e] = plain_score(query + (2 * c + (e & 1)) * D, t.k, tok + 4 * (e & 2));
+      __syncwarp();
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      s[e] = live0 ? (s[e] + s2[e] + (small[e] + tiny[e])) * sl2 : -INFINITY;
-      s[2 + e] = live1 ? (s[2 + e] + s2[2 + e] + (small[2 + e] + tiny[2 + e])) * sl2 : -INFINITY;
+      s[e] = live0 ? s[e] * sl2 : -INFINITY;
+      s[2 + e] = live1 ? s[2 + e] * sl2 : -INFINITY;
       moved |= fmaxf(s[e], s[2 + e]) > m[e];
     }
     if (__any_sync(0xffffffffu, moved)) {

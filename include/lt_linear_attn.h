@@ -542,9 +542,11 @@ LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *b
  *     out_bh = sum_j p_j V_jg / sum_j p_j,   p_j = exp(scale * q_bh . K_jg)
  *     lse_bh = log sum_j p_j
  * A sequence of no tokens gives out = 0 and lse = -infinity.  The 8-bit
- * caches are read as 8 bits; nothing is written back.  An infinity or a NaN
- * among the queries, keys or values that take part makes the outputs that it
- * reaches NaN or infinite; what a page holds past a sequence's end is not used.
+ * caches are read as 8 bits; nothing is written back.  A key whose score is
+ * -infinity has the weight 0 (where all have, as for no tokens); any other
+ * infinity and every NaN among the queries, keys or values that take part
+ * makes the outputs that it reaches NaN or infinite; what a page holds past a
+ * sequence's end is not used.
  *
  * q          [B][H_q][d] of element type dtype, dense, 16-byte aligned.
  * cache, block_table, table_stride, max_pages   as for lt_kv_cache_read; the

@@ -224,3 +224,33 @@ def test_value_scales_at_the_ends_of_fp32(qt, kv, exponent):
     tol = (half_step(qt) + 2.0 ** -20) * ref + 2.0 ** -150 + (smallest(qt) if qt == BF else 0)
     assert bool(torch.isfinite(out).all())
     assert bool(((out.double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("kv", [BF, torch.float16, F32])
+@pytest.mark.parametrize("G,d", [(1, 64), (4, 128), (12, 64)])
+def test_keys_of_score_minus_infinity_have_no_weight(kv, G, d):
+    """Keys that hold -infinity where the queries are positive: as if they were not
+    there.  Their removal only moves other keys to other tiles, so the results
+    agree within the roundings of sums (16 terms of 2^-24) and the output's."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    lens, H = [700, 30, 17], 2
+    n = sum(lens)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(kv)
+    q = r(3, G * H, d)
+    q[..., 3] = q[..., 3].abs() + 0.5
+    K, V = r(n, H, d), r(n, H, d).abs()
+    dead = torch.rand(n, generator=g, device="cuda") < 0.3
+    dead[700:730] = True                                     # a sequence of such keys alone
+    hit = K.clone()
+    hit[dead, :, 3] = -float("inf")
+    one = torch.ones(n, H, device="cuda")
+    out, lse = _decode(q, hit, V, one, one, lens, 1, kv)
+    left = [int((~dead[a:b]).sum()) for a, b in ((0, 700), (700, 730), (730, n))]
+    # (a page of its own for the sequence that has no key left)
+    pad = lambda x: torch.cat([x[:700][~dead[:700]], x[:1], x[730:][~dead[730:]]])
+    ref, ref_lse = _decode(q, pad(K), pad(V), pad(one), pad(one), left, 1, kv)
+    assert bool((out[1] == 0).all()) and bool((lse[1] == -float("inf")).all())
+    keep = [0, 2]
+    tol = 2 * half_step(kv) * ref[keep].double().abs() + 2.0 ** -20 + smallest(kv)
+    assert bool(((out[keep].double() - ref[keep].double()).abs() <= tol).all())
+    assert bool(((lse[keep] - ref_lse[keep]).abs() <= 2.0 ** -20 * (1 + ref_lse[keep].abs())).all())
