@@ -365,13 +365,11 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi, I
 // transposed word of V holds two columns of two tokens: the even columns are
 // rows 0 .. 7 of the product, the odd ones rows 8 .. 15.  Key scales multiply
 // the scores; value scales go into the weights, relative to a power of two A
-// >= every scale seen, so that the fp16 weights stay at most 2^kShift.  Q is
-// scaled by a power of two per head into [1, 2), so that no bf16 query leaves
-// fp16's range.
-//
-// fp32 queries (8-bit caches only) are three fp16 terms, which hold all 24 bits,
-// each head's largest entry at 2^12, so that what falls below fp16's smallest
-// numbers is under 2^-37 of it.
+// >= every scale seen, so that the fp16 weights stay at most 2^kShift (and what
+// falls below fp16's smallest numbers is under 2^-37 of the largest value row).  Q
+// is scaled by a power of two per head, its largest entry to 2^12: no bf16 query
+// leaves fp16's range, and what falls below it is under 2^-37 of that entry.
+// fp32 queries (8-bit caches only) are three fp16 terms, which hold all 24 bits.
 //
 // kShift: fp16 weights are held times 2^12, so that weights down to 2^-26 of the
 // largest keep fp16's full precision; 2^12 * 65504 * 2^31 keys stay inside fp32.
@@ -441,7 +439,7 @@ struct MmaEngine {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // times 2^(127 - ex) 2^kUp: the largest entry in [1, 2) 2^kUp
-        constexpr uint32_t kUp = kWide ? 12 : 0;
+        constexpr uint32_t kUp = 12;
         const uint32_t ex = min(max(__float_as_uint(top) >> 23, 13u), 253u);
         const float down = __uint_as_float((254u + kUp - ex) << 23);
         const float up = __uint_as_float((ex - kUp) << 23);

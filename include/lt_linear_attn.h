@@ -572,7 +572,9 @@ LT_API lt_status_t lt_kv_cache_read(const lt_kv_cache_t *cache, const int32_t *b
  * blocks.  Runs agree bit for bit.  Scores, sums and accumulators are fp32; for
  * the tensor cores the weights are split into terms that keep them to 2^-23
  * (three of bf16 for a bf16 cache, two of fp16 for an fp16 or 8-bit one), and
- * so are fp32 queries, keys and values (three terms, all 24 bits).  More than
+ * so are fp32 queries, keys and values (three terms, all 24 bits).  Over an
+ * 8-bit cache, weights times value scales below 2^-37 of the largest scale,
+ * and query entries below 2^-37 of their head's largest, are lost.  More than
  * 16 query heads per KV head (8 under LT_F32) read the cache once for every 16
  * (8).
  * Returns as lt_kv_cache_write.

@@ -254,3 +254,20 @@ def test_keys_of_score_minus_infinity_have_no_weight(kv, G, d):
     tol = 2 * half_step(kv) * ref[keep].double().abs() + 2.0 ** -20 + smallest(kv)
     assert bool(((out[keep].double() - ref[keep].double()).abs() <= tol).all())
     assert bool(((lse[keep] - ref_lse[keep]).abs() <= 2.0 ** -20 * (1 + ref_lse[keep].abs())).all())
+
+
+@pytest.mark.parametrize("qt", [BF, torch.float16])
+@pytest.mark.parametrize("kv", [E4M3, I8])
+def test_small_query_entries_beside_a_large_one(qt, kv):
+    """q = (1, t) over a key (0, c): the score is t c, every bit of t in it, however
+    small beside the head's largest entry (down to the type's own 2^-24)."""
+    B, d = 300, 64
+    t = (torch.logspace(-22, -4, B, base=2.0, device="cuda")).to(qt)
+    q = torch.zeros(B, 1, d, device="cuda", dtype=qt)
+    q[:, 0, 0], q[:, 0, 1] = 1, t
+    K = torch.zeros(B, 1, d, device="cuda")
+    K[:, 0, 1] = 64
+    one = torch.ones(B, 1, device="cuda")
+    _, lse = _decode(q, K, torch.ones_like(K), one, one, [1] * B, 1, kv, scale=2.0 ** 10)
+    ref = t.double()[:, None] * 2.0 ** 16
+    assert bool(((lse.double() - ref).abs() <= 2.0 ** -21 * ref).all())
