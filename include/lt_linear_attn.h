@@ -394,7 +394,8 @@ LT_API lt_status_t lt_linear_attn_decode_step(const void *q, const void *k, cons
  *            of a token are contiguous, tokens are q_stride (k_stride)
  *            elements apart (at least H*d; a multiple of 16 bytes), so a
  *            slice of a fused projection's output can be passed as it is.
- * q_weight, k_weight  [d] gains of element type w_dtype, or NULL (gain 1).
+ * q_weight, k_weight  [d] gains of element type w_dtype, 16-byte aligned, or
+ *            NULL (gain 1).
  * positions  [n_pos] int32 device; tokens must be a multiple of n_pos (a
  *            dense batch [B][N] shares one array of N, or passes B*N).
  * inv_freq   [rot/2] fp32 device, angle per position.  Angles are formed and
@@ -431,8 +432,9 @@ LT_API lt_status_t lt_qk_norm_rope(const void *q, const void *k, const void *q_w
  * dq, dk     the layouts of q and k with token strides dq_stride, dk_stride
  *            (so that they can be slices of a fused gradient); nothing
  *            between the heads of two tokens is written.
- * dq_weight, dk_weight  [d] of w_dtype, each NULL (not wanted) or written
- *            whole; a gain's gradient may be asked for with a NULL gain.
+ * dq_weight, dk_weight  [d] of w_dtype, 4-byte aligned, each NULL (not wanted)
+ *            or written whole; a gain's gradient may be asked for with a NULL
+ *            gain.
  * Outputs must not overlap any input or each other (dq and dk may share one
  * fused gradient tensor, in disjoint slices).
  * workspace  NULL (the library allocates it stream-ordered and releases it
