@@ -82,14 +82,14 @@ def _tokens(t, name):
     return n, H, w, step if n > 1 else H * w
 
 
-def _wants_gradient(tensors, outs):
-    """Whether autograd is to see the call; then it takes no outputs of the caller's."""
-    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in tensors):
-        return False
+_grad_enabled = torch.is_grad_enabled
+
+
+def _no_outputs(*outs):
+    """Autograd takes no outputs of the caller's."""
     if any(t is not None for t in outs):
         raise ValueError("an output that the caller gives takes no gradient, and an input requires "
                          "one: leave it out, or call under torch.no_grad()")
-    return True
 
 
 def _dense_like(t):
@@ -159,7 +159,11 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
         with ctx:
             return qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved,
                                 q_out, k_out)
-    if _wants_gradient((q, k, q_weight, k_weight, inv_freq), (q_out, k_out)):
+    if _grad_enabled() and (q.requires_grad or k.requires_grad or
+                            (q_weight is not None and q_weight.requires_grad) or
+                            (k_weight is not None and k_weight.requires_grad) or
+                            (inv_freq is not None and inv_freq.requires_grad)):
+        _no_outputs(q_out, k_out)
         return _QkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
     q_out = _dense_like(q) if q_out is None else _given(q_out, q.shape, q.dtype, "q_out")
     k_out = _dense_like(k) if k_out is None else _given(k_out, k.shape, q.dtype, "k_out")
@@ -252,8 +256,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, positio
 class _Pools:
     """A cache's pools as the library takes them: checked, and their places noted."""
 
-    __slots__ = ("at", "struct", "ref", "dev", "dtype", "num_pages", "page_size", "H_kv", "d", "dv",
-                 "workspace_bytes")
+    __slots__ = ("k_at", "v_at", "k_scale_at", "v_scale_at", "at", "quant", "struct", "ref", "dev",
+                 "dtype", "num_pages", "page_size", "H_kv", "d", "dv", "workspace_bytes")
 
     def __init__(self, k, v, k_scale, v_scale):
         if k.dim() != 4 or v.dim() != 4 or k.shape[:3] != v.shape[:3]:
@@ -277,7 +281,11 @@ class _Pools:
         for t in (v, k_scale, v_scale):
             if t is not None and t.device != k.device:
                 raise ValueError("all tensors must be on one device")
-        self.at = _places(k, v, k_scale, v_scale)
+        self.quant = quant
+        self.k_at, self.v_at = k.data_ptr, v.data_ptr
+        self.k_scale_at = k_scale.data_ptr if quant else None
+        self.v_scale_at = v_scale.data_ptr if quant else None
+        self.at = k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale)
         self.dtype, self.dev = k.dtype, k.get_device()
         self.num_pages, self.page_size, self.H_kv, self.d, self.dv = pages, page_size, H, d, \
             v.shape[3]
@@ -288,6 +296,12 @@ class _Pools:
         self.ref = ctypes.byref(self.struct)
         self.workspace_bytes = {}
 
+    def stay(self):
+        """Whether the pools' memory is where it was."""
+        at = self.at
+        return self.k_at() == at[0] and self.v_at() == at[1] and \
+            (not self.quant or (self.k_scale_at() == at[2] and self.v_scale_at() == at[3]))
+
     def workspace(self, Hq, code):
         """Workspace bytes of paged_attn_decode for Hq query heads of dtype `code`."""
         n = self.workspace_bytes.get((Hq, code))
@@ -297,10 +311,6 @@ class _Pools:
                                                  _KV_CODES[self.dtype], 0, need))
             n = self.workspace_bytes[(Hq, code)] = need.value
         return n
-
-
-def _places(k, v, k_scale, v_scale):
-    return k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale)
 
 
 def _pool(name):
@@ -336,9 +346,9 @@ class PagedKVCache:
 
     def _now(self):
         """The pools, noted anew where one was replaced or has moved."""
-        p, t = self._pools, self._tensors
-        if p is None or p.at != _places(*t):
-            p = self._pools = _Pools(*t)
+        p = self._pools
+        if p is None or not p.stay():
+            p = self._pools = _Pools(*self._tensors)
         return p
 
     _ref = property(lambda self: self._now().ref)
@@ -409,9 +419,9 @@ def kv_cache_read(cache, block_table, cu_seqlens, N, dtype=None, k_out=None, v_o
         with ctx:
             return kv_cache_read(cache, block_table, cu_seqlens, N, dtype, k_out, v_out)
     k_shape, v_shape = (N, pools.H_kv, pools.d), (N, pools.H_kv, pools.dv)
-    k_out = cache.k.new_empty(*k_shape, dtype=dtype) if k_out is None \
+    k_out = cu_seqlens.new_empty(*k_shape, dtype=dtype) if k_out is None \
         else _given(k_out, k_shape, dtype, "k_out")
-    v_out = cache.k.new_empty(*v_shape, dtype=dtype) if v_out is None \
+    v_out = cu_seqlens.new_empty(*v_shape, dtype=dtype) if v_out is None \
         else _given(v_out, v_shape, dtype, "v_out")
     if B == 0 or N == 0:
         return k_out, v_out
@@ -452,7 +462,8 @@ def paged_attn_decode(q, cache, block_table, seq_lens, scale=None, window=0, out
         with ctx:
             return paged_attn_decode(q, cache, block_table, seq_lens, scale, window, out,
                                      return_lse)
-    if _wants_gradient((q,), (out,)):
+    if q.requires_grad and _grad_enabled():
+        _no_outputs(out)
         return _PagedAttnDecode.apply(q, cache, block_table, seq_lens, scale, window, return_lse)
     out = q.new_empty(B, Hq, pools.dv) if out is None \
         else _given(out, (B, Hq, pools.dv), q.dtype, "out")
