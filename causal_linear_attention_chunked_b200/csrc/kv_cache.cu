@@ -22,7 +22,7 @@
 //
 // Measured on one B200 (plain copy 6.55 TB/s): 32768 bf16 tokens of 8 heads of
 // 128, keys and values, into e4m3 pages 38 us, 5.4 TB/s (16384 fp32 tokens 28 us,
-// 6.1 TB/s); 64 ragged sequences (266k tokens of 8 heads of 64) back from e4m3 to
+// 6.1 TB/s); 64 ragged sequences (270k tokens of 8 heads of 64) back from e4m3 to
 // bf16 134 us, 6.3 TB/s.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -548,7 +548,7 @@ cudaError_t launch_quant(const CacheArgs& a, bool e4m3, bool write, dim3 grid, c
 // Tokens per tile, at most kMaxTok: enough rows for every group of a block's
 // threads (at most 64: a row has four lanes or more), few enough that a batch
 // spreads over the device, and kTileBytes of the dense side at most (token: its
-// bytes there).  32 KB: 49k bf16 tokens of 8 heads of 128 read back in 64.7 us, 266k
+// bytes there).  32 KB: 49k bf16 tokens of 8 heads of 128 read back in 64.7 us, 270k
 // of 64 from e4m3 in 143; 16 KB 67.4 and 162, 64 KB 66.0 and 146.
 constexpr int kTileBytes = 32768;
 int tile_tokens(int64_t tokens, int heads, int lanes, int64_t token, int sms) {

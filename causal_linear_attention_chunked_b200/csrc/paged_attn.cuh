@@ -27,13 +27,14 @@
 // from the lengths alone, so results do not depend on timing.
 //
 // Measured on one B200 (plain copy 6.55 TB/s, reads alone up to 7.1), 32 query
-// over 8 KV heads of 128: 64 ragged sequences (266k tokens) bf16 170 us, 6.5 TB/s;
-// e4m3 99 us, 5.7 TB/s, where the widening of the codes keeps the issue slots
-// busy; one sequence of 65536 tokens, bf16, 50 us, of which 12 are the two
-// launches' starts and ends.  Runs of (sequence, KV head) pairs instead of whole
-// columns read the e4m3 rows of one token at different times: 128 us.  Bulk
-// copies of single rows are slower than 16-byte copies below 256 bytes a row
-// (128-byte rows 4.5 against 7.0 TB/s).
+// over 8 KV heads of 128: 64 ragged sequences (270k tokens) bf16 171 us, 6.5 TB/s;
+// e4m3 101 us, 5.6 TB/s, replayed from a graph, and up to 112 in seconds of
+// back-to-back calls, where the widening of the codes and the weights' two terms
+// keep the issue slots busy at a lower clock; one sequence of 65536 tokens, bf16, 51
+// us, of which 10 are the two launches' starts and ends.  Runs of (sequence, KV head)
+// pairs instead of whole columns read the e4m3 rows of one token at different times:
+// 30% slower.  Bulk copies of single rows are slower than 16-byte copies below 256
+// bytes a row (128-byte rows 4.5 against 7.0 TB/s).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -67,7 +68,7 @@ constexpr int tile_tokens(int kv_bytes, int d, int dv) {
 }
 // Warps per block, for units of up to `heads` query heads.  8-bit rows of 64: tiles
 // are 4 KB, and a warp's chain of steps per tile is no shorter, so twice the warps
-// where their registers do (64 sequences, 266k tokens of 8 heads, e4m3: 75.0 us
+// where their registers do (64 sequences, 270k tokens of 8 heads, e4m3: 75.0 us
 // with 8, 62.5 with 16).  Not for 9 heads or more, which spill in the 128 registers
 // of 16 warps (the same sequences, 16 heads over 1: 23.6 us with 8, 26.8 with 16; 80
 // over 8: 500 and 530; 256 over 4, of 16 units, 202 and 190), nor fp32 queries.
@@ -343,8 +344,8 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi, I
 // rows would be nearly empty, and the work is bound by memory.  The tokens are
 // the 16 rows of the instruction and the query heads its 8 columns, so that
 // few of its lanes idle: per 16 tokens of a 16-bit cache of width 128 a warp
-// issues 24 mma and 16 ldmatrix for 8 KB read.  kNB blocks of 8 heads share a
-// tile's registers.
+// issues 24 mma (bf16: 32) and 16 ldmatrix for 8 KB read.  kNB blocks of 8 heads
+// share a tile's registers.
 //
 // Scores S^T = K Q^T: A = K (ldmatrix of the token rows), B = Q (in registers).
 // Values O^T = V^T P^T: A = V by transposing ldmatrix, B = the weights, whose
@@ -356,7 +357,7 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi, I
 // most), which is enough beside a 16-bit output, and fp32 outputs take three.
 // One term fewer (one for bf16 queries over 8-bit caches) turned up to one output
 // in twenty to the neighbouring bf16 value and saved 1 to 7%: 64 ragged sequences,
-// 266k tokens of 8 heads of 128, bf16 171 us against 170, e4m3 101 against 99,
+// 270k tokens of 8 heads of 128, bf16 171 us against 170, e4m3 101 against 99,
 // int8 112 against 104.
 //
 // 8-bit caches are widened to fp16 in registers.  A lane's four bytes of a key
@@ -717,7 +718,7 @@ struct MmaEngine {
 // arithmetic itself rounds off.  (Two terms of tf32, three products, took as many
 // instructions but were 2^-21 off: a single key did not come back as its value.)
 // Sums as in MmaEngine.  Plain fp32 multiplications bound this kernel at 3 TB/s for 4
-// query heads per KV head; so it reads 5.6 TB/s (32 sequences, 147k tokens of 8
+// query heads per KV head; so it reads 5.6 TB/s (32 sequences, 153k tokens of 8
 // heads of 128: 225 us), held by the splitting of keys and values beside memory.
 // Subtracting after widening the packed terms, and the five small products in
 // one chain, were 3% slower each.

@@ -20,10 +20,11 @@
 // pair are in one lane, and no value crosses lanes for the rotation.  Products
 // run two at a time (f32x2).
 //
-// Measured on one B200 (plain copy 6.55 TB/s), 32 + 8 bf16 heads of 128: 32768
-// tokens forward 107 us, 6.3 TB/s; 16384 tokens backward 88 us, 5.7 TB/s (replayed
-// from a graph; 118 and 98 in seconds of back-to-back calls, whose power lowers the
-// clock: the issue slots are 64% busy).
+// Measured on one B200 (plain copy 6.55 TB/s), 32 + 8 heads of 128, replayed from a
+// graph: 32768 bf16 tokens forward 108 us, 6.2 TB/s; 16384 backward 88 us, 5.7 TB/s (118
+// and 98 in seconds of back-to-back calls, whose power lowers the clock: the
+// issue slots are 60% busy).  fp32: 16384 tokens forward 123 us, 5.5 TB/s; 8192 backward
+// 95 us, 5.3 TB/s.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
