@@ -144,3 +144,36 @@ def test_what_has_no_gradient_says_so():
             y.float().sum().backward(retain_graph=True)
     with pytest.raises(ValueError):
         L.paged_attn_decode(one, c, table, lens, out=torch.empty_like(out))
+
+
+def test_a_captured_training_step():
+    """Forward and backward with accumulation into the leaves' gradients, captured
+    after warm-up on a side stream, and replayed on new inputs."""
+    import causal_linear_attention_chunked_b200 as L
+    qkv, wq, wk, pos, freq, gq, gk = _case()
+    ref = _by_hand(qkv, wq, wk, pos, freq, gq, gk)
+    x = torch.zeros_like(qkv).requires_grad_()
+    leaves = (x, wq, wk)
+
+    def step():
+        torch.autograd.backward(L.qk_norm_rope(*_cut(x), wq, wk, pos, freq), (gq, gk))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            for t in leaves:
+                t.grad = None
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    for t in leaves:
+        t.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    with torch.no_grad():
+        x.copy_(qkv)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t.grad, r) for t, r in zip(leaves, ref))
